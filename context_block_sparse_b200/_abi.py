@@ -33,6 +33,15 @@ STATIC_SCRATCH_BYTES = 16 << 20
 
 DTYPE_F32 = 0
 DTYPE_BF16 = 1
+DTYPE_F16 = 2
+
+ROPE_INTERLEAVED = 1
+ROPE_ADJOINT = 2
+ROPE_POS64 = 4
+ROPE_SCALE_NONE = 0
+ROPE_SCALE_LINEAR = 1
+ROPE_SCALE_BASE = 2
+ROPE_SCALE_PARTS = 3
 
 WS_FWD = 0
 WS_BWD = 1
@@ -95,6 +104,52 @@ class Stats(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+def _fields(spec):
+    """(name, type) pairs from "type name name[n] ..." lines; types i (int32), u (uint32), l (int64),
+    f (float), d (double), p (pointer)."""
+    kinds = {"i": ctypes.c_int32, "u": ctypes.c_uint32, "l": ctypes.c_int64, "f": ctypes.c_float,
+             "d": ctypes.c_double, "p": ctypes.c_void_p}
+    out = []
+    for line in spec.strip().splitlines():
+        kind, *names = line.split()
+        for n in names:
+            name, _, count = n.rstrip("]").partition("[")
+            out.append((name, kinds[kind] * int(count) if count else kinds[kind]))
+    return out
+
+
+class RopeArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        l num_tokens
+        i q_heads k_heads head_dim rotary_dim dtype
+        u flags
+        d scale
+        p positions freqs q q_out k k_out
+        l q_stride[2] q_out_stride[2] k_stride[2] k_out_stride[2]""")
+
+
+class TreeArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        i num_seqs num_nodes max_nodes num_q_heads num_kv_heads head_dim dtype o_dtype page_size num_pages max_pages
+        f scale
+        p q kb vb k_cache v_cache mask node_ptr context_lens page_table o lse status
+        l q_stride[2] kb_stride[2] vb_stride[2] k_stride[3] v_stride[3] mask_stride table_stride""")
+
+
+class VerifyArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        i num_seqs num_nodes max_nodes vocab dtype token_int64 max_path reserved
+        p target draft tokens parents node_ptr u_accept u_sample path count next status
+        l target_stride draft_stride path_stride""")
+
+
+class CommitArgs(ctypes.Structure):
+    _fields_ = _fields("""
+        i num_layers num_seqs num_nodes max_rows num_kv_heads head_dim elem_bytes page_size num_pages max_pages
+        p kb vb k_cache v_cache path count node_ptr context_lens page_table status
+        l kb_stride[3] vb_stride[3] k_stride[4] v_stride[4] path_stride table_stride""")
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
@@ -132,6 +187,13 @@ SIGNATURES = {
     "splitkv_plan_set_wait_limit": (_I, [_P, ctypes.c_int64]),
     "splitkv_selftest_exp2": (_I, [_P, _P, ctypes.c_int64, _P]),
     "splitkv_selftest_wait_timeout": (_I, [ctypes.POINTER(ctypes.c_int32), _P]),
+    "splitkv_rope_freqs": (_I, [ctypes.c_int32, ctypes.c_double, _I, ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                ctypes.c_double, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double)]),
+    "splitkv_rope": (_I, [ctypes.POINTER(RopeArgs), _P]),
+    "splitkv_tree_workspace_size": (_I, [ctypes.POINTER(TreeArgs), ctypes.POINTER(_SZ)]),
+    "splitkv_tree_attn": (_I, [ctypes.POINTER(TreeArgs), _P, _SZ, _P]),
+    "splitkv_tree_verify": (_I, [ctypes.POINTER(VerifyArgs), _P]),
+    "splitkv_tree_commit": (_I, [ctypes.POINTER(CommitArgs), _P]),
     "splitkv_read_cta_times": (_I, [_P, _I, ctypes.POINTER(ctypes.c_int64), ctypes.c_int64, _P]),
 }
 

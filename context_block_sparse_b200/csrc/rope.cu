@@ -1,0 +1,295 @@
+// Rotary positions: every pair (a, b) of a head's first rotary_dim elements is turned by
+// the angle p w_i (p the token's position, w_i the pair's frequency) and multiplied by m:
+//
+//   (a, b) -> m (a cos - b sin, b cos + a sin);
+//
+// the adjoint (the backward pass: the transpose of that matrix) turns by -p w_i with the
+// same m.  Elements from rotary_dim on pass through.  Pairs are (i, i + rotary_dim / 2), or
+// (2i, 2i + 1) in the interleaved layout.
+//
+// HBM-bound: every element is read and written once, 2 * N * (Hq + Hk) * d elements.  A
+// thread owns P pairs of one token -- two 16-byte vectors of a head -- computes their
+// cosines and sines once and walks over heads with them (queries first, then keys: one
+// launch for both), so the angles cost nothing next to the traffic.  The angle is formed in
+// float64 in units of turns and reduced to [-1/2, 1/2] before the float32 sine and cosine:
+// at position 2^20 the float32 product would be off by 0.06 rad, this one by 1e-9.
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cmath>
+
+#include "common.cuh"
+#include "splitkv.h"
+#include "splitkv_internal.h"
+
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kUnroll = 4;   // heads whose loads are in flight together
+
+struct Side {
+  const char* in;
+  char* out;
+  int64_t in_tok, in_head, out_tok, out_head;   // strides in bytes
+  int heads;
+};
+
+struct RopeParams {
+  Side q, k;
+  const void* positions;
+  const double* freqs;
+  int64_t n_tokens;
+  int half;          // rotary_dim / 2
+  int units;         // threads per token: units that turn, then units that copy
+  int turn_units;
+  int copy_vecs;     // 16-byte vectors (or elements) of a head that pass through
+  int heads_per_thread;
+  float m;
+  int pos64, adjoint;
+};
+
+template <typename T>
+__device__ __forceinline__ float to_f(T x) {
+  return static_cast<float>(x);
+}
+template <typename T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f<float>(float x) {
+  return x;
+}
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+template <>
+__device__ __forceinline__ __half from_f<__half>(float x) {
+  return __float2half_rn(x);
+}
+
+// P values of type T, moved as one aligned access (16 bytes, or one element when P = 1).
+template <typename T, int P>
+struct alignas(sizeof(T) * P) Vec {
+  T v[P];
+};
+
+// P pairs per thread: 16 / sizeof(T) where rows allow 16-byte accesses, else 1.
+template <typename T, int P, bool kInterleaved>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+  using V = Vec<T, P>;
+  const int64_t idx = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  if (idx >= p.n_tokens * p.units) return;
+  const int64_t tok = idx / p.units;
+  const int unit = int(idx - tok * p.units);
+  const bool turns = unit < p.turn_units;
+
+  float c[P], s[P];
+  int off0, off1;          // element offsets of the thread's two vectors inside a head
+  bool second = true;
+  if (turns) {
+    const int i0 = unit * P;
+    const double pos = p.pos64 ? double(static_cast<const int64_t*>(p.positions)[tok])
+                               : double(static_cast<const int32_t*>(p.positions)[tok]);
+#pragma unroll
+    for (int j = 0; j < P; ++j) {
+      constexpr double kInv2Pi = 0.15915494309189533577;
+      const double t = pos * (p.freqs[i0 + j] * kInv2Pi);   // turns
+      float sn, cs;
+      sincospif(2.0f * float(t - rint(t)), &sn, &cs);
+      c[j] = cs * p.m;
+      s[j] = (p.adjoint ? -sn : sn) * p.m;
+    }
+    off0 = kInterleaved ? 2 * i0 : i0;
+    off1 = kInterleaved ? 2 * i0 + P : p.half + i0;
+  } else {
+    const int v0 = 2 * (unit - p.turn_units);
+    off0 = 2 * p.half + v0 * P;
+    off1 = off0 + P;
+    second = v0 + 1 < p.copy_vecs;
+  }
+
+  const int total = p.q.heads + p.k.heads;
+  const int h_end = min(total, (int(blockIdx.y) + 1) * p.heads_per_thread);
+  for (int h0 = int(blockIdx.y) * p.heads_per_thread; h0 < h_end; h0 += kUnroll) {
+    V a[kUnroll], b[kUnroll];
+    char* dst[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int h = h0 + u;
+      if (h < h_end) {
+        const bool is_q = h < p.q.heads;
+        const Side& sd = is_q ? p.q : p.k;
+        const int hh = is_q ? h : h - p.q.heads;
+        const char* src = sd.in + tok * sd.in_tok + hh * sd.in_head;
+        dst[u] = sd.out + tok * sd.out_tok + hh * sd.out_head;
+        a[u] = *reinterpret_cast<const V*>(src + off0 * sizeof(T));
+        if (second) b[u] = *reinterpret_cast<const V*>(src + off1 * sizeof(T));
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      if (h0 + u < h_end) {
+        if (turns) {
+          if (kInterleaved && P > 1) {
+            // element pairs (2j, 2j + 1) over the two vectors
+#pragma unroll
+            for (int j = 0; j < P; j += 2) {
+              const float x = to_f(a[u].v[j]), y = to_f(a[u].v[j + 1]);
+              a[u].v[j] = from_f<T>(x * c[j / 2] - y * s[j / 2]);
+              a[u].v[j + 1] = from_f<T>(y * c[j / 2] + x * s[j / 2]);
+              const float z = to_f(b[u].v[j]), w = to_f(b[u].v[j + 1]);
+              b[u].v[j] = from_f<T>(z * c[(P + j) / 2] - w * s[(P + j) / 2]);
+              b[u].v[j + 1] = from_f<T>(w * c[(P + j) / 2] + z * s[(P + j) / 2]);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < P; ++j) {
+              const float x = to_f(a[u].v[j]), y = to_f(b[u].v[j]);
+              a[u].v[j] = from_f<T>(x * c[j] - y * s[j]);
+              b[u].v[j] = from_f<T>(y * c[j] + x * s[j]);
+            }
+          }
+        }
+        *reinterpret_cast<V*>(dst[u] + off0 * sizeof(T)) = a[u];
+        if (second) *reinterpret_cast<V*>(dst[u] + off1 * sizeof(T)) = b[u];
+      }
+    }
+  }
+}
+
+template <typename T, int P>
+cudaError_t launch(const RopeParams& p, bool interleaved, dim3 grid, cudaStream_t s) {
+  if (interleaved)
+    rope_kernel<T, P, true><<<grid, kThreads, 0, s>>>(p);
+  else
+    rope_kernel<T, P, false><<<grid, kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+int dtype_bytes(int dt) { return dt == SPLITKV_DTYPE_F32 ? 4 : 2; }
+
+// Bytes from the first to one past the last element of a strided [tokens][heads][d] array.
+int64_t extent(int64_t n, int heads, int64_t st, int64_t sh, int64_t d, int64_t es) {
+  return ((n - 1) * st + (heads - 1) * sh + d) * es;
+}
+
+// The output of one side: strides that keep every element apart, and either exactly the
+// input (in place) or memory apart from it.
+bool side_ok(const splitkv_rope_args& a, const void* in, const void* out, int heads, const int64_t* is,
+             const int64_t* os) {
+  if (heads == 0) return true;
+  if (!in || !out) return false;
+  const int64_t es = dtype_bytes(a.dtype), d = a.head_dim, n = a.num_tokens;
+  const int64_t kMax = int64_t(1) << 44;
+  for (int i = 0; i < 2; ++i)
+    if (is[i] < 0 || os[i] < 0 || is[i] > kMax || os[i] > kMax) return false;
+  if (n > kMax / (1 + is[0] + os[0])) return false;
+  if (reinterpret_cast<uintptr_t>(in) % es || reinterpret_cast<uintptr_t>(out) % es) return false;
+  const bool token_major = (heads == 1 || os[1] >= d) && (n == 1 || os[0] >= (heads - 1) * os[1] + d);
+  const bool head_major = (n == 1 || os[0] >= d) && (heads == 1 || os[1] >= (n - 1) * os[0] + d);
+  if (!token_major && !head_major) return false;
+  const uintptr_t i0 = reinterpret_cast<uintptr_t>(in), o0 = reinterpret_cast<uintptr_t>(out);
+  const bool same = i0 == o0 && (n == 1 || is[0] == os[0]) && (heads == 1 || is[1] == os[1]);
+  const uintptr_t i1 = i0 + extent(n, heads, is[0], is[1], d, es), o1 = o0 + extent(n, heads, os[0], os[1], d, es);
+  return same || i1 <= o0 || o1 <= i0;
+}
+
+}  // namespace
+
+extern "C" int splitkv_rope_freqs(int32_t rotary_dim, double base, int scaling, double factor, double original_len,
+                                  double turns_low, double turns_high, double* freqs, double* scale) {
+  if (rotary_dim < 2 || rotary_dim % 2 || !freqs || !scale || !(base > 0) || !std::isfinite(base) || !(factor > 0) ||
+      !std::isfinite(factor))
+    return SPLITKV_ERR_INVALID_ARG;
+  if (scaling < SPLITKV_ROPE_SCALE_NONE || scaling > SPLITKV_ROPE_SCALE_PARTS) return SPLITKV_ERR_INVALID_ARG;
+  if (scaling == SPLITKV_ROPE_SCALE_PARTS && !(original_len > 0 && turns_high > turns_low)) return SPLITKV_ERR_INVALID_ARG;
+  if (scaling == SPLITKV_ROPE_SCALE_BASE && rotary_dim > 2) base *= std::pow(factor, double(rotary_dim) / (rotary_dim - 2));
+  *scale = 1.0;
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    double w = std::pow(base, -2.0 * i / rotary_dim);
+    if (scaling == SPLITKV_ROPE_SCALE_LINEAR) w /= factor;
+    if (scaling == SPLITKV_ROPE_SCALE_PARTS) {
+      const double turns = original_len * w / 6.283185307179586476925;
+      double keep = (turns - turns_low) / (turns_high - turns_low);
+      keep = keep < 0 ? 0 : keep > 1 ? 1 : keep;
+      w = w / factor * (1 - keep) + w * keep;
+    }
+    freqs[i] = w;
+  }
+  if (scaling == SPLITKV_ROPE_SCALE_PARTS && factor > 1) *scale = 0.1 * std::log(factor) + 1.0;
+  return SPLITKV_OK;
+}
+
+extern "C" int splitkv_rope(const splitkv_rope_args* a, void* stream) {
+  if (!a) return SPLITKV_ERR_INVALID_ARG;
+  if (a->num_tokens < 0 || a->q_heads < 0 || a->k_heads < 0 || a->head_dim < 1 || a->rotary_dim < 2 ||
+      a->rotary_dim % 2 || a->rotary_dim > a->head_dim || a->head_dim > 65536 || a->q_heads > 65536 ||
+      a->k_heads > 65536)
+    return SPLITKV_ERR_INVALID_ARG;
+  if (a->dtype != SPLITKV_DTYPE_F32 && a->dtype != SPLITKV_DTYPE_BF16 && a->dtype != SPLITKV_DTYPE_F16)
+    return SPLITKV_ERR_INVALID_ARG;
+  if (a->flags & ~(SPLITKV_ROPE_INTERLEAVED | SPLITKV_ROPE_ADJOINT | SPLITKV_ROPE_POS64)) return SPLITKV_ERR_INVALID_ARG;
+  const int heads = a->q_heads + a->k_heads;
+  if (a->num_tokens == 0 || heads == 0) return SPLITKV_OK;
+  const bool pos64 = (a->flags & SPLITKV_ROPE_POS64) != 0;
+  if (!a->positions || !a->freqs || !splitkv::ptr_aligned(a->positions, pos64 ? 8 : 4) ||
+      !splitkv::ptr_aligned(a->freqs, 8))
+    return SPLITKV_ERR_INVALID_ARG;
+  if (!side_ok(*a, a->q, a->q_out, a->q_heads, a->q_stride, a->q_out_stride) ||
+      !side_ok(*a, a->k, a->k_out, a->k_heads, a->k_stride, a->k_out_stride))
+    return SPLITKV_ERR_INVALID_ARG;
+
+  const int es = dtype_bytes(a->dtype), P = 16 / es;
+  // 16-byte accesses need every vector on a 16-byte boundary
+  bool vec = (a->rotary_dim / 2) % P == 0 && a->head_dim % P == 0;
+  const auto fits = [&](const void* in, const void* out, int n, const int64_t* is, const int64_t* os) {
+    return n == 0 || (splitkv::ptr_aligned(in, 16) && splitkv::ptr_aligned(out, 16) && is[0] % P == 0 &&
+                      is[1] % P == 0 && os[0] % P == 0 && os[1] % P == 0);
+  };
+  vec = vec && fits(a->q, a->q_out, a->q_heads, a->q_stride, a->q_out_stride) &&
+        fits(a->k, a->k_out, a->k_heads, a->k_stride, a->k_out_stride);
+  const int pairs = vec ? P : 1;
+
+  RopeParams p;
+  p.q = Side{static_cast<const char*>(a->q), static_cast<char*>(a->q_out), a->q_stride[0] * es, a->q_stride[1] * es,
+             a->q_out_stride[0] * es, a->q_out_stride[1] * es, a->q_heads};
+  p.k = Side{static_cast<const char*>(a->k), static_cast<char*>(a->k_out), a->k_stride[0] * es, a->k_stride[1] * es,
+             a->k_out_stride[0] * es, a->k_out_stride[1] * es, a->k_heads};
+  p.positions = a->positions;
+  p.freqs = a->freqs;
+  p.n_tokens = a->num_tokens;
+  p.half = a->rotary_dim / 2;
+  p.turn_units = p.half / pairs;
+  const bool in_place = (a->q_heads == 0 || a->q == a->q_out) && (a->k_heads == 0 || a->k == a->k_out);
+  p.copy_vecs = in_place ? 0 : (a->head_dim - a->rotary_dim) / pairs;
+  p.units = p.turn_units + (p.copy_vecs + 1) / 2;
+  p.m = float(a->scale);
+  p.pos64 = pos64;
+  p.adjoint = (a->flags & SPLITKV_ROPE_ADJOINT) != 0;
+
+  // Heads per thread: all of them would compute each angle once, but a few tokens then leave
+  // the GPU idle and one thread a long chain of loads.
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int64_t threads = p.n_tokens * p.units;
+  int64_t hpt = threads * heads / (int64_t(sms) * 2048);
+  hpt = hpt < kUnroll ? kUnroll : hpt > 16 ? 16 : hpt / kUnroll * kUnroll;
+  p.heads_per_thread = int(hpt);
+  const int64_t blocks = (threads + kThreads - 1) / kThreads;
+  const int64_t gy = (heads + hpt - 1) / hpt;
+  if (blocks > 0x7fffffff || gy > 65535) return SPLITKV_ERR_UNSUPPORTED;
+  const dim3 grid{unsigned(blocks), unsigned(gy)};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool il = (a->flags & SPLITKV_ROPE_INTERLEAVED) != 0;
+  cudaError_t e;
+  if (a->dtype == SPLITKV_DTYPE_F32)
+    e = vec ? launch<float, 4>(p, il, grid, s) : launch<float, 1>(p, il, grid, s);
+  else if (a->dtype == SPLITKV_DTYPE_BF16)
+    e = vec ? launch<__nv_bfloat16, 8>(p, il, grid, s) : launch<__nv_bfloat16, 1>(p, il, grid, s);
+  else
+    e = vec ? launch<__half, 8>(p, il, grid, s) : launch<__half, 1>(p, il, grid, s);
+  if (e == cudaSuccess) return SPLITKV_OK;
+  return SPLITKV_ERR_CUDA;
+}

@@ -1,0 +1,126 @@
+// Shared by the tree-attention kernels: the device view of a call, and how the context work
+// is cut over the CTAs of a launch.  Not part of the public ABI.
+//
+// A unit is one (sequence, KV head, row tile): up to Mt rows (node-major, the G query heads
+// of a node next to each other) against the sequence's whole context.  The units' key tiles
+// of kTileKeys keys lie on one line, in (sequence, KV head, row tile, key tile) order, and
+// CTA c of C takes the stretch [c W / C, (c + 1) W / C) of its W tiles: every CTA has the same
+// number of tiles to within one, whatever the lengths, and the lengths stay on the device (a
+// captured graph replays with new ones).  A CTA's part of a unit is one record (unnormalised
+// O, row maximum, row sum).  Walking the line, either the CTA or the unit number steps at
+// each boundary, so record (c, u) is number c + u: C + U - 1 records at most, no atomics and a
+// fixed order of the merge.
+#pragma once
+
+#include <cstdint>
+
+#include "splitkv.h"
+#include "splitkv_internal.h"
+
+namespace splitkv {
+namespace tree {
+
+constexpr int kTileKeys = 64;      // keys of one step of the line
+constexpr int kMaxNodes = 256;     // nodes of a sequence
+
+struct TreeParams {
+  const char *q, *kb, *vb, *kc, *vc;
+  char* o;
+  float* lse;
+  const uint8_t* mask;             // NULL: a node sees every node of its sequence
+  const int *node_ptr, *lens, *table;
+  int* status;
+  // strides in bytes
+  int64_t q_node, q_head, kb_node, kb_head, vb_node, vb_head;
+  int64_t kc_page, kc_slot, kc_head, vc_page, vc_slot, vc_head;
+  int64_t mask_row, table_row;     // elements
+  int B, Nq, T, Hq, Hkv, G, d;
+  int Mt, RT;                      // rows of a row tile; row tiles of max_nodes nodes
+  int page_shift, num_pages, max_pages;
+  int ctas;                        // C: CTAs of the context kernel
+  int o_f32;
+  float scale_log2;
+  float* rec_o;                    // [C + U][Mt][d]
+  float2* rec_ml;                  // [C + U][Mt]: maximum (log2 units), sum
+};
+
+#ifdef __CUDACC__
+
+// Nodes, first row and context length of sequence b as the kernels take them: what lies
+// outside the call's arrays counts as nothing (the context kernel records the error).
+__device__ __forceinline__ int seq_nodes(const TreeParams& p, int b, int& n0, bool& bad) {
+  n0 = p.node_ptr[b];
+  const int n1 = p.node_ptr[b + 1];
+  if (n0 < 0 || n1 < n0 || n1 > p.Nq || n1 - n0 > p.T) {
+    bad = true;
+    return 0;
+  }
+  return n1 - n0;
+}
+__device__ __forceinline__ int seq_len(const TreeParams& p, int b, bool& bad) {
+  const int len = p.lens[b];
+  const int64_t cap = int64_t(p.max_pages) << p.page_shift;
+  if (len < 0 || len > cap) {
+    bad = true;
+    return len < 0 ? 0 : int(cap);
+  }
+  return len;
+}
+
+struct SeqWork {
+  int n0, n, len, rts, nt;   // first node, nodes, context length, row tiles, key tiles of a unit
+  long long tiles;           // Hkv * rts * nt
+};
+
+__device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b, bool& bad) {
+  SeqWork w;
+  w.n = seq_nodes(p, b, w.n0, bad);
+  w.len = seq_len(p, b, bad);
+  w.rts = (w.n * p.G + p.Mt - 1) / p.Mt;
+  w.nt = (w.len + kTileKeys - 1) / kTileKeys;
+  w.tiles = (long long)(p.Hkv) * w.rts * w.nt;
+  return w;
+}
+
+// Block-wide: exclusive prefix of the threads' sums (each thread takes consecutive
+// sequences), through `scratch` [kThreads / 32 + 1].  Returns the total.
+template <int kThreads>
+__device__ __forceinline__ long long block_prefix(long long mine, long long& before, long long* scratch) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  long long inc = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) scratch[warp] = inc;
+  __syncthreads();
+  long long add = 0, all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) add += scratch[w];
+    all += scratch[w];
+  }
+  before = add + inc - mine;
+  return all;
+}
+
+// First tile of CTA c's stretch (c in [0, C]); C never exceeds the line's length W.
+__device__ __forceinline__ long long stretch(long long W, int c, int C) { return W * c / C; }
+
+// The CTA whose stretch holds tile x.
+__device__ __forceinline__ int cta_of(long long x, long long W, int C) {
+  int c = int(x * C / W);
+  while (c > 0 && stretch(W, c, C) > x) --c;
+  while (c + 1 < C && stretch(W, c + 1, C) <= x) ++c;
+  return c;
+}
+
+#endif  // __CUDACC__
+
+// ---- launchers
+cudaError_t launch_tree_context_mma(const TreeParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_tree_merge(const TreeParams& p, int dtype, cudaStream_t s);
+
+}  // namespace tree
+}  // namespace splitkv

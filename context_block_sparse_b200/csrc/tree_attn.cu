@@ -1,0 +1,809 @@
+// Attention of draft trees over a paged cache, on mma.sync: the context kernel (every row of
+// a sequence's nodes against its cached keys, split over the CTAs) and the merge (the
+// in-tree keys, then the context records).
+//
+// Per row (node i, query head h) of sequence b, over the keys j of its context [0, len_b) and
+// the nodes j of its own tree that mask lets i see, with KV head h / G:
+//   s_j = scale q.k_j, m = max s_j, l = sum exp(s_j - m), o = sum exp(s_j - m) v_j / l,
+//   lse = m + log l;  a row with no key: o = 0, lse = -inf.
+//
+// A few rows read a long cache once, so the context kernel is HBM-bound: 4 len_b d bytes a KV
+// head.  The G heads of all a sequence's nodes share every key tile (16, 32 or 64 rows of a
+// CTA); 64-key tiles flow through a ring of cp.async stages that does not drain at unit
+// boundaries, two CTAs to an SM: 128 KB of loads in flight per SM against the ~35 KB that
+// 6.5 TB/s at 0.8 us of latency need.  Pages are resolved per key (any power-of-two page size,
+// any strides), one tile ahead.  With 16 rows the four warps share the tile by keys, with 64 by
+// rows, and softmax statistics stay in registers; scores, maxima, sums and O are float32, P is
+// rounded to the keys' type for the second product, as in the training kernels.
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "tree.h"
+
+namespace splitkv {
+namespace tree {
+namespace {
+
+constexpr int kThreads = 128;
+constexpr int kPgRing = 8;         // page-id slots (tiles): at least the stages + 1
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                         __nv_bfloat16) {
+  mma_bf16_16816(c, a, b0, b1);
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, __half) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __nv_bfloat16) { return pack_bf16(lo, hi); }
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) {
+  __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// Offset of (row r, 16-byte chunk ch) in a [rows][N] tile.  Rows of 64 bytes (N = 32) swizzle their
+// four chunks by row pairs, wider ones as swz: ldmatrix over 8 consecutive rows touches 8 distinct
+// bank groups either way.
+template <int N>
+__device__ __forceinline__ int swz_v(int r, int ch) {
+  return N == 32 ? r * N + ((ch ^ ((r >> 1) & 3)) << 3) : swz<N>(r, ch);
+}
+
+// The A fragments of 16 rows of Q straight from global memory (rows past the tile's are zero):
+// thread t holds rows t/4 and t/4 + 8, column pairs 2 (t % 4) of every 8 columns.
+template <int D>
+__device__ __forceinline__ void load_q(uint32_t (&qf)[D / 16][4], const TreeParams& p, int n0, int n, int head,
+                                       int row0) {
+  const int lane = threadIdx.x & 31;
+  const char* ptr[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int r = row0 + (lane >> 2) + 8 * k;
+    const int node = r / p.G, g = r - node * p.G;
+    ptr[k] = node < n ? p.q + int64_t(n0 + node) * p.q_node + int64_t(head * p.G + g) * p.q_head + 4 * (lane & 3)
+                      : nullptr;
+  }
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const char* base = ptr[e & 1];
+      qf[kk][e] = base ? *reinterpret_cast<const uint32_t*>(base + kk * 32 + (e >> 1) * 16) : 0u;
+    }
+  }
+}
+
+// S (16 rows x kKeys keys) = Q K^T, K rows [key0, key0 + kKeys) of a swizzled [64][D] tile.
+template <typename T, int D, int kKeys>
+__device__ __forceinline__ void scores(float (&s)[kKeys / 8][4], const uint32_t (&qf)[D / 16][4], const T* sk,
+                                       int key0) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int i = 0; i < kKeys / 8; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[i][e] = 0.f;
+  const int row = key0 + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+#pragma unroll
+    for (int g = 0; g < kKeys / 16; ++g) {
+      uint32_t b0, b1, b2, b3;
+      ldsm_x4(b0, b1, b2, b3, sk + swz<D>(row + 16 * g, kk * 2 + ((lane >> 3) & 1)));
+      mma16816(s[2 * g], qf[kk], b0, b1, T());
+      mma16816(s[2 * g + 1], qf[kk], b2, b3, T());
+    }
+  }
+}
+
+// The state of two rows of a thread: maximum (log2 units), this thread's share of the sum, and
+// the rows' NC columns of O.
+template <int NC>
+struct Rows {
+  float m[2], l[2];
+  float o[NC / 8][4];
+  __device__ __forceinline__ void clear() {
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < NC / 8; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+  }
+};
+
+// One online-softmax step: s (log2 units, masked scores -inf) against V rows [key0, ...) and
+// columns of a swizzled [64][NC] tile.
+template <typename T, int NC, int kKeys>
+__device__ __forceinline__ void softmax_step(Rows<NC>& st, float (&s)[kKeys / 8][4], const T* sv, int key0) {
+  const int lane = threadIdx.x & 31;
+  float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+  for (int i = 0; i < kKeys / 8; ++i) {
+    mx[0] = fmaxf(mx[0], fmaxf(s[i][0], s[i][1]));
+    mx[1] = fmaxf(mx[1], fmaxf(s[i][2], s[i][3]));
+  }
+  float ref[2], f[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
+    mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
+    const float m = fmaxf(st.m[k], mx[k]);
+    ref[k] = m == -INFINITY ? 0.f : m;    // no key yet: every exponential below is exp2(-inf) = 0
+    f[k] = fast_exp2(st.m[k] - ref[k]);
+    st.m[k] = m;
+    st.l[k] *= f[k];
+  }
+#pragma unroll
+  for (int i = 0; i < kKeys / 8; ++i) {
+    s[i][0] = fast_exp2(s[i][0] - ref[0]);
+    s[i][1] = fast_exp2(s[i][1] - ref[0]);
+    s[i][2] = fast_exp2(s[i][2] - ref[1]);
+    s[i][3] = fast_exp2(s[i][3] - ref[1]);
+    st.l[0] += s[i][0] + s[i][1];
+    st.l[1] += s[i][2] + s[i][3];
+  }
+  if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+    for (int i = 0; i < NC / 8; ++i) {
+      st.o[i][0] *= f[0];
+      st.o[i][1] *= f[0];
+      st.o[i][2] *= f[1];
+      st.o[i][3] *= f[1];
+    }
+  }
+  const int row = key0 + (lane & 15);
+#pragma unroll
+  for (int g = 0; g < kKeys / 16; ++g) {
+    const uint32_t a[4] = {pack2(s[2 * g][0], s[2 * g][1], T()), pack2(s[2 * g][2], s[2 * g][3], T()),
+                           pack2(s[2 * g + 1][0], s[2 * g + 1][1], T()), pack2(s[2 * g + 1][2], s[2 * g + 1][3], T())};
+#pragma unroll
+    for (int c = 0; c < NC / 16; ++c) {
+      uint32_t b0, b1, b2, b3;
+      ldsm_x4_t(b0, b1, b2, b3, sv + swz_v<NC>(row + 16 * g, c * 2 + (lane >> 4)));
+      mma16816(st.o[2 * c], a, b0, b1, T());
+      mma16816(st.o[2 * c + 1], a, b2, b3, T());
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------- context kernel
+// A CTA's place on the line: the unit and key tile of the tile it points at.
+struct Cursor {
+  SeqWork w;
+  int b, head, rt, tile;
+  bool bad;
+  __device__ __forceinline__ void enter(const TreeParams& p, int seq, long long rel) {
+    b = seq;
+    w = seq_work(p, b, bad);
+    const long long unit = rel / w.nt;
+    tile = int(rel - unit * w.nt);
+    head = int(unit / w.rts);
+    rt = int(unit - (long long)(head) * w.rts);
+  }
+  // the next tile of the line; the caller knows that there is one
+  __device__ __forceinline__ void step(const TreeParams& p) {
+    if (++tile < w.nt) return;
+    tile = 0;
+    if (++rt < w.rts) return;
+    rt = 0;
+    if (++head < p.Hkv) return;
+    head = 0;
+    do {
+      ++b;
+      if (b >= p.B) return;
+      w = seq_work(p, b, bad);
+    } while (w.tiles == 0);
+  }
+};
+
+template <int D, int RG>
+struct Cfg {
+  static constexpr int kKG = 4 / RG;                    // warps that share a row group's keys
+  static constexpr int kKeysW = kTileKeys / kKG;        // keys of a tile that one warp takes
+  static constexpr int kStages = D == 128 ? 3 : 5;
+  static constexpr int kStageElems = 2 * kTileKeys * D; // K then V
+  static constexpr int kSmem = kStages * kStageElems * 2 + 16 * D * 4 /* O exchange */;
+};
+
+template <typename T, int D, int RG>
+__global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const TreeParams p) {
+  using C = Cfg<D, RG>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  T* stages = reinterpret_cast<T*>(smem);
+  float* s_o = reinterpret_cast<float*>(smem + C::kStages * C::kStageElems * 2);   // [16][D]
+  __shared__ long long s_scan[kThreads / 32];
+  __shared__ long long s_rel;
+  __shared__ int s_seq;
+  __shared__ int s_pg[kPgRing][kTileKeys];
+  __shared__ int s_part[kPgRing][2];        // a tile's first and second 32 keys: not all of them are there
+  __shared__ float2 s_ml[4][16];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rg = warp / C::kKG, kg = warp % C::kKG;
+
+  // this CTA's stretch of the line, and the sequence it begins in
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  long long mine = 0, before;
+  bool bad = false;
+  for (int b = b0; b < b1; ++b) mine += seq_work(p, b, bad).tiles;
+  if (bad && blockIdx.x == 0 && p.status) atomicCAS(p.status, 0, SPLITKV_ERR_INVALID_ARG);
+  const long long W = block_prefix<kThreads>(mine, before, s_scan);
+  const int ctas = int(min((long long)(p.ctas), W));
+  if (int(blockIdx.x) >= ctas) return;
+  const long long x0 = stretch(W, blockIdx.x, ctas);
+  const int n_tiles = int(stretch(W, blockIdx.x + 1, ctas) - x0);
+  if (x0 >= before && x0 < before + mine) {
+    long long at = before;
+    for (int b = b0; b < b1; ++b) {
+      const long long t = seq_work(p, b, bad).tiles;
+      if (x0 < at + t) {
+        s_seq = b;
+        s_rel = x0 - at;
+        break;
+      }
+      at += t;
+    }
+  }
+  __syncthreads();
+  Cursor load, use;   // the tile whose pages come next; the tile computed now
+  load.bad = use.bad = false;
+  use.enter(p, s_seq, s_rel);
+  load = use;
+  Cursor fill = use;  // the tile whose keys and values are requested next
+
+  // page ids of the `load` cursor's tile (-1: no such key), by 64 threads
+  auto resolve = [&](int t) {
+    if (tid < kTileKeys) {
+      const int key = load.tile * kTileKeys + tid;
+      int page = -1;
+      if (key < load.w.len) {
+        page = p.table[load.b * p.table_row + (key >> p.page_shift)];
+        if (page < 0 || page >= p.num_pages) {
+          page = -1;
+          if (p.status) atomicCAS(p.status, 0, SPLITKV_ERR_INVALID_ARG);
+        }
+      }
+      s_pg[t % kPgRing][tid] = page;
+      const bool part = __any_sync(0xffffffffu, page < 0);
+      if (lane == 0) s_part[t % kPgRing][warp] = part;
+    }
+  };
+  constexpr int kChunks = D / 8;                    // 16-byte chunks of a key row
+  constexpr int kRowsPer = kThreads / kChunks;      // rows of one pass of the CTA
+  auto request = [&](int t) {
+    T* sk = stages + (t % C::kStages) * C::kStageElems;
+    T* sv = sk + kTileKeys * D;
+    const int ch = tid % kChunks;
+    const char* kbase = p.kc + fill.head * p.kc_head + ch * 16;
+    const char* vbase = p.vc + fill.head * p.vc_head + ch * 16;
+    const int slot_mask = (1 << p.page_shift) - 1;
+#pragma unroll
+    for (int i = 0; i < kTileKeys / kRowsPer; ++i) {
+      const int r = tid / kChunks + i * kRowsPer;
+      const int page = s_pg[t % kPgRing][r];
+      const int slot = (fill.tile * kTileKeys + r) & slot_mask;
+      const bool there = page >= 0;
+      const int64_t pg = there ? page : 0, sl = there ? slot : 0;
+      cp_async16(sk + swz<D>(r, ch), kbase + pg * p.kc_page + sl * p.kc_slot, there);
+      cp_async16(sv + swz<D>(r, ch), vbase + pg * p.vc_page + sl * p.vc_slot, there);
+    }
+  };
+
+  for (int t = 0; t < C::kStages && t < n_tiles; ++t) {
+    resolve(t);
+    if (t + 1 < n_tiles) load.step(p);
+  }
+  __syncthreads();
+  for (int t = 0; t < C::kStages - 1; ++t) {
+    if (t < n_tiles) {
+      request(t);
+      if (t + 1 < n_tiles) fill.step(p);
+    }
+    cp_async_commit();
+  }
+
+  uint32_t qf[D / 16][4];
+  Rows<D> st;
+  bool fresh = true;
+  for (int t = 0; t < n_tiles; ++t) {
+    cp_async_wait<C::kStages - 2>();
+    __syncthreads();   // tile t has landed; every warp is done with tile t - 1's stage
+    if (t + C::kStages - 1 < n_tiles) {
+      request(t + C::kStages - 1);
+      if (t + C::kStages < n_tiles) fill.step(p);
+    }
+    cp_async_commit();
+    if (t + C::kStages < n_tiles) {
+      resolve(t + C::kStages);
+      if (t + C::kStages + 1 < n_tiles) load.step(p);
+    }
+    if (fresh) {
+      load_q<D>(qf, p, use.w.n0, use.w.n, use.head, use.rt * p.Mt + rg * 16);
+      st.clear();
+      fresh = false;
+    }
+    const T* sk = stages + (t % C::kStages) * C::kStageElems;
+    float s[C::kKeysW / 8][4];
+    scores<T, D, C::kKeysW>(s, qf, sk, kg * C::kKeysW);
+    const bool part = s_part[t % kPgRing][0] || s_part[t % kPgRing][1];
+#pragma unroll
+    for (int i = 0; i < C::kKeysW / 8; ++i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[i][e] *= p.scale_log2;
+      if (part) {
+        const int col = kg * C::kKeysW + 8 * i + 2 * (lane & 3);
+        if (s_pg[t % kPgRing][col] < 0) s[i][0] = s[i][2] = -INFINITY;
+        if (s_pg[t % kPgRing][col + 1] < 0) s[i][1] = s[i][3] = -INFINITY;
+      }
+    }
+    softmax_step<T, D, C::kKeysW>(st, s, sk + kTileKeys * D, kg * C::kKeysW);
+
+    const bool last = t + 1 == n_tiles || use.tile + 1 == use.w.nt;
+    if (last) {
+      // the unit's part of this CTA is complete: add the key groups, write the record
+      const int unit = (use.b * p.Hkv + use.head) * p.RT + use.rt;
+      const size_t rec = size_t(blockIdx.x) + unit;
+      const int rows = min(p.Mt, use.w.n * p.G - use.rt * p.Mt);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        st.l[k] += __shfl_xor_sync(0xffffffffu, st.l[k], 1);
+        st.l[k] += __shfl_xor_sync(0xffffffffu, st.l[k], 2);
+        if ((lane & 3) == 0) s_ml[warp][(lane >> 2) + 8 * k] = make_float2(st.m[k], st.l[k]);
+      }
+      __syncthreads();
+      float f[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = (lane >> 2) + 8 * k;
+        float m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int x = 0; x < C::kKG; ++x) m = fmaxf(m, s_ml[rg * C::kKG + x][r].x);
+        const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int x = 0; x < C::kKG; ++x) l += s_ml[rg * C::kKG + x][r].y * fast_exp2(s_ml[rg * C::kKG + x][r].x - ref);
+        f[k] = fast_exp2(st.m[k] - ref);
+        if (kg == 0 && (lane & 3) == 0 && rg * 16 + r < rows) p.rec_ml[rec * p.Mt + rg * 16 + r] = make_float2(m, l);
+      }
+      float4 acc[D / 32];   // this thread's float4s of the [16][D] block
+#pragma unroll 1
+      for (int w = 0; w < 4; ++w) {
+        if (warp == w) {
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              *reinterpret_cast<float2*>(s_o + ((lane >> 2) + 8 * k) * D + ((8 * i + 2 * (lane & 3)) ^ (((lane >> 2) & 3) << 3))) =
+                  make_float2(st.o[i][2 * k] * f[k], st.o[i][2 * k + 1] * f[k]);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+          const int e = (i * kThreads + tid) * 4, r = e / D, c = e % D;
+          const float4 x = *reinterpret_cast<const float4*>(s_o + r * D + (c ^ ((r & 3) << 3)));
+          if (w % C::kKG == 0)
+            acc[i] = x;
+          else
+            acc[i] = make_float4(acc[i].x + x.x, acc[i].y + x.y, acc[i].z + x.z, acc[i].w + x.w);
+          if (w % C::kKG == C::kKG - 1) {
+            const int row = (w / C::kKG) * 16 + r;
+            if (row < rows) *reinterpret_cast<float4*>(p.rec_o + (rec * p.Mt + row) * D + c) = acc[i];
+          }
+        }
+        __syncthreads();
+      }
+      fresh = true;
+    }
+    if (t + 1 < n_tiles) use.step(p);
+  }
+  cp_async_wait<0>();
+}
+
+// ------------------------------------------------------------------------------------ merge
+// One CTA per (unit, 16 RG rows, 32 columns of the head): the in-tree term first (64 nodes of
+// K and the slice's 32 columns of V at a time, by keys or rows over the four warps as in the
+// context kernel), then the unit's records streamed on top of it, in CTA order.
+constexpr int kSlice = 32;
+
+template <typename T>
+__device__ __forceinline__ bool not_finite16(uint16_t x);
+template <>
+__device__ __forceinline__ bool not_finite16<__nv_bfloat16>(uint16_t x) {
+  return (x & 0x7f80u) == 0x7f80u;
+}
+template <>
+__device__ __forceinline__ bool not_finite16<__half>(uint16_t x) {
+  return (x & 0x7c00u) == 0x7c00u;
+}
+
+template <typename T, int D, int RG>
+__global__ void __launch_bounds__(kThreads) tree_merge_kernel(const TreeParams p) {
+  constexpr int kKG = 4 / RG;
+  constexpr int kKeysW = kTileKeys / kKG;
+  constexpr int kRows = 16 * RG;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  T* s_k = reinterpret_cast<T*>(smem);                       // [64][D]
+  T* s_v = s_k + kTileKeys * D;                              // [64][32]
+  float* s_o = reinterpret_cast<float*>(s_v + kTileKeys * kSlice);   // [4 warps][16][32]
+  __shared__ long long s_scan[kThreads / 32];
+  __shared__ long long s_before;
+  __shared__ float2 s_ml[4][16];
+  __shared__ unsigned long long s_flag;
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rg = warp / kKG, kg = warp % kKG;
+  const int subs = p.Mt / kRows;
+  const int unit = blockIdx.x / subs, sub = blockIdx.x % subs;
+  const int rt = unit % p.RT, bh = unit / p.RT;
+  const int head = bh % p.Hkv, b = bh / p.Hkv;
+  const int col0 = blockIdx.y * kSlice;
+  bool bad = false;
+  const SeqWork w = seq_work(p, b, bad);
+  const int row0 = rt * p.Mt + sub * kRows;
+  const int rows = min(kRows, w.n * p.G - row0);
+  if (rows <= 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    return;
+  }
+
+  // the in-tree term
+  uint32_t qf[D / 16][4];
+  Rows<kSlice> st;
+  st.clear();
+  load_q<D>(qf, p, w.n0, w.n, head, row0 + rg * 16);
+  const uint8_t* mrow[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int r = row0 + rg * 16 + (lane >> 2) + 8 * k;
+    mrow[k] = p.mask && r / p.G < w.n ? p.mask + int64_t(w.n0 + r / p.G) * p.mask_row : nullptr;
+  }
+  for (int j0 = 0; j0 < w.n; j0 += kTileKeys) {
+    constexpr int kChunks = D / 8;
+    __syncthreads();   // the last tile's readers are done
+    if (tid == 0) s_flag = 0;
+    for (int i = tid; i < kTileKeys * kChunks; i += kThreads) {
+      const int r = i / kChunks, ch = i % kChunks;
+      const bool there = j0 + r < w.n;
+      const int64_t node = there ? w.n0 + j0 + r : w.n0;
+      cp_async16(s_k + swz<D>(r, ch), p.kb + node * p.kb_node + head * p.kb_head + ch * 16, there);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = tid / 4 + 32 * i, ch = tid % 4;
+      const bool there = j0 + r < w.n;
+      const int64_t node = there ? w.n0 + j0 + r : w.n0;
+      cp_async16(s_v + swz_v<kSlice>(r, ch), p.vb + node * p.vb_node + head * p.vb_head + col0 * 2 + ch * 16, there);
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+    __syncthreads();
+    // A node's V may hold infinities or NaN that only the rows which see it may meet, but the
+    // product below multiplies every V by P = 0 elsewhere: take such values out (each thread
+    // checks what it loaded) and add them back where they are seen.
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = tid / 4 + 32 * i;
+      uint16_t* x = reinterpret_cast<uint16_t*>(s_v + swz_v<kSlice>(r, tid % 4));
+      bool any = false;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (not_finite16<T>(x[e])) {
+          x[e] = 0;
+          any = true;
+        }
+      if (any) atomicOr(&s_flag, 1ull << r);
+    }
+    __syncthreads();
+    float s[kKeysW / 8][4];
+    scores<T, D, kKeysW>(s, qf, s_k, kg * kKeysW);
+#pragma unroll
+    for (int i = 0; i < kKeysW / 8; ++i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = j0 + kg * kKeysW + 8 * i + 2 * (lane & 3) + (e & 1);
+        const bool sees = j < w.n && (p.mask == nullptr || (mrow[e >> 1] && mrow[e >> 1][j]));
+        s[i][e] = sees ? s[i][e] * p.scale_log2 : -INFINITY;
+      }
+    }
+    softmax_step<T, kSlice, kKeysW>(st, s, s_v, kg * kKeysW);
+    unsigned long long flag = s_flag >> (kg * kKeysW) & (kKeysW == 64 ? ~0ull : (1ull << (kKeysW & 63)) - 1);
+    while (flag) {
+      const int j = j0 + kg * kKeysW + __ffsll(flag) - 1;
+      flag &= flag - 1;
+      const T* v = reinterpret_cast<const T*>(p.vb + int64_t(w.n0 + j) * p.vb_node + head * p.vb_head) + col0;
+#pragma unroll
+      for (int i = 0; i < kSlice / 8; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = float(v[8 * i + 2 * (lane & 3) + (e & 1)]);
+          if (!isfinite(x) && (p.mask == nullptr || (mrow[e >> 1] && mrow[e >> 1][j]))) st.o[i][e] += x;
+        }
+    }
+  }
+
+  // the four warps' parts to shared memory
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    st.l[k] += __shfl_xor_sync(0xffffffffu, st.l[k], 1);
+    st.l[k] += __shfl_xor_sync(0xffffffffu, st.l[k], 2);
+    if ((lane & 3) == 0) s_ml[warp][(lane >> 2) + 8 * k] = make_float2(st.m[k], st.l[k]);
+  }
+#pragma unroll
+  for (int i = 0; i < kSlice / 8; ++i)
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      *reinterpret_cast<float2*>(s_o + (warp * 16 + (lane >> 2) + 8 * k) * kSlice + 8 * i + 2 * (lane & 3)) =
+          make_float2(st.o[i][2 * k], st.o[i][2 * k + 1]);
+
+  // the line: where this sequence begins, how long it is
+  const int per = (p.B + kThreads - 1) / kThreads;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  long long mine = 0, before;
+  for (int i = b0; i < b1; ++i) mine += seq_work(p, i, bad).tiles;
+  const long long W = block_prefix<kThreads>(mine, before, s_scan);
+  if (b >= b0 && b < b1) {
+    for (int i = b0; i < b; ++i) before += seq_work(p, i, bad).tiles;
+    s_before = before;
+  }
+  __syncthreads();
+
+  // the context records: written by the kernel before this one in the stream
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  size_t rec0 = 0, rec1 = 0;
+  if (w.nt > 0) {
+    const int ctas = int(min((long long)(p.ctas), W));
+    const long long u0 = s_before + ((long long)(head) * w.rts + rt) * w.nt;
+    rec0 = size_t(unit) + cta_of(u0, W, ctas);
+    rec1 = size_t(unit) + cta_of(u0 + w.nt - 1, W, ctas) + 1;
+  }
+  constexpr int kVec = kRows * kSlice / 4 / kThreads;   // float4s of a thread
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int e = i * kThreads + tid, r = e / (kSlice / 4), c = (e % (kSlice / 4)) * 4;
+    if (r >= rows) continue;
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int wr = (r / 16) * kKG, rr = r % 16;
+#pragma unroll
+    for (int x = 0; x < kKG; ++x) m = fmaxf(m, s_ml[wr + x][rr].x);
+    float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int x = 0; x < kKG; ++x) {
+      const float f = fast_exp2(s_ml[wr + x][rr].x - ref);
+      const float4 y = *reinterpret_cast<const float4*>(s_o + ((wr + x) * 16 + rr) * kSlice + c);
+      l += s_ml[wr + x][rr].y * f;
+      o = make_float4(o.x + y.x * f, o.y + y.y * f, o.z + y.z * f, o.w + y.w * f);
+    }
+    const size_t at = size_t(sub) * kRows + r;
+    constexpr int kBatch = 8;
+    for (size_t r0 = rec0; r0 < rec1; r0 += kBatch) {
+      float2 ml[kBatch];
+      float4 y[kBatch];
+      const int nb = int(min(size_t(kBatch), rec1 - r0));
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (k < nb) {
+          ml[k] = p.rec_ml[(r0 + k) * p.Mt + at];
+          y[k] = *reinterpret_cast<const float4*>(p.rec_o + ((r0 + k) * p.Mt + at) * D + col0 + c);
+        }
+      }
+      float nm = m;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k)
+        if (k < nb) nm = fmaxf(nm, ml[k].x);
+      const float nref = nm == -INFINITY ? 0.f : nm;
+      const float f0 = fast_exp2(m - nref);
+      l *= f0;
+      o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (k < nb) {
+          const float f = fast_exp2(ml[k].x - nref);
+          l += ml[k].y * f;
+          o = make_float4(o.x + y[k].x * f, o.y + y[k].y * f, o.z + y[k].z * f, o.w + y[k].w * f);
+        }
+      }
+      m = nm;
+    }
+    const int row = row0 + r, node = w.n0 + row / p.G, h = head * p.G + row % p.G;
+    const float inv = l == 0.f ? 0.f : 1.f / l;   // no key: o = 0 (a NaN sum stays NaN)
+    o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    const size_t dst = (size_t(node) * p.Hq + h) * D + col0 + c;
+    if (p.o_f32)
+      *reinterpret_cast<float4*>(p.o + dst * 4) = o;
+    else
+      *reinterpret_cast<uint2*>(p.o + dst * 2) = make_uint2(pack2(o.x, o.y, T()), pack2(o.z, o.w, T()));
+    if (blockIdx.y == 0 && c == 0)
+      p.lse[size_t(node) * p.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  }
+}
+
+template <typename T, int D, int RG>
+cudaError_t context(const TreeParams& p, cudaStream_t s) {
+  constexpr int kSmem = Cfg<D, RG>::kSmem;
+  cudaError_t e = cudaFuncSetAttribute(tree_context_mma_kernel<T, D, RG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kSmem);
+  if (e != cudaSuccess) return e;
+  tree_context_mma_kernel<T, D, RG><<<p.ctas, kThreads, kSmem, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t context_rows(const TreeParams& p, cudaStream_t s) {
+  return p.Mt == 16 ? context<T, D, 1>(p, s) : p.Mt == 32 ? context<T, D, 2>(p, s) : context<T, D, 4>(p, s);
+}
+
+template <typename T, int D, int RG>
+cudaError_t merge(const TreeParams& p, cudaStream_t s) {
+  constexpr int kSmem = kTileKeys * (D + kSlice) * 2 + 4 * 16 * kSlice * 4;
+  const int64_t units = int64_t(p.B) * p.Hkv * p.RT * (p.Mt / (16 * RG));
+  if (units > 0x7fffffff) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(units), D / kSlice);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<T, D, RG>, p);
+}
+
+template <typename T, int D>
+cudaError_t merge_rows(const TreeParams& p, cudaStream_t s) {
+  return p.Mt >= 64 ? merge<T, D, 4>(p, s) : merge<T, D, 1>(p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_context_mma(const TreeParams& p, int dtype, cudaStream_t s) {
+  if (dtype == SPLITKV_DTYPE_BF16)
+    return p.d == 128 ? context_rows<__nv_bfloat16, 128>(p, s) : context_rows<__nv_bfloat16, 64>(p, s);
+  return p.d == 128 ? context_rows<__half, 128>(p, s) : context_rows<__half, 64>(p, s);
+}
+
+cudaError_t launch_tree_merge(const TreeParams& p, int dtype, cudaStream_t s) {
+  if (dtype == SPLITKV_DTYPE_BF16)
+    return p.d == 128 ? merge_rows<__nv_bfloat16, 128>(p, s) : merge_rows<__nv_bfloat16, 64>(p, s);
+  return p.d == 128 ? merge_rows<__half, 128>(p, s) : merge_rows<__half, 64>(p, s);
+}
+
+}  // namespace tree
+}  // namespace splitkv
+
+// -------------------------------------------------------------------------------- C entries
+namespace {
+
+using splitkv::tree::TreeParams;
+
+struct TreeSizes {
+  int Mt, RT, ctas;
+  size_t units, ml_off, total;
+};
+
+int sm_count() {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  cudaGetLastError();
+  return sms;
+}
+
+int check_sizes(const splitkv_tree_args* a, TreeSizes* z) {
+  if (!a || a->num_seqs < 0 || a->num_nodes < 0 || a->max_nodes < 1 || a->num_kv_heads < 1 || a->num_q_heads < 1 ||
+      a->num_q_heads % a->num_kv_heads || a->num_pages < 0 || a->max_pages < 0)
+    return SPLITKV_ERR_INVALID_ARG;
+  if (a->page_size < 1 || a->page_size > 65536 || (a->page_size & (a->page_size - 1))) return SPLITKV_ERR_INVALID_ARG;
+  if (a->dtype != SPLITKV_DTYPE_BF16 && a->dtype != SPLITKV_DTYPE_F16) return SPLITKV_ERR_INVALID_ARG;
+  if (a->o_dtype != a->dtype && a->o_dtype != SPLITKV_DTYPE_F32) return SPLITKV_ERR_INVALID_ARG;
+  if (a->head_dim != 64 && a->head_dim != 128) return SPLITKV_ERR_UNSUPPORTED;
+  if (a->max_nodes > splitkv::tree::kMaxNodes || a->num_q_heads > 1024 || a->num_seqs > 65536)
+    return SPLITKV_ERR_UNSUPPORTED;
+  if (int64_t(a->max_pages) * a->page_size > 0x7fffffff - splitkv::tree::kTileKeys) return SPLITKV_ERR_UNSUPPORTED;
+  const int rows = a->num_q_heads / a->num_kv_heads * a->max_nodes;
+  z->Mt = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  z->RT = (rows + z->Mt - 1) / z->Mt;
+  z->units = size_t(a->num_seqs) * a->num_kv_heads * z->RT;
+  if (z->units > 0x1fffffff) return SPLITKV_ERR_UNSUPPORTED;
+  // two CTAs to an SM, and no more than the longest line has tiles
+  const size_t tiles = z->units * ((size_t(a->max_pages) * a->page_size + splitkv::tree::kTileKeys - 1) /
+                                   splitkv::tree::kTileKeys);
+  const size_t ctas = size_t(2) * sm_count();
+  z->ctas = int(tiles < ctas ? (tiles > 0 ? tiles : 1) : ctas);
+  const size_t recs = z->units + z->ctas;
+  z->ml_off = splitkv::align_up(recs * z->Mt * a->head_dim * sizeof(float), 256);
+  z->total = z->ml_off + splitkv::align_up(recs * z->Mt * sizeof(float2), 256);
+  return SPLITKV_OK;
+}
+
+// A row-strided 16-bit array read in 16-byte pieces.
+bool rows_ok(const void* ptr, int64_t s0, int64_t s1, int64_t s2 = 0) {
+  const int64_t kMax = int64_t(1) << 44;
+  return ptr && splitkv::ptr_aligned(ptr, 16) && s0 >= 0 && s1 >= 0 && s2 >= 0 && s0 < kMax && s1 < kMax &&
+         s2 < kMax && s0 % 8 == 0 && s1 % 8 == 0 && s2 % 8 == 0;
+}
+
+}  // namespace
+
+extern "C" int splitkv_tree_workspace_size(const splitkv_tree_args* args, size_t* bytes) {
+  if (!bytes) return SPLITKV_ERR_INVALID_ARG;
+  TreeSizes z;
+  const int st = check_sizes(args, &z);
+  if (st == SPLITKV_OK) *bytes = z.total;
+  return st;
+}
+
+extern "C" int splitkv_tree_attn(const splitkv_tree_args* a, void* ws, size_t ws_bytes, void* stream) {
+  TreeSizes z;
+  const int st = check_sizes(a, &z);
+  if (st != SPLITKV_OK) return st;
+  if (a->num_seqs == 0 || a->num_nodes == 0) return SPLITKV_OK;
+  if (!rows_ok(a->q, a->q_stride[0], a->q_stride[1]) || !rows_ok(a->kb, a->kb_stride[0], a->kb_stride[1]) ||
+      !rows_ok(a->vb, a->vb_stride[0], a->vb_stride[1]) || !splitkv::all_aligned16(a->o, ws) || !a->lse ||
+      !a->node_ptr || !a->context_lens || !splitkv::ptr_aligned(a->lse, 4))
+    return SPLITKV_ERR_INVALID_ARG;
+  if (a->mask && a->mask_stride < 0) return SPLITKV_ERR_INVALID_ARG;
+  if (a->max_pages > 0 && a->num_pages > 0 &&
+      (!rows_ok(a->k_cache, a->k_stride[0], a->k_stride[1], a->k_stride[2]) ||
+       !rows_ok(a->v_cache, a->v_stride[0], a->v_stride[1], a->v_stride[2]) || !a->page_table || a->table_stride < 0))
+    return SPLITKV_ERR_INVALID_ARG;
+  if (ws_bytes < z.total) return SPLITKV_ERR_WORKSPACE_TOO_SMALL;
+  TreeParams p;
+  p.q = static_cast<const char*>(a->q);
+  p.kb = static_cast<const char*>(a->kb);
+  p.vb = static_cast<const char*>(a->vb);
+  p.kc = static_cast<const char*>(a->k_cache);
+  p.vc = static_cast<const char*>(a->v_cache);
+  p.o = static_cast<char*>(a->o);
+  p.lse = a->lse;
+  p.mask = static_cast<const uint8_t*>(a->mask);
+  p.node_ptr = a->node_ptr;
+  p.lens = a->context_lens;
+  p.table = a->page_table;
+  p.status = a->status;
+  p.q_node = a->q_stride[0] * 2;
+  p.q_head = a->q_stride[1] * 2;
+  p.kb_node = a->kb_stride[0] * 2;
+  p.kb_head = a->kb_stride[1] * 2;
+  p.vb_node = a->vb_stride[0] * 2;
+  p.vb_head = a->vb_stride[1] * 2;
+  p.kc_page = a->k_stride[0] * 2;
+  p.kc_slot = a->k_stride[1] * 2;
+  p.kc_head = a->k_stride[2] * 2;
+  p.vc_page = a->v_stride[0] * 2;
+  p.vc_slot = a->v_stride[1] * 2;
+  p.vc_head = a->v_stride[2] * 2;
+  p.mask_row = a->mask_stride;
+  p.table_row = a->table_stride;
+  p.B = a->num_seqs;
+  p.Nq = a->num_nodes;
+  p.T = a->max_nodes;
+  p.Hq = a->num_q_heads;
+  p.Hkv = a->num_kv_heads;
+  p.G = a->num_q_heads / a->num_kv_heads;
+  p.d = a->head_dim;
+  p.Mt = z.Mt;
+  p.RT = z.RT;
+  p.page_shift = 0;
+  while ((1 << p.page_shift) < a->page_size) ++p.page_shift;
+  p.num_pages = a->num_pages;
+  p.max_pages = a->max_pages;
+  p.ctas = z.ctas;
+  p.o_f32 = a->o_dtype == SPLITKV_DTYPE_F32;
+  p.scale_log2 = a->scale * splitkv::kLog2e;
+  p.rec_o = static_cast<float*>(ws);
+  p.rec_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + z.ml_off);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = splitkv::tree::launch_tree_context_mma(p, a->dtype, s);
+  if (e == cudaSuccess) e = splitkv::tree::launch_tree_merge(p, a->dtype, s);
+  if (e == cudaSuccess) return SPLITKV_OK;
+  cudaGetLastError();
+  return SPLITKV_ERR_CUDA;
+}

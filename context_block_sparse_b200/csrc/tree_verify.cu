@@ -1,0 +1,414 @@
+// Verification of drafted tokens against the target's distributions, from given uniform
+// random numbers (speculative sampling over a tree; a chain is a tree of one child a node).
+//
+// The walk starts at node 0 of the sequence (the token that is already certain).  At node
+// `cur`, with p = target[cur] and q = draft[cur], its children x_1, x_2, ... (in node order)
+// were drawn from q independently.  Child k is accepted when
+//     u_k S_k q(x_k) < R_k(x_k),
+// where R_1 = p, S_1 = 1, and a rejection leaves the residual
+//     R_{k+1} = max(R_k - S_k q, 0),   S_{k+1} = sum R_{k+1}.
+// Since q >= 0 the clamps nest: R_k = max(p - c_k q, 0) with c_1 = 0, c_{k+1} = c_k + S_k, so a
+// node's residual is its two rows and one scalar, and nothing of vocabulary size is stored.
+// Without draft distributions a child stands for certainty (q is 1 at x_k): accepted when
+// u_k S_k < p(x_k), a rejection takes x_k out of p and S_{k+1} = S_k - p(x_k).
+// The walk ends at a node none of whose children is accepted; the next token is the first i
+// with R_1 + ... + R_i > u' sum R (R = p where the residual has no mass), so the accepted
+// tokens and it are distributed as the target's own samples.
+//
+// The outputs are whole numbers decided at borders, so sums and comparisons are float64 of
+// the given values, in a fixed order.
+//
+// HBM-bound for large batches: the two rows of the node where the walk ends, 2 V elements a
+// sequence; otherwise latency.  One cluster of CTAs takes a sequence: each prefetches all
+// children's p(x), q(x) at once (one round of gathers instead of one a level), walks in
+// shared memory, and sums its slice of the vocabulary; slice sums are exchanged through
+// distributed shared memory and read in rank order, so every CTA takes the same decisions.
+// Each warp keeps the sums of its 1024-element chunks: the search for the next token
+// re-reads one chunk (from L2).
+#include <cooperative_groups.h>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "splitkv.h"
+#include "splitkv_internal.h"
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kChunk = 1024;            // vocabulary entries of one warp step
+constexpr int kPerLane = kChunk / 32;
+constexpr int kMaxNodes = 1024;
+constexpr int kMaxChunks = 2048;        // chunks of one CTA's slice
+constexpr int kMaxCluster = 8;
+
+struct VerifyParams {
+  const void *target, *draft;
+  int64_t target_row, draft_row;   // row strides in elements
+  const void* tokens;
+  const int *parents, *node_ptr;
+  const float *u_accept, *u_sample;
+  int *path, *count;
+  void* next;
+  int* status;
+  int64_t path_row;
+  int Nq, V, max_nodes, max_path, tok64;
+  int chunks_per_cta;
+};
+
+__device__ __forceinline__ float val(float x) { return x; }
+__device__ __forceinline__ float val(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float val(__half x) { return __half2float(x); }
+
+// A probability as it counts: entries that are negative, infinite or NaN have no mass.
+template <typename T>
+__device__ __forceinline__ double mass(T x) {
+  const float f = val(x);
+  return f > 0.f && f < INFINITY ? double(f) : 0.0;
+}
+
+template <typename T, int N>
+struct alignas(sizeof(T) * N) Pack {
+  T v[N];
+};
+
+// The residual at the walk's current node.
+template <typename T>
+struct Residual {
+  const T* p;
+  const T* q;          // NULL: certainty drafts, `removed` tokens have no mass left
+  double c;
+  const int* removed;
+  int n_removed;
+  __device__ __forceinline__ double at(T pv, T qv, int i) const {
+    double r = mass(pv);
+    if (q != nullptr) {
+      r = fmax(r - c * mass(qv), 0.0);
+    } else {
+      for (int k = 0; k < n_removed; ++k)
+        if (removed[k] == i) r = 0.0;
+    }
+    return r;
+  }
+};
+
+// This lane's share of chunk [base, base + kChunk): N-element vectors, lane-interleaved.
+template <typename T, int N>
+__device__ __forceinline__ double chunk_sum(const Residual<T>& R, int base, int V, int lane) {
+  double s = 0.0;
+  constexpr int kBatch = 8;   // vectors of each row in flight
+#pragma unroll 1
+  for (int j0 = 0; j0 < kPerLane / N; j0 += kBatch) {
+    Pack<T, N> a[kBatch], b[kBatch];
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = base + ((j0 + j) * 32 + lane) * N;
+      if (j0 + j < kPerLane / N && i < V) {
+        a[j] = *reinterpret_cast<const Pack<T, N>*>(R.p + i);
+        if (R.q != nullptr && R.c != 0.0) b[j] = *reinterpret_cast<const Pack<T, N>*>(R.q + i);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = base + ((j0 + j) * 32 + lane) * N;
+      if (j0 + j < kPerLane / N && i < V) {
+        if (R.q != nullptr && R.c == 0.0) {
+#pragma unroll
+          for (int e = 0; e < N; ++e) s += mass(a[j].v[e]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < N; ++e) s += R.at(a[j].v[e], b[j].v[e], i + e);
+        }
+      }
+    }
+  }
+  return s;
+}
+
+__device__ __forceinline__ double warp_sum(double s) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
+}
+
+template <typename T, int N>
+__global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyParams p) {
+  cg::cluster_group cluster = cg::this_cluster();
+  const int rank = int(cluster.block_rank()), ranks = int(cluster.num_blocks());
+  const int b = int(blockIdx.x) / ranks;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  __shared__ int s_parent[kMaxNodes], s_tok[kMaxNodes], s_removed[kMaxNodes];
+  __shared__ float s_p[kMaxNodes], s_q[kMaxNodes], s_u[kMaxNodes];
+  __shared__ double s_chunk[kMaxChunks];
+  __shared__ double s_total[2];   // this CTA's slice sum, by pass parity
+  __shared__ int s_found;
+
+  const int n0 = p.node_ptr[b], n1 = p.node_ptr[b + 1];
+  int n = n1 - n0;
+  if (n0 < 0 || n1 < n0 || n1 > p.Nq || n > p.max_nodes) {
+    if (tid == 0 && p.status) atomicCAS(p.status, 0, SPLITKV_ERR_INVALID_ARG);
+    n = 0;
+  }
+  const T* target = static_cast<const T*>(p.target);
+  const T* draft = static_cast<const T*>(p.draft);
+  const int V = p.V;
+
+  for (int i = tid; i < n; i += kThreads) {
+    int64_t tok = p.tok64 ? static_cast<const int64_t*>(p.tokens)[n0 + i] : static_cast<const int*>(p.tokens)[n0 + i];
+    int par = p.parents[n0 + i];
+    if (i > 0 && (par < 0 || par >= i || tok < 0 || tok >= V)) {
+      // a node that no walk reaches
+      if (p.status) atomicCAS(p.status, 0, SPLITKV_ERR_INVALID_ARG);
+      par = -1;
+    }
+    float pv = 0.f, qv = 1.f;
+    if (i > 0 && par >= 0) {
+      pv = float(mass(target[int64_t(n0 + par) * p.target_row + tok]));
+      if (draft != nullptr) qv = float(mass(draft[int64_t(n0 + par) * p.draft_row + tok]));
+    }
+    s_parent[i] = par;
+    s_tok[i] = int(tok);
+    s_p[i] = pv;
+    s_q[i] = qv;
+    s_u[i] = p.u_accept[n0 + i];
+  }
+  if (tid == 0) s_found = -1;
+  __syncthreads();
+
+  Residual<T> R;
+  R.removed = s_removed;
+  R.p = target + int64_t(n0) * p.target_row;
+  R.q = draft ? draft + int64_t(n0) * p.draft_row : nullptr;
+  R.c = 0.0;
+  R.n_removed = 0;
+  const int c0 = rank * p.chunks_per_cta;   // this CTA's chunks
+  const int nc = max(0, min(p.chunks_per_cta, (V + kChunk - 1) / kChunk - c0));
+  int pass = 0;
+  double before = 0.0;   // mass of the slices before this CTA's
+
+  // Sum of R over the vocabulary; leaves the chunk sums and `before` behind.  Every CTA of the
+  // cluster calls it the same number of times.
+  auto total = [&]() -> double {
+    __syncthreads();   // the last pass's readers of s_chunk are done
+    for (int k = warp; k < nc; k += kWarps) {
+      const double s = warp_sum(chunk_sum<T, N>(R, (c0 + k) * kChunk, V, lane));
+      if (lane == 0) s_chunk[k] = s;
+    }
+    __syncthreads();
+    if (warp == 0) {
+      double s = 0.0;
+      for (int k = lane; k < nc; k += 32) s += s_chunk[k];
+      s = warp_sum(s);
+      if (lane == 0) s_total[pass & 1] = s;
+    }
+    cluster.sync();
+    double all = 0.0;
+    for (int r = 0; r < ranks; ++r) {
+      if (r == rank) before = all;
+      all += *cluster.map_shared_rank(&s_total[pass & 1], r);
+    }
+    ++pass;
+    return all;
+  };
+
+  int cur = 0, len = n > 0 ? 1 : 0;
+  double S = 1.0;
+  bool summed = false;   // the chunk sums are those of the current R
+  int* path = p.path + b * p.path_row;
+  const bool writer = rank == 0 && tid == 0;
+  if (rank == 0)
+    for (int i = tid; i < p.max_path; i += kThreads) path[i] = (i == 0 && n > 0) ? 0 : -1;
+  __syncthreads();
+  for (int i = 1; i < n && len < p.max_path; ++i) {
+    if (s_parent[i] != cur) continue;
+    const double pv = s_p[i], qv = s_q[i];
+    double r;
+    if (R.q != nullptr) {
+      r = fmax(pv - R.c * qv, 0.0);
+    } else {
+      r = pv;
+      for (int k = 0; k < R.n_removed; ++k)
+        if (s_removed[k] == s_tok[i]) r = 0.0;
+    }
+    if (double(s_u[i]) * S * qv < r) {
+      if (writer) path[len] = i;
+      ++len;
+      cur = i;
+      R.p = target + int64_t(n0 + i) * p.target_row;
+      if (R.q != nullptr) R.q = draft + int64_t(n0 + i) * p.draft_row;
+      R.c = 0.0;
+      R.n_removed = 0;
+      S = 1.0;
+      summed = false;
+    } else if (R.q != nullptr) {
+      R.c += S;
+      S = total();
+      summed = true;
+    } else {
+      __syncthreads();   // every thread has read the removed list
+      if (tid == 0) s_removed[R.n_removed] = s_tok[i];
+      __syncthreads();
+      ++R.n_removed;
+      S = fmax(S - r, 0.0);
+      summed = false;
+    }
+  }
+
+  // the next token
+  int next = -1;
+  if (n > 0) {
+    double all = summed ? S : total();
+    if (!(all > 0.0) && (R.c != 0.0 || R.n_removed > 0)) {   // nothing left: the target's own row
+      R.c = 0.0;
+      R.n_removed = 0;
+      all = total();
+    }
+    // the first entry whose running sum exceeds the goal; below the total, so one exists
+    double goal = double(p.u_sample[b]) * all;
+    goal = fmin(goal, all * (1.0 - 1.2e-16));
+    const double mine = *cluster.map_shared_rank(&s_total[(pass - 1) & 1], rank);
+    // the last CTA that starts at or below the goal among those with mass before it ends
+    bool here = all > 0.0 && mine > 0.0 && before <= goal && goal < before + mine;
+    if (here) {
+      double run = before;
+      int k = 0, last = -1;
+      double last_base = 0.0;
+      for (; k < nc; ++k) {
+        if (s_chunk[k] > 0.0) {
+          last = k;
+          last_base = run;
+        }
+        if (run + s_chunk[k] > goal) break;
+        run += s_chunk[k];
+      }
+      if (k == nc) {   // rounding: the slice's running sum stayed below; its last chunk with mass
+        k = last;
+        run = last_base;
+      }
+      if (warp == 0) {
+        const int base = (c0 + k) * kChunk;
+        int found = -1, last_pos = -1;
+        for (int j = 0; j < kPerLane && found < 0; ++j) {
+          const int i = base + j * 32 + lane;
+          double r = 0.0;
+          if (i < V) r = R.at(R.p[i], R.q != nullptr ? R.q[i] : R.p[i], i);
+          double inc = r;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const double y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+          }
+          const unsigned over = __ballot_sync(0xffffffffu, r > 0.0 && run + inc > goal);
+          const unsigned pos = __ballot_sync(0xffffffffu, r > 0.0);
+          if (over) found = base + j * 32 + __ffs(over) - 1;
+          if (pos) last_pos = base + j * 32 + 31 - __clz(pos);
+          run += __shfl_sync(0xffffffffu, inc, 31);
+        }
+        if (lane == 0) s_found = found >= 0 ? found : last_pos;
+      }
+    }
+    __syncthreads();
+    if (here) next = s_found;
+    if (here && tid == 0) {
+      if (p.tok64)
+        static_cast<int64_t*>(p.next)[b] = next;
+      else
+        static_cast<int*>(p.next)[b] = next;
+    }
+    if (writer && !(all > 0.0)) {
+      if (p.tok64)
+        static_cast<int64_t*>(p.next)[b] = -1;
+      else
+        static_cast<int*>(p.next)[b] = -1;
+    }
+  } else if (writer) {
+    if (p.tok64)
+      static_cast<int64_t*>(p.next)[b] = -1;
+    else
+      static_cast<int*>(p.next)[b] = -1;
+  }
+  if (writer) p.count[b] = len;
+  cluster.sync();   // no CTA leaves while another may read its sums
+}
+
+template <typename T, int N>
+cudaError_t launch(const VerifyParams& p, int B, int ranks, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(B * ranks));
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(ranks);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_verify_kernel<T, N>, p);
+}
+
+template <typename T>
+cudaError_t dispatch(const VerifyParams& p, int B, int ranks, cudaStream_t s) {
+  constexpr int N = 16 / int(sizeof(T));
+  // 16-byte loads need every row on a 16-byte boundary and whole vectors to its end
+  const bool vec = p.V % N == 0 && p.target_row % N == 0 && splitkv::ptr_aligned(p.target, 16) &&
+                   (!p.draft || (p.draft_row % N == 0 && splitkv::ptr_aligned(p.draft, 16)));
+  return vec ? launch<T, N>(p, B, ranks, s) : launch<T, 1>(p, B, ranks, s);
+}
+
+}  // namespace
+
+extern "C" int splitkv_tree_verify(const splitkv_verify_args* a, void* stream) {
+  if (!a) return SPLITKV_ERR_INVALID_ARG;
+  if (a->num_seqs < 0 || a->num_nodes < 0 || a->vocab < 1 || a->max_nodes < 1 || a->max_path < 1)
+    return SPLITKV_ERR_INVALID_ARG;
+  if (a->dtype != SPLITKV_DTYPE_F32 && a->dtype != SPLITKV_DTYPE_BF16 && a->dtype != SPLITKV_DTYPE_F16)
+    return SPLITKV_ERR_INVALID_ARG;
+  if (a->max_nodes > kMaxNodes || a->vocab > kMaxChunks * kChunk || a->num_seqs > (1 << 24))
+    return SPLITKV_ERR_UNSUPPORTED;
+  if (a->num_seqs == 0) return SPLITKV_OK;
+  const int es = a->dtype == SPLITKV_DTYPE_F32 ? 4 : 2;
+  if (!a->node_ptr || !a->path || !a->count || !a->next || !a->u_sample) return SPLITKV_ERR_INVALID_ARG;
+  if (a->num_nodes > 0 && (!a->target || !a->tokens || !a->parents || !a->u_accept)) return SPLITKV_ERR_INVALID_ARG;
+  if (!splitkv::ptr_aligned(a->target, es) || !splitkv::ptr_aligned(a->draft, es) || a->target_stride < 0 ||
+      a->draft_stride < 0 || a->target_stride > (int64_t(1) << 40) || a->draft_stride > (int64_t(1) << 40))
+    return SPLITKV_ERR_INVALID_ARG;
+  VerifyParams p;
+  p.target = a->target;
+  p.draft = a->draft;
+  p.target_row = a->target_stride;
+  p.draft_row = a->draft_stride;
+  p.tokens = a->tokens;
+  p.parents = a->parents;
+  p.node_ptr = a->node_ptr;
+  p.u_accept = a->u_accept;
+  p.u_sample = a->u_sample;
+  p.path = a->path;
+  p.count = a->count;
+  p.next = a->next;
+  p.status = a->status;
+  p.path_row = a->path_stride;
+  p.Nq = a->num_nodes;
+  p.V = a->vocab;
+  p.max_nodes = a->max_nodes;
+  p.max_path = a->max_path;
+  p.tok64 = a->token_int64 ? 1 : 0;
+  // CTAs of a sequence: enough that the batch covers the SMs a few times, not so many that a
+  // CTA has less than four chunks (a cluster of one skips no work, only spreads less).
+  const int chunks = (a->vocab + kChunk - 1) / kChunk;
+  int ranks = 1;
+  while (ranks < kMaxCluster && int64_t(a->num_seqs) * ranks < 592 && chunks >= ranks * 2 * 4) ranks *= 2;
+  p.chunks_per_cta = (chunks + ranks - 1) / ranks;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = a->dtype == SPLITKV_DTYPE_F32    ? dispatch<float>(p, a->num_seqs, ranks, s)
+                  : a->dtype == SPLITKV_DTYPE_BF16 ? dispatch<__nv_bfloat16>(p, a->num_seqs, ranks, s)
+                                                   : dispatch<__half>(p, a->num_seqs, ranks, s);
+  if (e == cudaSuccess) return SPLITKV_OK;
+  cudaGetLastError();
+  return SPLITKV_ERR_CUDA;
+}

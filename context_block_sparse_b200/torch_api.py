@@ -2,13 +2,14 @@
 
 Allocates the outputs and workspaces with torch (device memory only) and calls
 splitkv_attn_fwd / splitkv_merge / splitkv_attn_bwd in order on the current
-stream.  No arithmetic happens here.
+stream, with the rotary call around them when a Rotary is given.  No arithmetic happens here.
 """
 
 from __future__ import annotations
 
 from typing import Optional
 
+import numpy as np
 import torch
 
 from . import (
@@ -25,13 +26,16 @@ class SplitKVAttention:
                  num_bwd_workers: int = 0, q_slice: int = 0, equal_count: bool = False,
                  device: Optional[torch.device] = None, block_keys_in_context: bool = False,
                  partial_bf16: bool = False, tile_cost: bool = False, fwd_tile_cost: bool = False,
-                 dynamic_claim: bool = False, contiguous_schedule: bool = False):
+                 dynamic_claim: bool = False, contiguous_schedule: bool = False, rotary=None):
         """block_keys_in_context: reading B of the block keys (the block's own tokens are
         the context positions after its anchor); kb, vb are then unused (pass None)
         and backward() returns no dkb, dvb.  partial_bf16: bf16 partial records.
         tile_cost / fwd_tile_cost: backward / forward LPT items costed by executed tile work.
         dynamic_claim: the CTAs claim the items in LPT order at run time.
-        contiguous_schedule: the contiguous baseline schedule instead of LPT."""
+        contiguous_schedule: the contiguous baseline schedule instead of LPT.
+        rotary: a Rotary applied to q, k and kb inside forward and backward (which take and differentiate the
+        unrotated ones): a context token's position is its offset in its sample, row r of block b's is its
+        anchor's offset + r (the context positions the block's tokens stand for)."""
         self.device = torch.device("cuda") if device is None else torch.device(device)
         if num_workers is None:
             num_workers = torch.cuda.get_device_properties(self.device).multi_processor_count
@@ -47,6 +51,16 @@ class SplitKVAttention:
         self.head_dim = head_dim
         self.ws_fwd = torch.empty(splitkv_workspace_size(self.plan, WS_FWD), dtype=torch.uint8, device=self.device)
         self._ws_bwd = None
+        self.rotary = rotary
+        if rotary is not None:
+            if rotary.head_dim != head_dim:
+                raise ValueError(f"rotary is for heads of {rotary.head_dim}, not {head_dim}")
+            lens, anc = np.asarray(sample_lens, dtype=np.int64), np.asarray(anchors, dtype=np.int64)
+            starts = np.concatenate([[0], np.cumsum(lens)])
+            ctx = np.arange(starts[-1]) - np.repeat(starts[:-1], lens)
+            rows = (anc - starts[np.searchsorted(starts, anc, side="right") - 1])[:, None] + np.arange(block_size)
+            self._ctx_pos, self._row_pos = (torch.from_numpy(x.astype(np.int32).ravel()).to(self.device)
+                                            for x in (ctx, rows))
         self._grad32 = None   # float32 gradients behind bf16 ones (grad_dtype=torch.bfloat16)
 
     def ws_bwd(self) -> torch.Tensor:
@@ -55,8 +69,19 @@ class SplitKVAttention:
                                        device=self.device)
         return self._ws_bwd
 
+    def _rotated(self, q, k, kb):
+        """q, k, kb as the attention takes them (the rotated ones are this call's own)."""
+        if self.rotary is None:
+            return q, k, kb
+        if kb is None:
+            q = self.rotary.forward(self._row_pos, q)
+        else:
+            q, kb = self.rotary.forward(self._row_pos, q, kb)
+        return q, self.rotary.forward(self._ctx_pos, k), kb
+
     def forward(self, q, k, v, kb, vb, scale: float, out_dtype=torch.float32, o=None, lse=None):
         Nq = q.shape[0]
+        q, k, kb = self._rotated(q, k, kb)
         if o is None:
             o = torch.empty((Nq, self.num_q_heads, self.head_dim), dtype=out_dtype, device=q.device)
         if lse is None:
@@ -89,8 +114,13 @@ class SplitKVAttention:
             if self._grad32 is None or self._grad32["dq"].shape != q.shape or self._grad32["dk"].shape != k.shape:
                 self._grad32 = self._grad_buffers(q, k, v, kb, vb, torch.float32)
             g32 = self._grad32
+        q, k, kb = self._rotated(q, k, kb)
         splitkv_attn_bwd(self.plan, q, k, v, kb, vb, o, lse, dout, g32["dq"], g32["dk"], g32["dv"],
                          g32["dkb"], g32["dvb"], scale, self.ws_bwd())
+        if self.rotary is not None:   # gradients of the unrotated q, k, kb, in place
+            dq, dk, dkb = g32["dq"], g32["dk"], g32["dkb"]
+            self.rotary.backward(self._row_pos, dq, dkb, out=(dq, dkb))
+            self.rotary.backward(self._ctx_pos, dk, out=(dk,))
         if grad_dtype == torch.bfloat16:
             for n, t in grads.items():
                 if t is not None:

@@ -141,6 +141,7 @@ extern "C" {
 /* ---- dtype codes (o) ------------------------------------------------------- */
 #define SPLITKV_DTYPE_F32   0
 #define SPLITKV_DTYPE_BF16  1
+#define SPLITKV_DTYPE_F16   2   /* rotary and draft-tree calls only */
 
 /* ---- workspace kinds --------------------------------------------------------- */
 #define SPLITKV_WS_FWD  0
@@ -518,6 +519,163 @@ int splitkv_selftest_wait_timeout(int32_t* status_out, void* stream);
  * WORKSPACE_TOO_SMALL (capacity below the worker count), CUDA. */
 int splitkv_read_cta_times(const splitkv_plan_t* plan, int which, int64_t* out_ns,
                            int64_t capacity, void* stream);
+
+/* ---- rotary positions ------------------------------------------------------------ */
+#define SPLITKV_ROPE_INTERLEAVED  1u  /* pairs (2i, 2i + 1) instead of (i, i + rotary_dim / 2)  */
+#define SPLITKV_ROPE_ADJOINT      2u  /* the transpose (backward pass): turns by the negative angle */
+#define SPLITKV_ROPE_POS64        4u  /* positions are int64 instead of int32                      */
+
+#define SPLITKV_ROPE_SCALE_NONE    0
+#define SPLITKV_ROPE_SCALE_LINEAR  1  /* w_i / factor (positions interpolated)                     */
+#define SPLITKV_ROPE_SCALE_BASE    2  /* base * factor^(r / (r - 2)): the slowest pair stretched by
+                                         factor, the fastest kept                                  */
+#define SPLITKV_ROPE_SCALE_PARTS   3  /* by parts: pairs that turn at least turns_high times over
+                                         original_len positions are kept, those below turns_low
+                                         divided by factor, linear in the turns between; the rotated
+                                         vectors are multiplied by 0.1 ln(factor) + 1               */
+
+/* One rotary call.  HOST struct, read during the call; q and k share positions, dtype and head
+ * size, and either may have 0 heads.  Strides are in elements, {token, head}; the last dimension is
+ * contiguous.  An output is its input itself (same pointer and strides: in place) or memory apart
+ * from every input. */
+typedef struct splitkv_rope_args {
+  int64_t       num_tokens;
+  int32_t       q_heads, k_heads;
+  int32_t       head_dim;
+  int32_t       rotary_dim;       /* even, 2 <= rotary_dim <= head_dim; the rest passes through     */
+  int32_t       dtype;            /* SPLITKV_DTYPE_F32, _BF16 or _F16, of q, k and the outputs      */
+  uint32_t      flags;            /* SPLITKV_ROPE_*                                                 */
+  double        scale;            /* factor on the rotated elements                                 */
+  const void*   positions;        /* device [num_tokens], any values                                */
+  const double* freqs;            /* device [rotary_dim / 2], radians per position                  */
+  const void*   q;
+  void*         q_out;
+  const void*   k;
+  void*         k_out;
+  int64_t       q_stride[2], q_out_stride[2], k_stride[2], k_out_stride[2];
+} splitkv_rope_args;
+
+/* Frequencies w_i = base^(-2i / rotary_dim), i < rotary_dim / 2, under a long-context scaling
+ * (SPLITKV_ROPE_SCALE_*; original_len, turns_low and turns_high are read by PARTS only), and the
+ * factor `scale` of the rotated vectors.  Host only.  Errors: INVALID_ARG. */
+int splitkv_rope_freqs(int32_t rotary_dim, double base, int scaling, double factor, double original_len,
+                       double turns_low, double turns_high, double* freqs, double* scale);
+
+/* Rotary positions on queries and keys in one launch: every pair (a, b) of the first rotary_dim
+ * elements of a head becomes scale (a cos t - b sin t, b cos t + a sin t), t = position * w_i (formed
+ * and reduced in float64); float32 arithmetic, one rounding.  SPLITKV_ROPE_ADJOINT is the backward
+ * pass.  Errors: INVALID_ARG, UNSUPPORTED (grid beyond the device's limits), CUDA. */
+int splitkv_rope(const splitkv_rope_args* args, void* stream);
+
+/* ---- draft trees over a paged cache -------------------------------------------------
+ * Speculative decoding: a trained drafter proposes a tree of tokens behind each sequence, the
+ * target's attention runs over the tree and the cached context (splitkv_tree_attn), the target's
+ * distributions decide which nodes stay (splitkv_tree_verify), and their keys and values join the
+ * cache (splitkv_tree_commit).
+ *
+ * Nodes are packed: sequence b owns rows [node_ptr[b], node_ptr[b + 1]) of every per-node array;
+ * rows behind the last sequence are neither read nor written.  Node numbers inside a sequence are
+ * local.  The cache holds pages of page_size tokens (a power of two); token t of sequence b is slot
+ * t % page_size of page page_table[b][t / page_size].
+ *
+ * node_ptr, context_lens, page_table, paths and counts live on the DEVICE and are not read by the
+ * host (a captured graph may replay with new values).  The kernels check them: what lies outside
+ * its array counts as absent -- a sequence with a bad node_ptr or more than max_nodes nodes has no
+ * nodes, a bad context length is clamped, a key on a bad page does not exist, a path row that is no
+ * node or has no page is not written -- and SPLITKV_ERR_INVALID_ARG is recorded in *status (device
+ * int32, may be NULL; the caller clears it). */
+typedef struct splitkv_tree_args {
+  int32_t        num_seqs;        /* B <= 65536                                                   */
+  int32_t        num_nodes;       /* rows of q, kb, vb, mask, o, lse                              */
+  int32_t        max_nodes;       /* bound on a sequence's nodes, <= 256                          */
+  int32_t        num_q_heads, num_kv_heads, head_dim;   /* Hq a multiple of Hkv; d 64 or 128        */
+  int32_t        dtype;           /* SPLITKV_DTYPE_BF16 or _F16: q, kb, vb and the cache           */
+  int32_t        o_dtype;         /* dtype, or SPLITKV_DTYPE_F32                                   */
+  int32_t        page_size, num_pages;
+  int32_t        max_pages;       /* entries of a page-table row                                  */
+  float          scale;
+  const void     *q, *kb, *vb;    /* [num_nodes][heads][d]                                         */
+  const void     *k_cache, *v_cache;   /* [num_pages][page_size][Hkv][d]                            */
+  const void*    mask;            /* uint8 [num_nodes][>= max_nodes]: nonzero where the row's node sees
+                                     the local node of the column; NULL: every node of its sequence */
+  const int32_t  *node_ptr, *context_lens, *page_table;   /* [B + 1], [B], [B][max_pages]            */
+  void*          o;               /* [num_nodes][Hq][d], contiguous                                */
+  float*         lse;             /* [num_nodes][Hq], natural log, contiguous                      */
+  int32_t*       status;
+  /* strides in elements (multiples of 8 for the 16-bit arrays): {node, head} and {page, slot, head} */
+  int64_t        q_stride[2], kb_stride[2], vb_stride[2], k_stride[3], v_stride[3];
+  int64_t        mask_stride, table_stride;
+} splitkv_tree_args;
+
+/* Bytes of workspace of splitkv_tree_attn for these sizes (host only; the pointers are not read).
+ * Errors: INVALID_ARG, UNSUPPORTED. */
+int splitkv_tree_workspace_size(const splitkv_tree_args* args, size_t* bytes);
+
+/* Attention of every node (row) and query head over its sequence's cached context and the nodes of
+ * its own tree that it sees:
+ *   s_j = scale q.k_j, o = sum exp(s_j - m) v_j / l, l = sum exp(s_j - m), lse = m + log l.
+ * A row that sees no key gets o = 0, lse = -inf; values that a row does not see never reach it,
+ * infinities and NaN among them.  Two launches; the workspace is written and read inside the call
+ * and may be used again by the next call on the stream, not by a concurrent one.  Deterministic.
+ * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, CUDA. */
+int splitkv_tree_attn(const splitkv_tree_args* args, void* ws, size_t ws_bytes, void* stream);
+
+typedef struct splitkv_verify_args {
+  int32_t        num_seqs, num_nodes;
+  int32_t        max_nodes;       /* bound on a sequence's nodes, <= 1024                         */
+  int32_t        vocab;           /* <= 2^21                                                      */
+  int32_t        dtype;           /* SPLITKV_DTYPE_F32, _BF16 or _F16 of target and draft          */
+  int32_t        token_int64;     /* tokens and next are int64 (else int32)                        */
+  int32_t        max_path;        /* columns of path: the walk ends at that many nodes             */
+  int32_t        reserved;
+  const void*    target;          /* [num_nodes][vocab]: the target's distribution after each node  */
+  const void*    draft;           /* [num_nodes][vocab]: what the node's children were drawn from;
+                                     NULL: children were proposed with certainty                    */
+  const void*    tokens;          /* [num_nodes]                                                   */
+  const int32_t  *parents, *node_ptr;   /* [num_nodes] local, smaller than the node; [B + 1]         */
+  const float    *u_accept, *u_sample;  /* [num_nodes], [B]: uniform in [0, 1)                       */
+  int32_t        *path, *count;   /* [B][max_path] local nodes, -1 behind them; [B]                 */
+  void*          next;            /* [B]                                                           */
+  int32_t*       status;
+  int64_t        target_stride, draft_stride, path_stride;   /* rows, in elements                  */
+} splitkv_verify_args;
+
+/* Verification of drafted tokens.  The walk starts at local node 0 (the last certain token); at a
+ * node with target row p and draft row q its children x_1, x_2, ... are tried in node order: child k
+ * is accepted when u_accept S_k q(x_k) < R_k(x_k), where R_1 = p, S_1 = 1, and a rejection leaves
+ * R_{k+1} = max(R_k - S_k q, 0), S_{k+1} = sum R_{k+1} (certainty drafts: q(x_k) = 1, x_k leaves R and
+ * S_{k+1} = S_k - p(x_k)).  Where no child is accepted (or max_path nodes are), the next token is the
+ * first i with R_1 + ... + R_i > u_sample sum R; R = p where the residual has no mass.  path lists the
+ * accepted nodes from node 0 on, count how many.  With u_* uniform, the accepted tokens and the next
+ * one are distributed as the target's own samples.  Sums and comparisons are float64; entries that are
+ * negative, infinite or NaN have no mass; rows are taken as normalised.  next is -1 for a sequence
+ * without nodes or whose row has no mass.  A node whose parent is not an earlier node, or whose token
+ * is outside the vocabulary, is never reached, and INVALID_ARG is recorded.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int splitkv_tree_verify(const splitkv_verify_args* args, void* stream);
+
+typedef struct splitkv_commit_args {
+  int32_t        num_layers;      /* caches written by the call (1 for a single one)              */
+  int32_t        num_seqs, num_nodes;
+  int32_t        max_rows;        /* bound on count (columns of path), or on a sequence's nodes    */
+  int32_t        num_kv_heads, head_dim;
+  int32_t        elem_bytes;      /* 1, 2 or 4; head_dim * elem_bytes a multiple of 16              */
+  int32_t        page_size, num_pages, max_pages;
+  const void     *kb, *vb;        /* [layers][num_nodes][Hkv][d]                                    */
+  void           *k_cache, *v_cache;   /* [layers][num_pages][page_size][Hkv][d]                     */
+  const int32_t  *path, *count;   /* [B][max_rows], [B]; path NULL: every node, in order             */
+  const int32_t  *node_ptr, *context_lens, *page_table;
+  int32_t*       status;
+  /* strides in elements (16-byte multiples): {layer, node, head} and {layer, page, slot, head} */
+  int64_t        kb_stride[3], vb_stride[3], k_stride[4], v_stride[4];
+  int64_t        path_stride, table_stride;
+} splitkv_commit_args;
+
+/* Copy row path[b][i] (i < count[b]) of sequence b's new keys and values to cache token
+ * context_lens[b] + i, in every layer.  context_lens is not advanced (one sequence state serves all
+ * layers): the caller adds count once.  Sequences must not share the pages they write.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
+int splitkv_tree_commit(const splitkv_commit_args* args, void* stream);
 
 #ifdef __cplusplus
 }  /* extern "C" */
