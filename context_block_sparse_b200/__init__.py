@@ -473,227 +473,6 @@ def splitkv_cast_bf16(src, dst, stream=None) -> None:
     _check("splitkv_cast_bf16", _lib.splitkv_cast_bf16(int(src.numel()), _ptr(src), _ptr(dst), _stream_ptr(stream)))
 
 
-# ---------------------------------------------------------------- rotary positions, draft trees
-# These calls take strided tensors: the last dimension is contiguous, the others have any stride
-# (in 16-byte steps where the header says so).  They run on the tensors' device and on its current
-# stream.
-
-_DTYPES = {}
-
-
-def _dtype_code(t, name: str) -> int:
-    if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.float32: DTYPE_F32, torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_F16})
-    code = _DTYPES.get(t.dtype)
-    if code is None:
-        raise ValueError(f"{name} must be float32, bfloat16 or float16")
-    return code
-
-
-def _strided(t, name: str, shape, dtype, dev: int):
-    """Address and strides of a tensor of that shape, type and device (None in shape: any size)."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name} must be a CUDA tensor on the device of the others")
-    got = t.shape
-    if len(got) != len(shape) or any(w is not None and w != g for g, w in zip(got, shape)):
-        raise ValueError(f"{name} has shape {tuple(got)}; expected {tuple(shape)} (None: any)")
-    st = t.stride()
-    if shape and st[-1] != 1 and got[-1] > 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
-    return t.data_ptr(), st
-
-
-def _dense(t, name: str, shape, dtype, dev: int) -> int:
-    """Address of a contiguous tensor of that shape, type and device."""
-    ptr, _ = _strided(t, name, shape, dtype, dev)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return ptr
-
-
-def _device_of(t, name: str) -> int:
-    dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return dev
-
-
-def _call(fn: str, dev: int, *args) -> None:
-    """The entry point with `args` and device dev's current stream, dev being the current device."""
-    import torch
-    stream = torch.cuda.current_stream(dev).cuda_stream
-    if torch.cuda.current_device() == dev:
-        status = getattr(_lib, fn)(*args, stream)
-    else:
-        with torch.cuda.device(dev):
-            status = getattr(_lib, fn)(*args, stream)
-    if status != _abi.OK:
-        raise SplitKVError(fn, status)
-
-
-def _status_ptr(status, dev: int):
-    if status is None:
-        return None
-    import torch
-    return _dense(status, "status", (1,), torch.int32, dev)
-
-
-def splitkv_rope_freqs(rotary_dim: int, base: float = 10000.0, scaling: int = ROPE_SCALE_NONE, factor: float = 1.0,
-                       original_len: float = 0.0, turns_low: float = 1.0, turns_high: float = 32.0):
-    """Frequencies (radians per position, float64 [rotary_dim / 2]) and the factor on rotated vectors."""
-    out = np.zeros(max(0, int(rotary_dim)) // 2, dtype=np.float64)
-    scale = ctypes.c_double()
-    _check("splitkv_rope_freqs", _lib.splitkv_rope_freqs(
-        int(rotary_dim), float(base), int(scaling), float(factor), float(original_len), float(turns_low),
-        float(turns_high), out.ctypes.data_as(ctypes.POINTER(ctypes.c_double)), ctypes.byref(scale)))
-    return out, scale.value
-
-
-def splitkv_rope(positions, freqs, scale: float, q, k, q_out, k_out, interleaved: bool = False,
-                 adjoint: bool = False) -> None:
-    """q_out, k_out = the rotary positions (adjoint: their transpose) of q [n, Hq, d] and k [n, Hk, d]
-    (k and k_out may be None) at positions [n] (int32 or int64); rotary_dim = 2 * freqs.numel()."""
-    import torch
-    dev = _device_of(q, "q")
-    code = _dtype_code(q, "q")
-    n, hq, d = q.shape
-    dt = q.dtype
-    pos64 = positions.dtype == torch.int64
-    ppos = _dense(positions, "positions", (n,), torch.int64 if pos64 else torch.int32, dev)
-    pf = _dense(freqs, "freqs", (None,), torch.float64, dev)
-    pq, sq = _strided(q, "q", (n, hq, d), dt, dev)
-    pqo, sqo = _strided(q_out, "q_out", (n, hq, d), dt, dev)
-    hk, pk, pko, sk, sko = 0, None, None, (0, 0), (0, 0)
-    if k is not None:
-        hk = k.shape[1]
-        pk, sk = _strided(k, "k", (n, hk, d), dt, dev)
-        pko, sko = _strided(k_out, "k_out", (n, hk, d), dt, dev)
-    flags = (ROPE_INTERLEAVED if interleaved else 0) | (ROPE_ADJOINT if adjoint else 0) | (ROPE_POS64 if pos64 else 0)
-    args = _abi.RopeArgs(n, hq, hk, d, 2 * freqs.numel(), code, flags, scale, ppos, pf, pq, pqo, pk, pko,
-                         sq[:2], sqo[:2], sk[:2], sko[:2])
-    _call("splitkv_rope", dev, ctypes.byref(args))
-
-
-def splitkv_tree_args(q, kb, vb, node_ptr, mask, k_cache, v_cache, page_table, context_lens, scale: float,
-                      max_nodes: int, o, lse, status=None):
-    """The checked arguments of splitkv_tree_attn (shapes as in the header), and their device."""
-    import torch
-    i32 = torch.int32
-    dev = _device_of(q, "q")
-    code = _dtype_code(q, "q")
-    dt = q.dtype
-    if q.dim() != 3 or k_cache.dim() != 4 or page_table.dim() != 2:
-        raise ValueError("q is [nodes, heads, d], the caches [pages, page_size, heads, d], page_table [seqs, pages]")
-    nq, hq, d = q.shape
-    pages, page, hkv, _ = k_cache.shape
-    B, max_pages = page_table.shape
-    pq, sq = _strided(q, "q", (nq, hq, d), dt, dev)
-    pkb, skb = _strided(kb, "kb", (nq, hkv, d), dt, dev)
-    pvb, svb = _strided(vb, "vb", (nq, hkv, d), dt, dev)
-    pk, sk = _strided(k_cache, "k_cache", (pages, page, hkv, d), dt, dev)
-    pv, sv = _strided(v_cache, "v_cache", (pages, page, hkv, d), dt, dev)
-    ptab, stab = _strided(page_table, "page_table", (B, max_pages), i32, dev)
-    pptr = _dense(node_ptr, "node_ptr", (B + 1,), i32, dev)
-    plen = _dense(context_lens, "context_lens", (B,), i32, dev)
-    pm, sm = None, 0
-    if mask is not None:
-        if mask.dtype != torch.bool and mask.dtype != torch.uint8:
-            raise ValueError("mask must be bool or uint8")
-        pm, st = _strided(mask, "mask", (nq, None), mask.dtype, dev)
-        if mask.shape[1] < max_nodes:
-            raise ValueError(f"mask has {mask.shape[1]} columns; max_nodes is {max_nodes}")
-        sm = st[0]
-    o_code = code if o.dtype == dt else DTYPE_F32
-    po = _dense(o, "o", (nq, hq, d), dt if o_code == code else torch.float32, dev)
-    pl = _dense(lse, "lse", (nq, hq), torch.float32, dev)
-    return _abi.TreeArgs(B, nq, max_nodes, hq, hkv, d, code, o_code, page, pages, max_pages, scale, pq, pkb, pvb, pk,
-                         pv, pm, pptr, plen, ptab, po, pl, _status_ptr(status, dev), sq[:2], skb[:2], svb[:2], sk[:3],
-                         sv[:3], sm, stab[0]), dev
-
-
-def splitkv_tree_workspace_size(args, dev: int) -> int:
-    """Workspace bytes of splitkv_tree_attn for splitkv_tree_args' sizes on device dev."""
-    import torch
-    out = ctypes.c_size_t()
-    if torch.cuda.is_available() and torch.cuda.current_device() != dev:
-        with torch.cuda.device(dev):
-            status = _lib.splitkv_tree_workspace_size(ctypes.byref(args), ctypes.byref(out))
-    else:
-        status = _lib.splitkv_tree_workspace_size(ctypes.byref(args), ctypes.byref(out))
-    _check("splitkv_tree_workspace_size", status)
-    return out.value
-
-
-def splitkv_tree_attn(args, ws, dev: int) -> None:
-    """Attention of draft trees over the cache (args, dev from splitkv_tree_args)."""
-    if ws.get_device() != dev or not ws.is_contiguous():
-        raise ValueError("ws must be a contiguous CUDA tensor on the device of the others")
-    _call("splitkv_tree_attn", dev, ctypes.byref(args), ws.data_ptr(), ws.numel() * ws.element_size())
-
-
-def splitkv_tree_verify(target, draft, tokens, parents, node_ptr, u_accept, u_sample, max_nodes: int, path, count,
-                        next_token, status=None) -> None:
-    """path, count, next_token = the verification of the drafted tokens (see the header)."""
-    import torch
-    i32, f32 = torch.int32, torch.float32
-    dev = _device_of(target, "target")
-    code = _dtype_code(target, "target")
-    if target.dim() != 2 or path.dim() != 2:
-        raise ValueError("target is [nodes, vocab], path [seqs, max_path]")
-    nq, vocab = target.shape
-    B = path.shape[0]
-    pt, st = _strided(target, "target", (nq, vocab), target.dtype, dev)
-    pd, sd = (None, (0, 1)) if draft is None else _strided(draft, "draft", (nq, vocab), target.dtype, dev)
-    tok = tokens.dtype
-    if tok != i32 and tok != torch.int64:
-        raise ValueError("tokens must be int32 or int64")
-    args = _abi.VerifyArgs(
-        B, nq, max_nodes, vocab, code, tok == torch.int64, path.shape[1], 0, pt, pd,
-        _dense(tokens, "tokens", (nq,), tok, dev), _dense(parents, "parents", (nq,), i32, dev),
-        _dense(node_ptr, "node_ptr", (B + 1,), i32, dev), _dense(u_accept, "u_accept", (nq,), f32, dev),
-        _dense(u_sample, "u_sample", (B,), f32, dev), _dense(path, "path", (B, None), i32, dev),
-        _dense(count, "count", (B,), i32, dev), _dense(next_token, "next_token", (B,), tok, dev),
-        _status_ptr(status, dev), st[0], sd[0], path.shape[1])
-    _call("splitkv_tree_verify", dev, ctypes.byref(args))
-
-
-def splitkv_tree_commit(k_cache, v_cache, page_table, context_lens, kb, vb, node_ptr, path, count, max_rows: int,
-                        status=None) -> None:
-    """Copy the path's rows of kb, vb ([layers, nodes, heads, d]) behind each sequence's context in the
-    caches ([layers, pages, page_size, heads, d]); path None: every node, in order."""
-    import torch
-    i32 = torch.int32
-    dev = _device_of(k_cache, "k_cache")
-    if k_cache.dim() != 5 or page_table.dim() != 2:
-        raise ValueError("the caches are [layers, pages, page_size, heads, d], page_table [seqs, pages]")
-    dt = k_cache.dtype
-    layers, pages, page, hkv, d = k_cache.shape
-    nq = kb.shape[1]
-    B, max_pages = page_table.shape
-    pk, sk = _strided(k_cache, "k_cache", k_cache.shape, dt, dev)
-    pv, sv = _strided(v_cache, "v_cache", k_cache.shape, dt, dev)
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if any(n > 1 and s == 0 for n, s in zip(t.shape, t.stride())):
-            raise ValueError(f"{name} is written: its elements must not share memory")
-    pkb, skb = _strided(kb, "kb", (layers, nq, hkv, d), dt, dev)
-    pvb, svb = _strided(vb, "vb", (layers, nq, hkv, d), dt, dev)
-    ptab, stab = _strided(page_table, "page_table", (B, max_pages), i32, dev)
-    ppath, spath, pcount = None, 0, None
-    if path is not None:
-        ppath, st = _strided(path, "path", (B, None), i32, dev)
-        if path.shape[1] < max_rows:
-            raise ValueError(f"path has {path.shape[1]} columns; max_rows is {max_rows}")
-        spath, pcount = st[0], _dense(count, "count", (B,), i32, dev)
-    args = _abi.CommitArgs(
-        layers, B, nq, max_rows, hkv, d, k_cache.element_size(), page, pages, max_pages, pkb, pvb, pk, pv, ppath, pcount,
-        _dense(node_ptr, "node_ptr", (B + 1,), i32, dev), _dense(context_lens, "context_lens", (B,), i32, dev), ptab,
-        _status_ptr(status, dev), skb[:3], svb[:3], sk[:4], sv[:4], spath, stab[0])
-    _call("splitkv_tree_commit", dev, ctypes.byref(args))
-
-
 def splitkv_selftest_wait_timeout(stream=None):
     """Run the bounded-wait self-test; returns the status words (code, site) it recorded."""
     out = (ctypes.c_int32 * 2)()
@@ -703,3 +482,15 @@ def splitkv_selftest_wait_timeout(stream=None):
 
 def library_path() -> str:
     return _abi.LIB_PATH
+
+
+# The rotary and draft-tree entry points are bound in draft_calls.py, which needs torch at import.
+_DRAFT_CALLS = ("splitkv_rope_freqs", "splitkv_rope", "splitkv_tree_workspace_size", "splitkv_tree_attn",
+                "splitkv_tree_verify", "splitkv_tree_commit")
+
+
+def __getattr__(name):
+    if name in _DRAFT_CALLS:
+        from . import draft_calls
+        return getattr(draft_calls, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -43,6 +43,25 @@ bool make_bf16_map_3d(void* map, const void* base, uint64_t dim0, uint64_t dim1,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_page_map_4d(void* map, const void* base, bool f16, uint64_t d, uint64_t heads, uint64_t slots, uint64_t pages,
+                      int64_t head_bytes, int64_t slot_bytes, int64_t page_bytes, uint32_t box_slots) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  // the stride of a dimension of one is never used, but has to be a valid one
+  const cuuint64_t hs = heads > 1 ? head_bytes : d * 2, ss = slots > 1 ? slot_bytes : d * 2,
+                   ps = pages > 1 ? page_bytes : d * 2;
+  const cuuint64_t kMax = cuuint64_t(1) << 40;
+  if (hs == 0 || ss == 0 || ps == 0 || hs >= kMax || ss >= kMax || ps >= kMax) return false;
+  const cuuint64_t dims[4] = {d, heads, slots, pages};
+  const cuuint64_t strides[3] = {hs, ss, ps};
+  const cuuint32_t box[4] = {64, 1, box_slots, 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(static_cast<CUtensorMap*>(map), f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_bf16_store_map_3d(void* map, void* base, uint64_t dim0, uint64_t dim1, uint64_t dim2, uint32_t box1,
                             uint32_t box2) {
   EncodeTiledFn fn = encode_fn();

@@ -3,7 +3,7 @@
 //
 // A unit is one (sequence, KV head, row tile): up to Mt rows (node-major, the G query heads
 // of a node next to each other) against the sequence's whole context.  The units' key tiles
-// of kTileKeys keys lie on one line, in (sequence, KV head, row tile, key tile) order, and
+// of tile_keys keys lie on one line, in (sequence, KV head, row tile, key tile) order, and
 // CTA c of C takes the stretch [c W / C, (c + 1) W / C) of its W tiles: every CTA has the same
 // number of tiles to within one, whatever the lengths, and the lengths stay on the device (a
 // captured graph replays with new ones).  A CTA's part of a unit is one record (unnormalised
@@ -20,7 +20,6 @@
 namespace splitkv {
 namespace tree {
 
-constexpr int kTileKeys = 64;      // keys of one step of the line
 constexpr int kMaxNodes = 256;     // nodes of a sequence
 
 struct TreeParams {
@@ -29,13 +28,14 @@ struct TreeParams {
   float* lse;
   const uint8_t* mask;             // NULL: a node sees every node of its sequence
   const int *node_ptr, *lens, *table;
-  int* status;
+  int* status;                     // two words: code, site of a timed-out wait
   // strides in bytes
   int64_t q_node, q_head, kb_node, kb_head, vb_node, vb_head;
   int64_t kc_page, kc_slot, kc_head, vc_page, vc_slot, vc_head;
   int64_t mask_row, table_row;     // elements
   int B, Nq, T, Hq, Hkv, G, d;
   int Mt, RT;                      // rows of a row tile; row tiles of max_nodes nodes
+  int tile_shift;                  // log2 of the keys of a tile: 6 (mma.sync) or 7 (tcgen05)
   int page_shift, num_pages, max_pages;
   int ctas;                        // C: CTAs of the context kernel
   int o_f32;
@@ -77,7 +77,7 @@ __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b, bool& ba
   w.n = seq_nodes(p, b, w.n0, bad);
   w.len = seq_len(p, b, bad);
   w.rts = (w.n * p.G + p.Mt - 1) / p.Mt;
-  w.nt = (w.len + kTileKeys - 1) / kTileKeys;
+  w.nt = (w.len + (1 << p.tile_shift) - 1) >> p.tile_shift;
   w.tiles = (long long)(p.Hkv) * w.rts * w.nt;
   return w;
 }
@@ -120,6 +120,7 @@ __device__ __forceinline__ int cta_of(long long x, long long W, int C) {
 
 // ---- launchers
 cudaError_t launch_tree_context_mma(const TreeParams& p, int dtype, cudaStream_t s);
+cudaError_t launch_tree_context_sm100(const TreeParams& p, int dtype, cudaStream_t s);
 cudaError_t launch_tree_merge(const TreeParams& p, int dtype, cudaStream_t s);
 
 }  // namespace tree

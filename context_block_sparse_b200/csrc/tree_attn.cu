@@ -16,6 +16,7 @@
 // rows, and softmax statistics stay in registers; scores, maxima, sums and O are float32, P is
 // rounded to the keys' type for the second product, as in the training kernels.
 #include <cstdint>
+#include <cstdlib>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -28,6 +29,7 @@ namespace tree {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kTileKeys = 64;      // keys of a tile
 constexpr int kPgRing = 8;         // page-id slots (tiles): at least the stages + 1
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
   long long mine = 0, before;
   bool bad = false;
   for (int b = b0; b < b1; ++b) mine += seq_work(p, b, bad).tiles;
-  if (bad && blockIdx.x == 0 && p.status) atomicCAS(p.status, 0, SPLITKV_ERR_INVALID_ARG);
+  if (bad && blockIdx.x == 0) atomicCAS(p.status, 0, SPLITKV_ERR_INVALID_ARG);
   const long long W = block_prefix<kThreads>(mine, before, s_scan);
   const int ctas = int(min((long long)(p.ctas), W));
   if (int(blockIdx.x) >= ctas) return;
@@ -251,6 +253,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
       at += t;
     }
   }
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge may begin its in-tree term
   __syncthreads();
   Cursor load, use;   // the tile whose pages come next; the tile computed now
   load.bad = use.bad = false;
@@ -267,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
         page = p.table[load.b * p.table_row + (key >> p.page_shift)];
         if (page < 0 || page >= p.num_pages) {
           page = -1;
-          if (p.status) atomicCAS(p.status, 0, SPLITKV_ERR_INVALID_ARG);
+          atomicCAS(p.status, 0, SPLITKV_ERR_INVALID_ARG);
         }
       }
       s_pg[t % kPgRing][tid] = page;
@@ -685,8 +688,8 @@ namespace {
 using splitkv::tree::TreeParams;
 
 struct TreeSizes {
-  int Mt, RT, ctas;
-  size_t units, ml_off, total;
+  int Mt, RT, ctas, tile_shift;
+  size_t units, ml_off, status_off, total;
 };
 
 int sm_count() {
@@ -694,6 +697,22 @@ int sm_count() {
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   cudaGetLastError();
   return sms;
+}
+
+// Whether a tensor map can describe the cache: pages of 8 tokens or more (a swizzle atom), and a
+// stride for every dimension longer than one.
+bool maps_ok(const splitkv_tree_args* a) {
+  const auto side = [&](const int64_t* s) {
+    return (a->num_pages == 1 || s[0] > 0) && s[1] > 0 && (a->num_kv_heads == 1 || s[2] > 0);
+  };
+  return a->page_size >= 8 && a->num_pages > 0 && a->max_pages > 0 && side(a->k_stride) && side(a->v_stride) &&
+         splitkv::tensor_maps_available();
+}
+
+// SPLITKV_TREE_KERNEL=mma or =tcgen05 in the environment asks for one of the context kernels.
+char asked_kernel() {
+  const char* e = std::getenv("SPLITKV_TREE_KERNEL");
+  return e ? e[0] : 0;
 }
 
 int check_sizes(const splitkv_tree_args* a, TreeSizes* z) {
@@ -706,26 +725,33 @@ int check_sizes(const splitkv_tree_args* a, TreeSizes* z) {
   if (a->head_dim != 64 && a->head_dim != 128) return SPLITKV_ERR_UNSUPPORTED;
   if (a->max_nodes > splitkv::tree::kMaxNodes || a->num_q_heads > 1024 || a->num_seqs > 65536)
     return SPLITKV_ERR_UNSUPPORTED;
-  if (int64_t(a->max_pages) * a->page_size > 0x7fffffff - splitkv::tree::kTileKeys) return SPLITKV_ERR_UNSUPPORTED;
+  if (int64_t(a->max_pages) * a->page_size > 0x7fffffff - 128) return SPLITKV_ERR_UNSUPPORTED;
   const int rows = a->num_q_heads / a->num_kv_heads * a->max_nodes;
-  z->Mt = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  const char ask = asked_kernel();
+  const bool tc = maps_ok(a) && ask != 'm' && (rows > 16 || ask == 't');
+  if (tc)
+    z->Mt = rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
+  else
+    z->Mt = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  z->tile_shift = tc ? 7 : 6;
   z->RT = (rows + z->Mt - 1) / z->Mt;
   z->units = size_t(a->num_seqs) * a->num_kv_heads * z->RT;
   if (z->units > 0x1fffffff) return SPLITKV_ERR_UNSUPPORTED;
-  // two CTAs to an SM, and no more than the longest line has tiles
-  const size_t tiles = z->units * ((size_t(a->max_pages) * a->page_size + splitkv::tree::kTileKeys - 1) /
-                                   splitkv::tree::kTileKeys);
-  const size_t ctas = size_t(2) * sm_count();
+  // One tcgen05 CTA to an SM, two of mma.sync, and no more than the longest line has tiles.
+  const size_t tiles =
+      z->units * ((size_t(a->max_pages) * a->page_size + (size_t(1) << z->tile_shift) - 1) >> z->tile_shift);
+  const size_t ctas = size_t(tc ? 1 : 2) * sm_count();
   z->ctas = int(tiles < ctas ? (tiles > 0 ? tiles : 1) : ctas);
   const size_t recs = z->units + z->ctas;
   z->ml_off = splitkv::align_up(recs * z->Mt * a->head_dim * sizeof(float), 256);
-  z->total = z->ml_off + splitkv::align_up(recs * z->Mt * sizeof(float2), 256);
+  z->status_off = z->ml_off + splitkv::align_up(recs * z->Mt * sizeof(float2), 256);
+  z->total = z->status_off + 256;
   return SPLITKV_OK;
 }
 
 // A row-strided 16-bit array read in 16-byte pieces.
 bool rows_ok(const void* ptr, int64_t s0, int64_t s1, int64_t s2 = 0) {
-  const int64_t kMax = int64_t(1) << 44;
+  const int64_t kMax = int64_t(1) << 38;   // elements; a tensor map's strides stay below 2^40 bytes
   return ptr && splitkv::ptr_aligned(ptr, 16) && s0 >= 0 && s1 >= 0 && s2 >= 0 && s0 < kMax && s1 < kMax &&
          s2 < kMax && s0 % 8 == 0 && s1 % 8 == 0 && s2 % 8 == 0;
 }
@@ -767,7 +793,7 @@ extern "C" int splitkv_tree_attn(const splitkv_tree_args* a, void* ws, size_t ws
   p.node_ptr = a->node_ptr;
   p.lens = a->context_lens;
   p.table = a->page_table;
-  p.status = a->status;
+  p.status = a->status ? a->status : reinterpret_cast<int*>(static_cast<char*>(ws) + z.status_off);
   p.q_node = a->q_stride[0] * 2;
   p.q_head = a->q_stride[1] * 2;
   p.kb_node = a->kb_stride[0] * 2;
@@ -791,6 +817,7 @@ extern "C" int splitkv_tree_attn(const splitkv_tree_args* a, void* ws, size_t ws
   p.d = a->head_dim;
   p.Mt = z.Mt;
   p.RT = z.RT;
+  p.tile_shift = z.tile_shift;
   p.page_shift = 0;
   while ((1 << p.page_shift) < a->page_size) ++p.page_shift;
   p.num_pages = a->num_pages;
@@ -801,7 +828,8 @@ extern "C" int splitkv_tree_attn(const splitkv_tree_args* a, void* ws, size_t ws
   p.rec_o = static_cast<float*>(ws);
   p.rec_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + z.ml_off);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  cudaError_t e = splitkv::tree::launch_tree_context_mma(p, a->dtype, s);
+  cudaError_t e = z.tile_shift == 7 ? splitkv::tree::launch_tree_context_sm100(p, a->dtype, s)
+                                    : splitkv::tree::launch_tree_context_mma(p, a->dtype, s);
   if (e == cudaSuccess) e = splitkv::tree::launch_tree_merge(p, a->dtype, s);
   if (e == cudaSuccess) return SPLITKV_OK;
   cudaGetLastError();

@@ -1,0 +1,632 @@
+// The context part of draft-tree attention on tcgen05: every row of a unit (sequence, KV head,
+// row tile) against the sequence's cached keys, for row tiles of 32 to 256 rows.
+//
+// A row tile's keys stream past it once, so the kernel wants HBM speed: a 128-key tile of K and V
+// (64 KB at d = 128) reaches an SM every ~2700 clocks.  A tcgen05.mma with M = 128, K = 16 costs
+// ~129 clocks for every N from 64 to 256, so both products are transposed, with keys and the head
+// dimension as M and the rows as N:
+//   S^T [128 keys x N rows] = K Q^T,     O^T [d x N rows] += V^T P^T,
+// 16 instructions a tile at d = 128 whatever the rows (2064 clocks), where rows as M would pay that
+// for every 128 of them.
+//
+// In S^T a TMEM lane is a key, so a softmax thread holds one key's scores of 64 rows (32 at a time).
+// Its row maxima would need 128 lanes' agreement at every tile; instead a row keeps a reference, the
+// maximum of its first tile, and P = exp2(s - reference) may grow up to 2^kHeadroom before the
+// reference moves (O^T and the sums are then rescaled): a tile costs one barrier vote instead of a
+// reduction.  Row sums stay in registers, one lane's share of 64 rows, and are reduced when the unit
+// ends.  A thread's 64 probabilities are one 128-byte row of P^T in the swizzled layout that the
+// second product reads as its MN-major B operand.
+//
+// The first warps are softmax groups of four, 64 rows each, which also load Q and write the
+// records.  Behind them one warp loads pages by TMA (one box a page and 64 columns) into a ring of
+// tiles in the order in which the products take them: K0, K1, V0, K2, V1, ...; the last issues the
+// products, S(j + 1) before PV(j), so that scores are formed while the softmax of the tile before
+// runs.
+// Keys behind the context's end or on a bad page are masked as lanes; their V rows are zeroed in
+// shared memory before the product (P = 0 does not hide a NaN).
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "sm100.cuh"
+#include "tree.h"
+
+namespace splitkv {
+namespace tree {
+namespace {
+
+using namespace sm100;
+
+constexpr int kKeys = 128;                    // keys of a tile (M of the first product)
+constexpr uint32_t kHalf = kKeys * 128;       // bytes of 128 rows x 64 columns
+constexpr int kMetaRing = 16;                 // page-error masks in flight (K tiles)
+constexpr float kHeadroom = 8.0f;             // log2: P up to 256 (float16 P stays far from its limits)
+constexpr int kFile = 8 * 10000;              // site number of this file's waits
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
+                                            int w) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5, %6}], "
+      "[%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z), "r"(w)
+      : "memory");
+}
+
+// kind::f16, float32 accumulator; A and B of one 16-bit type.
+__host__ __device__ constexpr uint32_t idesc(bool f16, int M, int N, int a_mn, int b_mn) {
+  return (1u << 4) | ((f16 ? 0u : 1u) << 7) | ((f16 ? 0u : 1u) << 10) | (uint32_t(a_mn) << 15) |
+         (uint32_t(b_mn) << 16) | (uint32_t(N >> 3) << 17) | (uint32_t(M >> 4) << 24);
+}
+
+template <typename T>
+constexpr bool kIsF16 = false;
+template <>
+constexpr bool kIsF16<__half> = true;
+template <typename T>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+  if constexpr (kIsF16<T>) {
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+  } else {
+    return pack_bf16(lo, hi);
+  }
+}
+
+// Barriers over one softmax group (128 threads); vote returns whether any thread's predicate holds.
+__device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(g + 1) : "memory"); }
+__device__ __forceinline__ bool group_any(int g, bool pred) {
+  uint32_t out;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.or.pred q, %1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(out)
+      : "r"(g + 1), "r"(pred ? 1u : 0u)
+      : "memory");
+  return out != 0;
+}
+__device__ __forceinline__ float warp_max(float x) {
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+template <int D, int NR>
+struct Dims {
+  static constexpr int kCols = NR < 64 ? NR : 64;            // rows (TMEM columns) of a softmax group
+  static constexpr int kGroups = NR / kCols;
+  static constexpr int kThreads = 128 * kGroups + 64;        // (four groups: 576 threads of 112 registers)
+  static constexpr uint32_t kTile = uint32_t(D / 64) * kHalf;
+  static constexpr uint32_t kQ = uint32_t(D / 64) * NR * 128;
+  static constexpr uint32_t kP = uint32_t(kGroups) * kHalf;
+  static constexpr uint32_t kMeta = 512 + NR * 8;            // barriers, shifts, factors
+  static constexpr int kFit = int((232448 - kMeta - kQ - kP) / kTile);
+  static constexpr int kStages = kFit > 8 ? 8 : kFit;
+  static_assert(kStages >= 3, "ring");
+  // the ring comes first: at d = 64 the second half of the V^T operand's M is whatever follows the tile
+  static constexpr uint32_t kOffQ = kStages * kTile;
+  static constexpr uint32_t kOffP = kOffQ + kQ;
+  static constexpr uint32_t kOffMeta = kOffP + kP;
+  static constexpr uint32_t kSmem = kOffMeta + kMeta;
+  static constexpr uint32_t kTmem = NR * 2 < 32 ? 32 : NR * 2;
+};
+
+struct Bars {
+  uint64_t full[8], empty[8];
+  uint64_t q_full, s_full, s_free, p_ready, o_done, mma_done;
+  long long scan[20];
+  long long rel;
+  int seq;
+  uint32_t tmem_base;
+  int abort_flag;
+  int bad[kMetaRing];
+};
+static_assert(sizeof(Bars) <= 512, "barrier block");
+
+// One stretch of a unit's tiles on this CTA.
+struct Segment {
+  SeqWork w;
+  int b, head, rt, tile0, tiles;
+};
+struct Walk {
+  long long left;   // tiles of this CTA's stretch not yet handed out
+  int b, unit, tile;
+  SeqWork w;
+  bool bad;
+  __device__ void begin(const TreeParams& p, int seq, long long rel, long long n) {
+    left = n;
+    b = seq;
+    bad = false;
+    if (n <= 0) return;
+    w = seq_work(p, b, bad);
+    unit = int(rel / w.nt);
+    tile = int(rel % w.nt);
+  }
+  __device__ bool next(const TreeParams& p, Segment& s) {
+    if (left <= 0) return false;
+    while (unit >= p.Hkv * w.rts || w.tiles == 0) {
+      if (++b >= p.B) return false;
+      w = seq_work(p, b, bad);
+      unit = tile = 0;
+    }
+    s.w = w;
+    s.b = b;
+    s.head = unit / w.rts;
+    s.rt = unit % w.rts;
+    s.tile0 = tile;
+    s.tiles = int(min((long long)(w.nt - tile), left));
+    left -= s.tiles;
+    ++unit;
+    tile = 0;
+    return true;
+  }
+};
+
+template <typename T, int D, int NR>
+__global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
+    tree_context_sm100_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                              const TreeParams p) {
+  using Dm = Dims<D, NR>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars* bars = reinterpret_cast<Bars*>(smem + Dm::kOffMeta);
+  // a row's shift: minus its reference (log2 units); -0.0: it has none yet (a reference of 0 is stored as +0.0)
+  float* s_nref = reinterpret_cast<float*>(smem + Dm::kOffMeta + 512);
+  float* s_f = s_nref + NR;   // factor of a moved reference
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const WaitCtx wctx{&bars->abort_flag, p.status, kWaitLimitNs};
+  constexpr int kSoftWarps = 4 * Dm::kGroups;
+
+  if (tid == 0) {
+    for (int s = 0; s < Dm::kStages; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], 1);
+    }
+    mbar_init(&bars->q_full, kSoftWarps);
+    mbar_init(&bars->s_full, 1);
+    mbar_init(&bars->s_free, kSoftWarps);
+    mbar_init(&bars->p_ready, kSoftWarps);
+    mbar_init(&bars->o_done, 1);
+    mbar_init(&bars->mma_done, 1);
+    bars->abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == kSoftWarps + 1) {
+    tmem_alloc(&bars->tmem_base, Dm::kTmem);
+    tmem_relinquish();
+  }
+  if (warp == kSoftWarps && lane == 0) {
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  // this CTA's stretch of the line, and the sequence it begins in
+  const int per = (p.B + Dm::kThreads - 1) / Dm::kThreads;
+  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+  long long mine = 0, before;
+  bool bad = false;
+  for (int b = b0; b < b1; ++b) mine += seq_work(p, b, bad).tiles;
+  if (bad && blockIdx.x == 0) atomicCAS(p.status, 0, SPLITKV_ERR_INVALID_ARG);
+  const long long W = block_prefix<Dm::kThreads>(mine, before, bars->scan);
+  const int ctas = int(min((long long)(p.ctas), W));
+  const bool work = int(blockIdx.x) < ctas;
+  const long long x0 = work ? stretch(W, blockIdx.x, ctas) : 0;
+  const long long n_tiles = work ? stretch(W, blockIdx.x + 1, ctas) - x0 : 0;
+  if (work && x0 >= before && x0 < before + mine) {
+    long long at = before;
+    for (int b = b0; b < b1; ++b) {
+      const long long t = seq_work(p, b, bad).tiles;
+      if (x0 < at + t) {
+        bars->seq = b;
+        bars->rel = x0 - at;
+        break;
+      }
+      at += t;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const uint32_t tmem = bars->tmem_base;
+  Walk walk;
+  walk.begin(p, work ? bars->seq : 0, work ? bars->rel : 0, n_tiles);
+  Segment sg;
+
+  const int page = 1 << p.page_shift;
+  const int box = min(page, kKeys);      // keys of a TMA box
+
+  if (warp == kSoftWarps) {
+    // ------------------------------------------------------------ TMA producer
+    uint32_t c = 0, kc = 0;
+    bool ok = true;
+    const int boxes = kKeys / box;
+    // lane l's page id of a tile (lanes past the tile's pages: none)
+    auto page_of = [&](const Segment& s, int j) -> int {
+      const int key = (s.tile0 + j) * kKeys + lane * box;
+      if (lane >= boxes || key >= s.w.len) return -2;      // no box
+      return p.table[s.b * p.table_row + (key >> p.page_shift)];
+    };
+    auto load = [&](const CUtensorMap* map, const Segment& s, int j, int pg) -> bool {
+      const int slot = int(c % Dm::kStages);
+      if (!warp_wait(&bars->empty[slot], ((c / Dm::kStages) & 1) ^ 1, wctx, kFile + __LINE__)) return false;
+      const int n = __popc(__ballot_sync(0xffffffffu, pg != -2));
+      if (lane == 0) mbar_expect_tx(&bars->full[slot], uint32_t(n) * box * 128 * (D / 64));
+      __syncwarp();
+      if (pg != -2) {
+        // a page outside the cache reads as zeros: a page coordinate past the last one
+        const int pc = pg < 0 || pg >= p.num_pages ? p.num_pages : pg;
+        const int at = ((s.tile0 + j) * kKeys + lane * box) & (page - 1);
+        for (int h = 0; h < D / 64; ++h)
+          tma_load_4d(smem + slot * Dm::kTile + h * kHalf + lane * box * 128, map, &bars->full[slot], h * 64, s.head, at,
+                      pc);
+      }
+      ++c;
+      return true;
+    };
+    auto note = [&](int pg) {     // pages of a K tile that do not exist, for the softmax
+      const bool wrong = pg != -2 && (pg < 0 || pg >= p.num_pages);
+      const uint32_t m = __ballot_sync(0xffffffffu, wrong);
+      if (lane == 0) {
+        bars->bad[kc % kMetaRing] = int(m);
+        if (m) atomicCAS(p.status, 0, SPLITKV_ERR_INVALID_ARG);
+      }
+      ++kc;
+    };
+    while (ok && walk.next(p, sg)) {
+      int now = page_of(sg, 0), nxt = sg.tiles > 1 ? page_of(sg, 1) : -2;
+      note(now);
+      if (!load(&tm_k, sg, 0, now)) { ok = false; break; }
+      for (int j = 0; j < sg.tiles; ++j) {
+        const int ahead = j + 2 < sg.tiles ? page_of(sg, j + 2) : -2;
+        if (j + 1 < sg.tiles) {
+          note(nxt);
+          if (!load(&tm_k, sg, j + 1, nxt)) { ok = false; break; }
+        }
+        if (!load(&tm_v, sg, j, now)) { ok = false; break; }
+        now = nxt;
+        nxt = ahead;
+      }
+    }
+    if (!ok) bars->abort_flag = 1;
+    // copies in flight land before the CTA may exit
+    if (lane == 0)
+      for (uint32_t i = c >= uint32_t(Dm::kStages) ? c - Dm::kStages : 0; i < c; ++i)
+        mbar_drain(&bars->full[i % Dm::kStages], (i / Dm::kStages) & 1, wctx, kFile + __LINE__);
+    __syncwarp();
+  } else if (warp == kSoftWarps + 1) {
+    // ------------------------------------------------------------ MMA issuer
+    if (lane == 0) {
+      constexpr uint32_t kIdS = idesc(kIsF16<T>, kKeys, NR, 0, 0), kIdO = idesc(kIsF16<T>, 128, NR, 1, 1);
+      const uint32_t ring = smem_u32(smem), sQ = smem_u32(smem + Dm::kOffQ), sP = smem_u32(smem + Dm::kOffP);
+      uint32_t c = 0, t = 0, seg = 0;     // ring slots, tiles, segments so far
+      bool ok = true;
+      // scores of the next tile: S^T = K Q^T once its K has landed and the scores before are read
+      auto issue_s = [&](uint32_t tile) -> bool {
+        const int slot = int(c % Dm::kStages);
+        if (tile > 0 && !mbar_wait(&bars->s_free, (tile - 1) & 1, wctx, kFile + __LINE__)) return false;
+        if (!mbar_wait(&bars->full[slot], (c / Dm::kStages) & 1, wctx, kFile + __LINE__)) return false;
+        tc_fence_after();
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t a = smem_desc_sw128(ring + slot * Dm::kTile + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024);
+          const uint64_t b = smem_desc_sw128(sQ + (kk >> 2) * (NR * 128) + (kk & 3) * 32, 16, 1024);
+          mma_ss(tmem, a, b, kIdS, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(&bars->empty[slot]);
+        mma_commit(&bars->s_full);
+        ++c;
+        return true;
+      };
+      while (ok && walk.next(p, sg)) {
+        if (!mbar_wait(&bars->q_full, seg & 1, wctx, kFile + __LINE__)) { ok = false; break; }
+        ++seg;
+        if (!issue_s(t)) { ok = false; break; }
+        for (int j = 0; j < sg.tiles; ++j, ++t) {
+          if (j + 1 < sg.tiles && !issue_s(t + 1)) { ok = false; break; }
+          const int slot = int(c % Dm::kStages);
+          if (!mbar_wait(&bars->p_ready, t & 1, wctx, kFile + __LINE__)) { ok = false; break; }
+          if (!mbar_wait(&bars->full[slot], (c / Dm::kStages) & 1, wctx, kFile + __LINE__)) { ok = false; break; }
+          tc_fence_after();
+          for (int kk = 0; kk < kKeys / 16; ++kk) {
+            const uint64_t a = smem_desc_sw128(ring + slot * Dm::kTile + kk * 2048, kHalf, 1024);
+            const uint64_t b = smem_desc_sw128(sP + kk * 2048, kHalf, 1024);
+            mma_ss(tmem + NR, a, b, kIdO, (j > 0 || kk > 0) ? 1u : 0u);
+          }
+          mma_commit(&bars->empty[slot]);
+          mma_commit(&bars->o_done);
+          ++c;
+        }
+      }
+      if (!ok) bars->abort_flag = 1;
+      mma_commit(&bars->mma_done);   // every product ends before tensor memory is released
+      mbar_drain(&bars->mma_done, 0, wctx, kFile + __LINE__);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax groups
+    const int g = warp >> 2, wq = warp & 3;
+    const int key_lane = wq * 32 + lane;               // key of a tile = TMEM lane; head element in O^T
+    const int col0 = g * Dm::kCols;                    // this group's rows
+    constexpr int kChunks = Dm::kCols / 32;
+    // Row sums of a thread: its own share of every row of the group; with four groups (few registers a thread) two
+    // neighbouring lanes add theirs at every tile and keep 16 of each chunk's 32 rows.
+    constexpr bool kPair = Dm::kGroups == 4;
+    constexpr int kL = kPair ? Dm::kCols / 2 : Dm::kCols;
+    const bool odd = (lane & 1) != 0;
+    const uint32_t tS = tmem + (uint32_t(wq * 32) << 16) + col0, tO = tS + NR;
+    uint8_t* my_p = smem + Dm::kOffP + g * kHalf + key_lane * 128;
+    const float scale = p.scale_log2;
+    uint32_t t = 0, ring0 = 0;      // tiles and ring slots of the segments before
+    bool ok = true;
+
+    auto load_q = [&](const Segment& s) {
+      // rows col0.. of the tile into the K-major operand layout, rows past the tile's end zero
+      const int rows = s.w.n * p.G - s.rt * NR;
+      constexpr int kCh = D / 8;
+      for (int i = tid & 127; i < Dm::kCols * kCh; i += 128) {
+        const int r = col0 + i / kCh, ch = i % kCh;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < rows) {
+          const int row = s.rt * NR + r, node = row / p.G, h = s.head * p.G + row - node * p.G;
+          x = __ldg(reinterpret_cast<const uint4*>(p.q + int64_t(s.w.n0 + node) * p.q_node + int64_t(h) * p.q_head + ch * 16));
+        }
+        *reinterpret_cast<uint4*>(smem + Dm::kOffQ + (ch >> 3) * (NR * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x;
+      }
+      fence_async_smem();
+      warp_arrive(&bars->q_full);
+    };
+
+    // After a wait gave up (ok is false, the kernel winds down) a warp walks on without waiting, so that its group's
+    // barriers still meet; what it writes is inside its records.
+    bool more = walk.next(p, sg);
+    if (more) load_q(sg);
+    while (more) {
+      const Segment s = sg;
+      const int rows = min(NR, s.w.n * p.G - s.rt * NR);
+      const int live = max(0, min(kChunks, (rows - col0 + 31) / 32));   // chunks with rows
+      float l[kL];
+#pragma unroll
+      for (int i = 0; i < kL; ++i) l[i] = 0.f;
+      if ((tid & 127) < Dm::kCols) s_nref[col0 + (tid & 127)] = -0.0f;
+      bool need = true;       // a row has no reference yet
+      group_sync(g);
+      for (int j = 0; j < s.tiles; ++j, ++t) {
+        const int key = (s.tile0 + j) * kKeys + key_lane;
+        ok = ok && warp_wait(&bars->s_full, t & 1, wctx, kFile + __LINE__);
+        tc_fence_after();
+        const uint32_t wrong = uint32_t(bars->bad[t % kMetaRing]);
+        const bool valid = key < s.w.len && !((wrong >> (key_lane / box)) & 1u);
+        const bool part = wrong != 0 || (s.tile0 + j + 1) * kKeys > s.w.len;
+        bool first_need = need;
+        bool still = false;
+        bool waited = false;
+#pragma unroll
+        for (int ch = 0; ch < kChunks; ++ch) {
+          if (ch < live) {
+            uint32_t v[32];
+            tmem_ld32(tS + ch * 32, v);
+            tmem_wait_ld();
+            reg_fence<32>(v);
+            if (ch == live - 1) {
+              tc_fence_before();
+              warp_arrive(&bars->s_free);
+            }
+            float* nref = s_nref + col0 + ch * 32;
+            float* fac = s_f + col0 + ch * 32;
+            float x[32];
+            bool over = first_need;
+            if (!first_need) {
+              float mx = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const float4 r = *reinterpret_cast<const float4*>(nref + i);
+                ffma2(x[i], x[i + 1], __uint_as_float(v[i]), __uint_as_float(v[i + 1]), scale, scale, r.x, r.y);
+                ffma2(x[i + 2], x[i + 3], __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]), scale, scale, r.z, r.w);
+                mx = fmax3(mx, x[i], x[i + 1]);
+                mx = fmax3(mx, x[i + 2], x[i + 3]);
+              }
+              over = group_any(g, valid && mx > kHeadroom);
+            }
+            if (over) {
+              // new references for this chunk's rows: lane i of every warp gets column i's maximum
+              float m = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const float y = warp_max(valid ? __uint_as_float(v[i]) * scale : -INFINITY);
+                m = lane == i ? y : m;
+              }
+              // exchanged through the factors' and shifts' slots of this chunk, two warps at a time
+              const uint32_t was = __float_as_uint(nref[lane]);
+              const float old = was == 0x80000000u ? -INFINITY : -__uint_as_float(was);
+              group_sync(g);
+              if (wq == 0) fac[lane] = m;
+              if (wq == 1) nref[lane] = m;
+              group_sync(g);
+              if (wq == 2) fac[lane] = fmaxf(fac[lane], m);
+              if (wq == 3) nref[lane] = fmaxf(nref[lane], m);
+              group_sync(g);
+              m = fmaxf(fac[lane], nref[lane]);
+              const float to = old == -INFINITY ? m : (m > old + kHeadroom ? m : old);
+              const float f = old == -INFINITY ? 1.f : fast_exp2(old - to);
+              group_sync(g);
+              if (wq == 0) {
+                nref[lane] = to == -INFINITY ? -0.0f : 0.f - to;
+                fac[lane] = f;
+              }
+              const bool moved = group_any(g, f != 1.f);
+              still |= group_any(g, to == -INFINITY);
+              if (moved) {
+                if constexpr (kPair) {
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) l[ch * 16 + i] *= fac[(odd ? 16 : 0) + i];
+                } else {
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) l[ch * 32 + i] *= fac[i];
+                }
+                if (j > 0) {
+                  ok = ok && warp_wait(&bars->o_done, (t - 1) & 1, wctx, kFile + __LINE__);
+                  waited = true;
+                  tc_fence_after();
+#pragma unroll 1
+                  for (int e = 0; e < 32; e += 16) {
+                    uint32_t o[16];
+                    tmem_ld16(tO + ch * 32 + e, o);
+                    tmem_wait_ld();
+                    reg_fence<16>(o);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fac[e + i]);
+                    tmem_st16(tO + ch * 32 + e, o);
+                  }
+                  tmem_wait_st();
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = fmaf(__uint_as_float(v[i]), scale, nref[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 32; ++i) x[i] = fast_exp2(x[i]);
+            if (part) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = valid ? x[i] : 0.f;
+            }
+            if constexpr (kPair) {
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float y = __shfl_xor_sync(0xffffffffu, odd ? x[i] : x[16 + i], 1);
+                l[ch * 16 + i] += (odd ? x[16 + i] : x[i]) + y;
+              }
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; i += 2)
+                fadd2(l[ch * 32 + i], l[ch * 32 + i + 1], l[ch * 32 + i], l[ch * 32 + i + 1], x[i], x[i + 1]);
+            }
+            // P^T may be rewritten once the product before has read it
+            if (t > 0 && !waited) {
+              ok = ok && warp_wait(&bars->o_done, (t - 1) & 1, wctx, kFile + __LINE__);
+              waited = true;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(my_p + (((ch * 4 + i) ^ (key_lane & 7)) << 4)) =
+                  make_uint4(pack<T>(x[8 * i], x[8 * i + 1]), pack<T>(x[8 * i + 2], x[8 * i + 3]),
+                             pack<T>(x[8 * i + 4], x[8 * i + 5]), pack<T>(x[8 * i + 6], x[8 * i + 7]));
+          }
+        }
+        if (live == 0) {
+          warp_arrive(&bars->s_free);
+        } else {
+          need = still;
+        }
+        // (a group without rows keeps step: its arrival must not fall into the tile before)
+        if (t > 0 && !waited) ok = ok && warp_wait(&bars->o_done, (t - 1) & 1, wctx, kFile + __LINE__);
+        if (g == 0 && (s.tile0 + j + 1) * kKeys > s.w.len) {
+          // the context ends inside this tile, the unit's last: V rows behind it become zeros
+          const uint32_t i = ring0 + 2 * s.tiles - 1;
+          ok = ok && warp_wait(&bars->full[i % Dm::kStages], (i / Dm::kStages) & 1, wctx, kFile + __LINE__);
+          if (ok && key >= s.w.len) {
+            for (int h = 0; h < D / 64; ++h)
+              for (int e = 0; e < 8; ++e)
+                *reinterpret_cast<uint4*>(smem + (i % Dm::kStages) * Dm::kTile + h * kHalf + key_lane * 128 + e * 16) =
+                    make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_async_smem();
+        tc_fence_before();
+        warp_arrive(&bars->p_ready);
+      }
+      ring0 += 2 * s.tiles;
+      // the next unit's queries (the last scores of this one are done), so that its first scores overlap this epilogue
+      more = walk.next(p, sg);
+      if (more) load_q(sg);
+      ok = ok && warp_wait(&bars->o_done, (t - 1) & 1, wctx, kFile + __LINE__);
+      tc_fence_after();
+      const size_t rec = size_t(blockIdx.x) + (size_t(s.b) * p.Hkv + s.head) * p.RT + s.rt;
+      float* dst = p.rec_o + (rec * NR + col0) * D + key_lane;
+#pragma unroll 1
+      for (int ch = 0; ch < live; ++ch) {
+        uint32_t o[32];
+        tmem_ld32(tO + ch * 32, o);
+        tmem_wait_ld();
+        reg_fence<32>(o);
+        if (D == 128 || wq < D / 32) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (col0 + ch * 32 + i < rows) dst[(ch * 32 + i) * D] = __uint_as_float(o[i]);
+        }
+      }
+      tc_fence_before();
+      // row sums: over the warp's lanes (each step leaves half the rows to a lane), then over the four warps
+      if (live > 0) {
+        int r = 0;       // this lane's first row after the steps
+#pragma unroll
+        for (int st = 16, n = kL / 2; st > (kPair ? 1 : 0); st >>= 1, n >>= 1) {
+          const bool up = (lane & st) != 0;
+#pragma unroll
+          for (int i = 0; i < n; ++i) {
+            const float send = up ? l[i] : l[i + n];
+            const float keep = up ? l[i + n] : l[i];
+            l[i] = keep + __shfl_xor_sync(0xffffffffu, send, st);
+          }
+          r += up ? n : 0;
+        }
+        float* s_l = reinterpret_cast<float*>(smem + Dm::kOffP + g * kHalf);   // P^T of this group: read by no product now
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+          const int e = r + i;
+          s_l[wq * 64 + (kPair ? (e / 16) * 32 + (odd ? 16 : 0) + e % 16 : e)] = l[i];
+        }
+        group_sync(g);
+        const int row = tid & 127;
+        if (row < Dm::kCols && col0 + row < rows)
+        {
+          const float nr = s_nref[col0 + row];
+          p.rec_ml[rec * NR + col0 + row] =
+              make_float2(__float_as_uint(nr) == 0x80000000u ? -INFINITY : -nr,
+                          s_l[row] + s_l[64 + row] + s_l[128 + row] + s_l[192 + row]);
+        }
+        group_sync(g);
+      }
+    }
+    if (!ok) bars->abort_flag = 1;
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kSoftWarps + 1) tmem_dealloc(tmem, Dm::kTmem);
+}
+
+template <typename T, int D, int NR>
+cudaError_t launch(const TreeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  using Dm = Dims<D, NR>;
+  cudaError_t e = cudaFuncSetAttribute(tree_context_sm100_kernel<T, D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       int(Dm::kSmem));
+  if (e != cudaSuccess) return e;
+  tree_context_sm100_kernel<T, D, NR><<<p.ctas, Dm::kThreads, Dm::kSmem, s>>>(tk, tv, p);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t rows(const TreeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+  switch (p.Mt) {
+    case 32: return launch<T, D, 32>(p, tk, tv, s);
+    case 64: return launch<T, D, 64>(p, tk, tv, s);
+    case 128: return launch<T, D, 128>(p, tk, tv, s);
+    default: return launch<T, D, 256>(p, tk, tv, s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_tree_context_sm100(const TreeParams& p, int dtype, cudaStream_t s) {
+  const bool f16 = dtype == SPLITKV_DTYPE_F16;
+  const int page = 1 << p.page_shift;
+  const uint32_t box = page < kKeys ? page : kKeys;
+  CUtensorMap tk, tv;
+  if (!make_page_map_4d(&tk, p.kc, f16, p.d, p.Hkv, page, p.num_pages, p.kc_head, p.kc_slot, p.kc_page, box) ||
+      !make_page_map_4d(&tv, p.vc, f16, p.d, p.Hkv, page, p.num_pages, p.vc_head, p.vc_slot, p.vc_page, box))
+    return cudaErrorInvalidValue;
+  if (f16) return p.d == 128 ? rows<__half, 128>(p, tk, tv, s) : rows<__half, 64>(p, tk, tv, s);
+  return p.d == 128 ? rows<__nv_bfloat16, 128>(p, tk, tv, s) : rows<__nv_bfloat16, 64>(p, tk, tv, s);
+}
+
+}  // namespace tree
+}  // namespace splitkv

@@ -24,23 +24,23 @@ from typing import Optional
 import numpy as np
 import torch
 
-from . import (
-    SplitKVError, splitkv_tree_args, splitkv_tree_attn, splitkv_tree_commit, splitkv_tree_verify,
-    splitkv_tree_workspace_size,
+from . import SplitKVError, _with_site
+from .draft_calls import (
+    splitkv_tree_args, splitkv_tree_attn, splitkv_tree_commit, splitkv_tree_verify, splitkv_tree_workspace_size,
 )
 
 
 def new_status(device=None) -> torch.Tensor:
-    """A cleared status word: the kernels record an error about the device arrays they were given in it."""
-    return torch.zeros(1, dtype=torch.int32, device="cuda" if device is None else device)
+    """Cleared status words: the kernels record an error about the device arrays they were given in them."""
+    return torch.zeros(2, dtype=torch.int32, device="cuda" if device is None else device)
 
 
 def check_status(status: torch.Tensor) -> None:
     """Raise SplitKVError if a call that was given `status` recorded an error; clears it.  Synchronises."""
-    code = int(status.item())
+    code, site = status.tolist()
     if code:
         status.zero_()
-        raise SplitKVError("draft tree call", code)
+        raise _with_site(SplitKVError("draft tree call", code), site)
 
 
 def tree_mask(parents, node_ptr, max_nodes: int) -> np.ndarray:
@@ -80,19 +80,19 @@ class SplitKVTreeAttention:
         power of two); page_table int32 [B, pages]; context_lens int32 [B].  bfloat16 or float16; the last
         dimension contiguous, other strides in multiples of 8 elements.  Returns o [nodes, Hq, d] (out_dtype: q's
         type, or float32) and lse [nodes, Hq]; rows behind the last sequence's nodes are left as they were."""
-        if q.dim() != 3 or q.shape[1] != self.num_q_heads or q.shape[2] != self.head_dim:
+        shape = q.shape
+        if len(shape) != 3 or shape[1] != self.num_q_heads or shape[2] != self.head_dim:
             raise ValueError(f"q must be [nodes, {self.num_q_heads}, {self.head_dim}]")
         if k_cache.dim() != 4 or k_cache.shape[2] != self.num_kv_heads:
             raise ValueError(f"k_cache must be [pages, page_size, {self.num_kv_heads}, {self.head_dim}]")
         if o is None:
-            o = torch.empty(q.shape, dtype=q.dtype if out_dtype is None else out_dtype, device=q.device)
+            o = q.new_empty(shape) if out_dtype is None else q.new_empty(shape, dtype=out_dtype)
         if lse is None:
-            lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        status = self.status if self.status.device == q.device else None
+            lse = q.new_empty((shape[0], shape[1]), dtype=torch.float32)
         args, dev = splitkv_tree_args(q, kb, vb, node_ptr, mask, k_cache, v_cache, page_table, context_lens, scale,
-                                      self.max_nodes, o, lse, status)
+                                      self.max_nodes, o, lse, self.status)
         # the workspace is this call's own: calls on other streams and captured graphs share nothing
-        ws = torch.empty(splitkv_tree_workspace_size(args, dev), dtype=torch.uint8, device=q.device)
+        ws = q.new_empty((splitkv_tree_workspace_size(args, dev),), dtype=torch.uint8)
         splitkv_tree_attn(args, ws, dev)
         return o, lse
 
@@ -112,10 +112,9 @@ def verify_draft(target_probs, draft_probs, tokens, parents, node_ptr, u_accept,
     Returns path int32 [B, max_path] (local nodes from node 0 on, -1 behind them; max_path defaults to max_nodes,
     and the walk ends there), count int32 [B], next_token [B] (as tokens; -1 where there is none)."""
     B = node_ptr.shape[0] - 1
-    dev = target_probs.device
-    path = torch.empty((B, max_nodes if max_path is None else max_path), dtype=torch.int32, device=dev)
-    count = torch.empty(B, dtype=torch.int32, device=dev)
-    next_token = torch.empty(B, dtype=tokens.dtype, device=dev)
+    path = node_ptr.new_empty((B, max_nodes if max_path is None else max_path))
+    count = node_ptr.new_empty((B,))
+    next_token = tokens.new_empty((B,))
     splitkv_tree_verify(target_probs, draft_probs, tokens, parents, node_ptr, u_accept, u_sample, max_nodes, path,
                         count, next_token, status)
     return path, count, next_token
@@ -129,8 +128,6 @@ def commit_draft(k_cache, v_cache, page_table, context_lens, kb, vb, node_ptr, p
     dimension on the four.  path, count: as verify_draft returns them; without a path every node is appended in
     order (max_nodes then bounds a sequence's nodes).  context_lens is not advanced: add count once all layers are
     written.  Sequences must not share the pages they write."""
-    if k_cache.dim() == 4:
-        k_cache, v_cache, kb, vb = k_cache[None], v_cache[None], kb[None], vb[None]
     if path is None:
         if max_nodes is None:
             raise ValueError("max_nodes bounds the nodes of a sequence where no path is given")

@@ -14,9 +14,8 @@ from typing import Optional
 
 import torch
 
-from . import (
-    ROPE_SCALE_BASE, ROPE_SCALE_LINEAR, ROPE_SCALE_NONE, ROPE_SCALE_PARTS, splitkv_rope, splitkv_rope_freqs,
-)
+from ._abi import ROPE_SCALE_BASE, ROPE_SCALE_LINEAR, ROPE_SCALE_NONE, ROPE_SCALE_PARTS
+from .draft_calls import splitkv_rope, splitkv_rope_freqs
 
 SCALINGS = {"none": ROPE_SCALE_NONE, "linear": ROPE_SCALE_LINEAR, "base": ROPE_SCALE_BASE, "parts": ROPE_SCALE_PARTS}
 
@@ -46,27 +45,29 @@ class Rotary:
         self.freqs = torch.from_numpy(freqs)      # float64, radians per position
         self._on = {}                             # per device (uploaded once; before a graph is captured)
         if torch.cuda.is_available():
-            self._table(torch.device("cuda" if device is None else device))
+            device = torch.device("cuda" if device is None else device)
+            self._table(torch.cuda.current_device() if device.index is None else device.index)
 
-    def _table(self, device) -> torch.Tensor:
-        index = torch.cuda.current_device() if device.index is None else device.index
+    def _table(self, index: int) -> torch.Tensor:
         t = self._on.get(index)
         if t is None:
             t = self._on[index] = self.freqs.to(torch.device("cuda", index))
         return t
 
     def _apply(self, positions, q, k, out, adjoint: bool):
-        for name, t in (("q", q), ("k", k)):
-            if t is not None and (t.dim() != 3 or t.shape[2] != self.head_dim):
-                raise ValueError(f"{name} must be [n, heads, {self.head_dim}]")
-        if q.device.type != "cuda":
+        d = self.head_dim
+        if q.dim() != 3 or q.shape[2] != d:
+            raise ValueError(f"q must be [n, heads, {d}]")
+        if k is not None and (k.dim() != 3 or k.shape[2] != d):
+            raise ValueError(f"k must be [n, heads, {d}]")
+        dev = q.get_device()
+        if dev < 0:
             raise ValueError("q must be a CUDA tensor")
         if out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            k_out = None if k is None else torch.empty(k.shape, dtype=k.dtype, device=q.device)
+            q_out, k_out = torch.empty_like(q), None if k is None else torch.empty_like(k)
         else:
             q_out, k_out = out if k is not None else (out[0], None)
-        splitkv_rope(positions, self._table(q.device), self.scale, q, k, q_out, k_out, self.interleaved, adjoint)
+        splitkv_rope(positions, self._table(dev), self.scale, q, k, q_out, k_out, self.interleaved, adjoint)
         return q_out if k is None else (q_out, k_out)
 
     def forward(self, positions, q, k=None, out=None):

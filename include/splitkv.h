@@ -582,8 +582,9 @@ int splitkv_rope(const splitkv_rope_args* args, void* stream);
  * host (a captured graph may replay with new values).  The kernels check them: what lies outside
  * its array counts as absent -- a sequence with a bad node_ptr or more than max_nodes nodes has no
  * nodes, a bad context length is clamped, a key on a bad page does not exist, a path row that is no
- * node or has no page is not written -- and SPLITKV_ERR_INVALID_ARG is recorded in *status (device
- * int32, may be NULL; the caller clears it). */
+ * node or has no page is not written -- and SPLITKV_ERR_INVALID_ARG is recorded in status[0] (device
+ * int32 [2], may be NULL; the caller clears it).  A bounded wait of a kernel that gave up records
+ * SPLITKV_ERR_TIMEOUT there and its site in status[1]; the call's results are then invalid. */
 typedef struct splitkv_tree_args {
   int32_t        num_seqs;        /* B <= 65536                                                   */
   int32_t        num_nodes;       /* rows of q, kb, vb, mask, o, lse                              */
