@@ -40,6 +40,7 @@ using namespace sm100;
 
 constexpr int kKeys = 128;                    // keys of a tile (M of the first product)
 constexpr uint32_t kHalf = kKeys * 128;       // bytes of 128 rows x 64 columns
+constexpr uint32_t kBarBytes = 768;           // barrier block
 constexpr int kMetaRing = 16;                 // page-error masks in flight (K tiles)
 constexpr float kHeadroom = 8.0f;             // log2: P up to 256 (float16 P stays far from its limits)
 constexpr int kFile = 8 * 10000;              // site number of this file's waits
@@ -93,27 +94,41 @@ __device__ __forceinline__ float warp_max(float x) {
 
 template <int D, int NR>
 struct Dims {
-  static constexpr int kCols = NR < 64 ? NR : 64;            // rows (TMEM columns) of a softmax group
+  // Rows (TMEM columns) of a softmax group.  A thread keeps its scores in registers from the check to the
+  // exponentials, except at NR = 256, where it has 96 of them: scores are read twice, 16 at a time.
+  static constexpr int kCols = NR <= 64 ? 32 : 64;
   static constexpr int kGroups = NR / kCols;
-  static constexpr int kThreads = 128 * kGroups + 64;        // (four groups: 576 threads of 112 registers)
+  static constexpr int kThreads = 128 * kGroups + 64;
+  static constexpr int kPBufs = NR <= 128 ? 2 : 1;           // P^T buffers
   static constexpr uint32_t kTile = uint32_t(D / 64) * kHalf;
   static constexpr uint32_t kQ = uint32_t(D / 64) * NR * 128;
-  static constexpr uint32_t kP = uint32_t(kGroups) * kHalf;
-  static constexpr uint32_t kMeta = 512 + NR * 8;            // barriers, shifts, factors
-  static constexpr int kFit = int((232448 - kMeta - kQ - kP) / kTile);
+  static constexpr uint32_t kP = uint32_t((NR + 63) / 64) * kHalf;
+  // barriers, shifts, factors, and the warps' row sums (at NR = 256 these take a group's own half of P^T)
+  static constexpr uint32_t kMeta = kBarBytes + NR * 8 + (kPBufs == 2 ? NR * 16 : 0);
+  static constexpr int kFit = int((232448 - kMeta - kQ - kPBufs * kP) / kTile);
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static_assert(kStages >= 3, "ring");
   // the ring comes first: at d = 64 the second half of the V^T operand's M is whatever follows the tile
   static constexpr uint32_t kOffQ = kStages * kTile;
   static constexpr uint32_t kOffP = kOffQ + kQ;
-  static constexpr uint32_t kOffMeta = kOffP + kP;
+  static constexpr uint32_t kOffMeta = kOffP + kPBufs * kP;
   static constexpr uint32_t kSmem = kOffMeta + kMeta;
   static constexpr uint32_t kTmem = NR * 2 < 32 ? 32 : NR * 2;
 };
 
+// One stretch of a unit's tiles on this CTA, as the loading warp hands it to the others.
+struct Segment {
+  int n0, rows, len;       // first node; rows of the row tile (past NR: a full one); context length
+  int tile0, tiles;        // key tiles; tiles == 0: the end
+  int rt, head, unit;
+};
+constexpr int kSegRing = 4;
+
 struct Bars {
   uint64_t full[8], empty[8];
-  uint64_t q_full, s_full, s_free, p_ready, o_done, mma_done;
+  uint64_t q_full, s_full, s_free, p_ready[2], p_free[2], o_done, mma_done;
+  uint64_t seg_full[kSegRing], seg_empty[kSegRing];   // one arrival of the loading warp; of every reader
+  Segment seg[kSegRing];
   long long scan[20];
   long long rel;
   int seq;
@@ -121,15 +136,11 @@ struct Bars {
   int abort_flag;
   int bad[kMetaRing];
 };
-static_assert(sizeof(Bars) <= 512, "barrier block");
+static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
 
-// One stretch of a unit's tiles on this CTA.
-struct Segment {
-  SeqWork w;
-  int b, head, rt, tile0, tiles;
-};
+// The segments of a CTA's stretch of the line, in order.
 struct Walk {
-  long long left;   // tiles of this CTA's stretch not yet handed out
+  long long left;   // tiles not yet handed out
   int b, unit, tile;
   SeqWork w;
   bool bad;
@@ -149,10 +160,12 @@ struct Walk {
       w = seq_work(p, b, bad);
       unit = tile = 0;
     }
-    s.w = w;
-    s.b = b;
     s.head = unit / w.rts;
     s.rt = unit % w.rts;
+    s.n0 = w.n0;
+    s.rows = w.n * p.G - s.rt * p.Mt;
+    s.len = w.len;
+    s.unit = (b * p.Hkv + s.head) * p.RT + s.rt;
     s.tile0 = tile;
     s.tiles = int(min((long long)(w.nt - tile), left));
     left -= s.tiles;
@@ -170,7 +183,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars* bars = reinterpret_cast<Bars*>(smem + Dm::kOffMeta);
   // a row's shift: minus its reference (log2 units); -0.0: it has none yet (a reference of 0 is stored as +0.0)
-  float* s_nref = reinterpret_cast<float*>(smem + Dm::kOffMeta + 512);
+  float* s_nref = reinterpret_cast<float*>(smem + Dm::kOffMeta + kBarBytes);
   float* s_f = s_nref + NR;   // factor of a moved reference
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const WaitCtx wctx{&bars->abort_flag, p.status, kWaitLimitNs};
@@ -184,9 +197,16 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
     mbar_init(&bars->q_full, kSoftWarps);
     mbar_init(&bars->s_full, 1);
     mbar_init(&bars->s_free, kSoftWarps);
-    mbar_init(&bars->p_ready, kSoftWarps);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars->p_ready[i], kSoftWarps);   // by tile parity: a group may be a tile ahead of another
+      mbar_init(&bars->p_free[i], 1);
+    }
     mbar_init(&bars->o_done, 1);
     mbar_init(&bars->mma_done, 1);
+    for (int i = 0; i < kSegRing; ++i) {
+      mbar_init(&bars->seg_full[i], 1);
+      mbar_init(&bars->seg_empty[i], kSoftWarps + 1);
+    }
     bars->abort_flag = 0;
     mbar_fence_init();
   }
@@ -227,23 +247,21 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
   tc_fence_after();
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const uint32_t tmem = bars->tmem_base;
-  Walk walk;
-  walk.begin(p, work ? bars->seq : 0, work ? bars->rel : 0, n_tiles);
-  Segment sg;
-
   const int page = 1 << p.page_shift;
   const int box = min(page, kKeys);      // keys of a TMA box
 
   if (warp == kSoftWarps) {
     // ------------------------------------------------------------ TMA producer
-    uint32_t c = 0, kc = 0;
+    uint32_t c = 0, kc = 0, seg = 0;
     bool ok = true;
+    Walk walk;
+    walk.begin(p, work ? bars->seq : 0, work ? bars->rel : 0, n_tiles);
     const int boxes = kKeys / box;
     // lane l's page id of a tile (lanes past the tile's pages: none)
     auto page_of = [&](const Segment& s, int j) -> int {
       const int key = (s.tile0 + j) * kKeys + lane * box;
-      if (lane >= boxes || key >= s.w.len) return -2;      // no box
-      return p.table[s.b * p.table_row + (key >> p.page_shift)];
+      if (lane >= boxes || key >= s.len) return -2;        // no box
+      return p.table[walk.b * p.table_row + (key >> p.page_shift)];
     };
     auto load = [&](const CUtensorMap* map, const Segment& s, int j, int pg) -> bool {
       const int slot = int(c % Dm::kStages);
@@ -271,7 +289,16 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
       }
       ++kc;
     };
-    while (ok && walk.next(p, sg)) {
+    for (;;) {
+      Segment sg;
+      const bool more = walk.next(p, sg);
+      const int ring = int(seg % kSegRing);
+      if (!warp_wait(&bars->seg_empty[ring], ((seg / kSegRing) & 1) ^ 1, wctx, kFile + __LINE__)) { ok = false; break; }
+      if (!more) sg.tiles = 0;
+      if (lane == 0) bars->seg[ring] = sg;
+      warp_arrive(&bars->seg_full[ring]);
+      ++seg;
+      if (!more) break;
       int now = page_of(sg, 0), nxt = sg.tiles > 1 ? page_of(sg, 1) : -2;
       note(now);
       if (!load(&tm_k, sg, 0, now)) { ok = false; break; }
@@ -285,6 +312,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
         now = nxt;
         nxt = ahead;
       }
+      if (!ok) break;
     }
     if (!ok) bars->abort_flag = 1;
     // copies in flight land before the CTA may exit
@@ -315,22 +343,28 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
         ++c;
         return true;
       };
-      while (ok && walk.next(p, sg)) {
+      while (ok) {
+        const int at = int(seg % kSegRing);
+        if (!mbar_wait(&bars->seg_full[at], (seg / kSegRing) & 1, wctx, kFile + __LINE__)) { ok = false; break; }
+        const int tiles = bars->seg[at].tiles;
+        if (tiles == 0) break;
+        mbar_arrive(&bars->seg_empty[at]);
         if (!mbar_wait(&bars->q_full, seg & 1, wctx, kFile + __LINE__)) { ok = false; break; }
         ++seg;
         if (!issue_s(t)) { ok = false; break; }
-        for (int j = 0; j < sg.tiles; ++j, ++t) {
-          if (j + 1 < sg.tiles && !issue_s(t + 1)) { ok = false; break; }
+        for (int j = 0; j < tiles; ++j, ++t) {
+          if (j + 1 < tiles && !issue_s(t + 1)) { ok = false; break; }
           const int slot = int(c % Dm::kStages);
-          if (!mbar_wait(&bars->p_ready, t & 1, wctx, kFile + __LINE__)) { ok = false; break; }
+          if (!mbar_wait(&bars->p_ready[t & 1], (t >> 1) & 1, wctx, kFile + __LINE__)) { ok = false; break; }
           if (!mbar_wait(&bars->full[slot], (c / Dm::kStages) & 1, wctx, kFile + __LINE__)) { ok = false; break; }
           tc_fence_after();
           for (int kk = 0; kk < kKeys / 16; ++kk) {
             const uint64_t a = smem_desc_sw128(ring + slot * Dm::kTile + kk * 2048, kHalf, 1024);
-            const uint64_t b = smem_desc_sw128(sP + kk * 2048, kHalf, 1024);
+            const uint64_t b = smem_desc_sw128(sP + (Dm::kPBufs == 2 ? (t & 1) * Dm::kP : 0) + kk * 2048, kHalf, 1024);
             mma_ss(tmem + NR, a, b, kIdO, (j > 0 || kk > 0) ? 1u : 0u);
           }
           mma_commit(&bars->empty[slot]);
+          mma_commit(&bars->p_free[t & 1]);
           mma_commit(&bars->o_done);
           ++c;
         }
@@ -346,182 +380,232 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
     const int key_lane = wq * 32 + lane;               // key of a tile = TMEM lane; head element in O^T
     const int col0 = g * Dm::kCols;                    // this group's rows
     constexpr int kChunks = Dm::kCols / 32;
-    // Row sums of a thread: its own share of every row of the group; with four groups (few registers a thread) two
-    // neighbouring lanes add theirs at every tile and keep 16 of each chunk's 32 rows.
-    constexpr bool kPair = Dm::kGroups == 4;
+    constexpr bool kKeep = Dm::kPBufs == 2;            // scores stay in registers between the check and the exponentials
+    constexpr int kW = kKeep ? Dm::kCols : 16;         // rows of one pass of exponentials
+    // Row sums of a thread: its own share of every row of the group; at NR = 256 two neighbouring lanes add theirs at
+    // every tile and each keeps half.
+    constexpr bool kPair = !kKeep;
     constexpr int kL = kPair ? Dm::kCols / 2 : Dm::kCols;
     const bool odd = (lane & 1) != 0;
     const uint32_t tS = tmem + (uint32_t(wq * 32) << 16) + col0, tO = tS + NR;
-    uint8_t* my_p = smem + Dm::kOffP + g * kHalf + key_lane * 128;
+    // this thread's key row of P^T: 128 bytes of 64 rows, 16-byte chunks swizzled
+    uint8_t* my_p = smem + Dm::kOffP + (col0 >> 6) * kHalf + key_lane * 128;
+    const int pch0 = (col0 & 63) >> 3;
+    float* nref = s_nref + col0;
+    float* fac = s_f + col0;
     const float scale = p.scale_log2;
     uint32_t t = 0, ring0 = 0;      // tiles and ring slots of the segments before
     bool ok = true;
 
     auto load_q = [&](const Segment& s) {
       // rows col0.. of the tile into the K-major operand layout, rows past the tile's end zero
-      const int rows = s.w.n * p.G - s.rt * NR;
       constexpr int kCh = D / 8;
+      const int n_rows = s.rows, n0 = s.n0, first = s.rt * NR, h0 = s.head * p.G;
       for (int i = tid & 127; i < Dm::kCols * kCh; i += 128) {
         const int r = col0 + i / kCh, ch = i % kCh;
         uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < rows) {
-          const int row = s.rt * NR + r, node = row / p.G, h = s.head * p.G + row - node * p.G;
-          x = __ldg(reinterpret_cast<const uint4*>(p.q + int64_t(s.w.n0 + node) * p.q_node + int64_t(h) * p.q_head + ch * 16));
+        if (r < n_rows) {
+          const int row = first + r, node = row / p.G, h = h0 + row - node * p.G;
+          x = __ldg(reinterpret_cast<const uint4*>(p.q + int64_t(n0 + node) * p.q_node + int64_t(h) * p.q_head + ch * 16));
         }
         *reinterpret_cast<uint4*>(smem + Dm::kOffQ + (ch >> 3) * (NR * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x;
       }
       fence_async_smem();
       warp_arrive(&bars->q_full);
     };
-
-    // After a wait gave up (ok is false, the kernel winds down) a warp walks on without waiting, so that its group's
-    // barriers still meet; what it writes is inside its records.
-    bool more = walk.next(p, sg);
-    if (more) load_q(sg);
+    // After a wait gave up (ok is false, the kernel winds down) a warp goes on without waiting to the end of its segment,
+    // where the group leaves together: its barriers always meet.  What is written until then lies inside its records.
+    auto open = [&](uint32_t i) -> bool {
+      ok = ok && warp_wait(&bars->seg_full[i % kSegRing], (i / kSegRing) & 1, wctx, kFile + __LINE__);
+      if (group_any(g, !ok)) return false;
+      return bars->seg[i % kSegRing].tiles > 0;
+    };
+    uint32_t seg = 0;
+    bool more = open(0);
+    if (more) load_q(bars->seg[0]);
     while (more) {
-      const Segment s = sg;
-      const int rows = min(NR, s.w.n * p.G - s.rt * NR);
-      const int live = max(0, min(kChunks, (rows - col0 + 31) / 32));   // chunks with rows
+      const Segment& s = bars->seg[seg % kSegRing];
+      const int rows = min(NR, s.rows), len = s.len, tiles = s.tiles;
+      const int live = max(0, min(kChunks, (rows - col0 + 31) / 32));   // chunks of 32 with rows
       float l[kL];
 #pragma unroll
       for (int i = 0; i < kL; ++i) l[i] = 0.f;
-      if ((tid & 127) < Dm::kCols) s_nref[col0 + (tid & 127)] = -0.0f;
-      bool need = true;       // a row has no reference yet
+      if ((tid & 127) < Dm::kCols) nref[tid & 127] = -0.0f;
+      bool need = live > 0;       // a row has no reference yet
       group_sync(g);
-      for (int j = 0; j < s.tiles; ++j, ++t) {
-        const int key = (s.tile0 + j) * kKeys + key_lane;
+      int end = (s.tile0 + 1) * kKeys;     // behind the tile's last key
+      for (int j = 0; j < tiles; ++j, ++t, end += kKeys) {
+        const int key = end - kKeys + key_lane;
         ok = ok && warp_wait(&bars->s_full, t & 1, wctx, kFile + __LINE__);
         tc_fence_after();
         const uint32_t wrong = uint32_t(bars->bad[t % kMetaRing]);
-        const bool valid = key < s.w.len && !((wrong >> (key_lane / box)) & 1u);
-        const bool part = wrong != 0 || (s.tile0 + j + 1) * kKeys > s.w.len;
-        bool first_need = need;
-        bool still = false;
-        bool waited = false;
+        const bool valid = key < len && !((wrong >> (key_lane / box)) & 1u);
+        const bool part = wrong != 0 || end > len;
+        // scores in log2 units, shifted by the rows' references; is one of them past the headroom?
+        float x[kW];
+        float mx = -INFINITY;
+        if (!need) {
 #pragma unroll
-        for (int ch = 0; ch < kChunks; ++ch) {
-          if (ch < live) {
-            uint32_t v[32];
-            tmem_ld32(tS + ch * 32, v);
-            tmem_wait_ld();
-            reg_fence<32>(v);
-            if (ch == live - 1) {
-              tc_fence_before();
-              warp_arrive(&bars->s_free);
+          for (int e = 0; e < Dm::kCols; e += 16) {
+            if (e < live * 32) {
+              uint32_t v[16];
+              tmem_ld16(tS + e, v);
+              tmem_wait_ld();
+              reg_fence<16>(v);
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                const float4 r = *reinterpret_cast<const float4*>(nref + e + i);
+                float y0, y1, y2, y3;
+                ffma2(y0, y1, __uint_as_float(v[i]), __uint_as_float(v[i + 1]), scale, scale, r.x, r.y);
+                ffma2(y2, y3, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]), scale, scale, r.z, r.w);
+                mx = fmax3(mx, y0, y1);
+                mx = fmax3(mx, y2, y3);
+                if constexpr (kKeep) {
+                  x[e + i] = y0;
+                  x[e + i + 1] = y1;
+                  x[e + i + 2] = y2;
+                  x[e + i + 3] = y3;
+                }
+              }
             }
-            float* nref = s_nref + col0 + ch * 32;
-            float* fac = s_f + col0 + ch * 32;
-            float x[32];
-            bool over = first_need;
-            if (!first_need) {
-              float mx = -INFINITY;
+          }
+        }
+        bool over = need;
+        if (!need && live > 0) over = group_any(g, valid && mx > kHeadroom);
+        if (over) {
+          need = false;
+#pragma unroll 1
+          for (int ch = 0; ch < live; ++ch) {
+            float* nr = nref + ch * 32;
+            float* fc = fac + ch * 32;
+            // new references of this chunk's rows: lane i of every warp gets column i's maximum
+            float m = -INFINITY;
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const float4 r = *reinterpret_cast<const float4*>(nref + i);
+            for (int e = 0; e < 32; e += 16) {
+              uint32_t v[16];
+              tmem_ld16(tS + ch * 32 + e, v);
+              tmem_wait_ld();
+              reg_fence<16>(v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float y = warp_max(valid ? __uint_as_float(v[i]) * scale : -INFINITY);
+                m = lane == e + i ? y : m;
+              }
+            }
+            // exchanged through the factors' and shifts' slots of this chunk, two warps at a time
+            const uint32_t was = __float_as_uint(nr[lane]);
+            const float old = was == 0x80000000u ? -INFINITY : -__uint_as_float(was);
+            group_sync(g);
+            if (wq == 0) fc[lane] = m;
+            if (wq == 1) nr[lane] = m;
+            group_sync(g);
+            if (wq == 2) fc[lane] = fmaxf(fc[lane], m);
+            if (wq == 3) nr[lane] = fmaxf(nr[lane], m);
+            group_sync(g);
+            m = fmaxf(fc[lane], nr[lane]);
+            const float to = old == -INFINITY ? m : (m > old + kHeadroom ? m : old);
+            const float f = old == -INFINITY ? 1.f : fast_exp2(old - to);
+            group_sync(g);
+            if (wq == 0) {
+              nr[lane] = to == -INFINITY ? -0.0f : 0.f - to;
+              fc[lane] = f;
+            }
+            const bool moved = group_any(g, f != 1.f);
+            need |= group_any(g, to == -INFINITY);
+            if (moved) {
+#pragma unroll
+              for (int c = 0; c < kChunks; ++c) {
+                if (c == ch) {
+                  constexpr int kN = kL / kChunks;
+#pragma unroll
+                  for (int i = 0; i < kN; ++i) l[c * kN + i] *= fc[kPair ? (i / 8) * 16 + (odd ? 8 : 0) + i % 8 : i];
+                }
+              }
+              if (j > 0) {
+                ok = ok && warp_wait(&bars->o_done, (t - 1) & 1, wctx, kFile + __LINE__);
+                tc_fence_after();
+#pragma unroll 1
+                for (int e = 0; e < 32; e += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(tO + ch * 32 + e, o);
+                  tmem_wait_ld();
+                  reg_fence<16>(o);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fc[e + i]);
+                  tmem_st16(tO + ch * 32 + e, o);
+                }
+                tmem_wait_st();
+              }
+            }
+          }
+          if constexpr (kKeep) {
+#pragma unroll
+            for (int e = 0; e < Dm::kCols; e += 16) {
+              uint32_t v[16];
+              tmem_ld16(tS + e, v);
+              tmem_wait_ld();
+              reg_fence<16>(v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) x[e + i] = fmaf(__uint_as_float(v[i]), scale, nref[e + i]);
+            }
+          }
+        }
+        if (kKeep || live == 0) {
+          tc_fence_before();
+          warp_arrive(&bars->s_free);
+        }
+        // this P^T buffer may be rewritten once the product that read it is done
+        constexpr uint32_t kB = Dm::kPBufs;
+        if (t >= kB)
+          ok = ok && warp_wait(&bars->p_free[(t - kB) & 1], ((t - kB) >> 1) & 1, wctx, kFile + __LINE__);
+        uint8_t* pp = my_p + (kB == 2 ? (t & 1) * Dm::kP : 0);
+#pragma unroll
+        for (int w = 0; w < Dm::kCols / kW; ++w) {
+          if (w * kW < live * 32) {
+            if constexpr (!kKeep) {
+              uint32_t v[16];
+              tmem_ld16(tS + w * kW, v);
+              tmem_wait_ld();
+              reg_fence<16>(v);
+              if ((w + 1) * kW == live * 32) {
+                tc_fence_before();
+                warp_arrive(&bars->s_free);
+              }
+#pragma unroll
+              for (int i = 0; i < 16; i += 4) {
+                const float4 r = *reinterpret_cast<const float4*>(nref + w * kW + i);
                 ffma2(x[i], x[i + 1], __uint_as_float(v[i]), __uint_as_float(v[i + 1]), scale, scale, r.x, r.y);
                 ffma2(x[i + 2], x[i + 3], __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]), scale, scale, r.z, r.w);
-                mx = fmax3(mx, x[i], x[i + 1]);
-                mx = fmax3(mx, x[i + 2], x[i + 3]);
               }
-              over = group_any(g, valid && mx > kHeadroom);
-            }
-            if (over) {
-              // new references for this chunk's rows: lane i of every warp gets column i's maximum
-              float m = -INFINITY;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float y = warp_max(valid ? __uint_as_float(v[i]) * scale : -INFINITY);
-                m = lane == i ? y : m;
-              }
-              // exchanged through the factors' and shifts' slots of this chunk, two warps at a time
-              const uint32_t was = __float_as_uint(nref[lane]);
-              const float old = was == 0x80000000u ? -INFINITY : -__uint_as_float(was);
-              group_sync(g);
-              if (wq == 0) fac[lane] = m;
-              if (wq == 1) nref[lane] = m;
-              group_sync(g);
-              if (wq == 2) fac[lane] = fmaxf(fac[lane], m);
-              if (wq == 3) nref[lane] = fmaxf(nref[lane], m);
-              group_sync(g);
-              m = fmaxf(fac[lane], nref[lane]);
-              const float to = old == -INFINITY ? m : (m > old + kHeadroom ? m : old);
-              const float f = old == -INFINITY ? 1.f : fast_exp2(old - to);
-              group_sync(g);
-              if (wq == 0) {
-                nref[lane] = to == -INFINITY ? -0.0f : 0.f - to;
-                fac[lane] = f;
-              }
-              const bool moved = group_any(g, f != 1.f);
-              still |= group_any(g, to == -INFINITY);
-              if (moved) {
-                if constexpr (kPair) {
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) l[ch * 16 + i] *= fac[(odd ? 16 : 0) + i];
-                } else {
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) l[ch * 32 + i] *= fac[i];
-                }
-                if (j > 0) {
-                  ok = ok && warp_wait(&bars->o_done, (t - 1) & 1, wctx, kFile + __LINE__);
-                  waited = true;
-                  tc_fence_after();
-#pragma unroll 1
-                  for (int e = 0; e < 32; e += 16) {
-                    uint32_t o[16];
-                    tmem_ld16(tO + ch * 32 + e, o);
-                    tmem_wait_ld();
-                    reg_fence<16>(o);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fac[e + i]);
-                    tmem_st16(tO + ch * 32 + e, o);
-                  }
-                  tmem_wait_st();
-                }
-              }
-#pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = fmaf(__uint_as_float(v[i]), scale, nref[i]);
             }
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = fast_exp2(x[i]);
+            for (int i = 0; i < kW; ++i) x[i] = fast_exp2(x[i]);
             if (part) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = valid ? x[i] : 0.f;
+              for (int i = 0; i < kW; ++i) x[i] = valid ? x[i] : 0.f;
             }
             if constexpr (kPair) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float y = __shfl_xor_sync(0xffffffffu, odd ? x[i] : x[16 + i], 1);
-                l[ch * 16 + i] += (odd ? x[16 + i] : x[i]) + y;
+              for (int i = 0; i < 8; ++i) {
+                const float y = __shfl_xor_sync(0xffffffffu, odd ? x[i] : x[8 + i], 1);
+                l[w * 8 + i] += (odd ? x[8 + i] : x[i]) + y;
               }
             } else {
 #pragma unroll
-              for (int i = 0; i < 32; i += 2)
-                fadd2(l[ch * 32 + i], l[ch * 32 + i + 1], l[ch * 32 + i], l[ch * 32 + i + 1], x[i], x[i + 1]);
-            }
-            // P^T may be rewritten once the product before has read it
-            if (t > 0 && !waited) {
-              ok = ok && warp_wait(&bars->o_done, (t - 1) & 1, wctx, kFile + __LINE__);
-              waited = true;
+              for (int i = 0; i < kW; i += 2) fadd2(l[i], l[i + 1], l[i], l[i + 1], x[i], x[i + 1]);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              *reinterpret_cast<uint4*>(my_p + (((ch * 4 + i) ^ (key_lane & 7)) << 4)) =
+            for (int i = 0; i < kW / 8; ++i)
+              *reinterpret_cast<uint4*>(pp + (((pch0 + w * (kW / 8) + i) ^ (key_lane & 7)) << 4)) =
                   make_uint4(pack<T>(x[8 * i], x[8 * i + 1]), pack<T>(x[8 * i + 2], x[8 * i + 3]),
                              pack<T>(x[8 * i + 4], x[8 * i + 5]), pack<T>(x[8 * i + 6], x[8 * i + 7]));
           }
         }
-        if (live == 0) {
-          warp_arrive(&bars->s_free);
-        } else {
-          need = still;
-        }
-        // (a group without rows keeps step: its arrival must not fall into the tile before)
-        if (t > 0 && !waited) ok = ok && warp_wait(&bars->o_done, (t - 1) & 1, wctx, kFile + __LINE__);
-        if (g == 0 && (s.tile0 + j + 1) * kKeys > s.w.len) {
+        if (g == 0 && end > len) {
           // the context ends inside this tile, the unit's last: V rows behind it become zeros
-          const uint32_t i = ring0 + 2 * s.tiles - 1;
+          const uint32_t i = ring0 + 2 * tiles - 1;
           ok = ok && warp_wait(&bars->full[i % Dm::kStages], (i / Dm::kStages) & 1, wctx, kFile + __LINE__);
-          if (ok && key >= s.w.len) {
+          if (ok && key >= len) {
             for (int h = 0; h < D / 64; ++h)
               for (int e = 0; e < 8; ++e)
                 *reinterpret_cast<uint4*>(smem + (i % Dm::kStages) * Dm::kTile + h * kHalf + key_lane * 128 + e * 16) =
@@ -530,15 +614,15 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
         }
         fence_async_smem();
         tc_fence_before();
-        warp_arrive(&bars->p_ready);
+        warp_arrive(&bars->p_ready[t & 1]);
       }
-      ring0 += 2 * s.tiles;
+      ring0 += 2 * tiles;
       // the next unit's queries (the last scores of this one are done), so that its first scores overlap this epilogue
-      more = walk.next(p, sg);
-      if (more) load_q(sg);
+      more = open(seg + 1);
+      if (more) load_q(bars->seg[(seg + 1) % kSegRing]);
       ok = ok && warp_wait(&bars->o_done, (t - 1) & 1, wctx, kFile + __LINE__);
       tc_fence_after();
-      const size_t rec = size_t(blockIdx.x) + (size_t(s.b) * p.Hkv + s.head) * p.RT + s.rt;
+      const size_t rec = size_t(blockIdx.x) + s.unit;
       float* dst = p.rec_o + (rec * NR + col0) * D + key_lane;
 #pragma unroll 1
       for (int ch = 0; ch < live; ++ch) {
@@ -555,7 +639,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
       tc_fence_before();
       // row sums: over the warp's lanes (each step leaves half the rows to a lane), then over the four warps
       if (live > 0) {
-        int r = 0;       // this lane's first row after the steps
+        int r = 0;       // this lane's first sum after the steps
 #pragma unroll
         for (int st = 16, n = kL / 2; st > (kPair ? 1 : 0); st >>= 1, n >>= 1) {
           const bool up = (lane & st) != 0;
@@ -567,23 +651,26 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
           }
           r += up ? n : 0;
         }
-        float* s_l = reinterpret_cast<float*>(smem + Dm::kOffP + g * kHalf);   // P^T of this group: read by no product now
+        float* s_l = Dm::kPBufs == 2 ? s_f + NR + g * (4 * Dm::kCols)
+                                     : reinterpret_cast<float*>(smem + Dm::kOffP + g * kHalf);   // read by no product now
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
           const int e = r + i;
-          s_l[wq * 64 + (kPair ? (e / 16) * 32 + (odd ? 16 : 0) + e % 16 : e)] = l[i];
+          s_l[wq * Dm::kCols + (kPair ? (e / 8) * 16 + (odd ? 8 : 0) + e % 8 : e)] = l[i];
         }
         group_sync(g);
         const int row = tid & 127;
         if (row < Dm::kCols && col0 + row < rows)
         {
-          const float nr = s_nref[col0 + row];
+          const float nr = nref[row];
           p.rec_ml[rec * NR + col0 + row] =
               make_float2(__float_as_uint(nr) == 0x80000000u ? -INFINITY : -nr,
-                          s_l[row] + s_l[64 + row] + s_l[128 + row] + s_l[192 + row]);
+                          s_l[row] + s_l[Dm::kCols + row] + s_l[2 * Dm::kCols + row] + s_l[3 * Dm::kCols + row]);
         }
         group_sync(g);
       }
+      warp_arrive(&bars->seg_empty[seg % kSegRing]);
+      ++seg;
     }
     if (!ok) bars->abort_flag = 1;
   }
