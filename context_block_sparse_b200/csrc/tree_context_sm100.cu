@@ -94,9 +94,9 @@ __device__ __forceinline__ float warp_max(float x) {
 
 template <int D, int NR>
 struct Dims {
-  // Rows (TMEM columns) of a softmax group.  A thread keeps its scores in registers from the check to the
-  // exponentials, except at NR = 256, where it has 96 of them: scores are read twice, 16 at a time.
-  static constexpr int kCols = NR <= 64 ? 32 : 64;
+  // Rows (TMEM columns) of a softmax group.  With one or two groups a thread keeps its scores in registers from the
+  // check to the exponentials; with four it has 96 registers, and scores are read twice, 16 at a time.
+  static constexpr int kCols = NR <= 128 ? 32 : 64;
   static constexpr int kGroups = NR / kCols;
   static constexpr int kThreads = 128 * kGroups + 64;
   static constexpr int kPBufs = NR <= 128 ? 2 : 1;           // P^T buffers
@@ -380,11 +380,11 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
     const int key_lane = wq * 32 + lane;               // key of a tile = TMEM lane; head element in O^T
     const int col0 = g * Dm::kCols;                    // this group's rows
     constexpr int kChunks = Dm::kCols / 32;
-    constexpr bool kKeep = Dm::kPBufs == 2;            // scores stay in registers between the check and the exponentials
+    constexpr bool kKeep = NR <= 64;                   // scores stay in registers between the check and the exponentials
     constexpr int kW = kKeep ? Dm::kCols : 16;         // rows of one pass of exponentials
     // Row sums of a thread: its own share of every row of the group; at NR = 256 two neighbouring lanes add theirs at
     // every tile and each keeps half.
-    constexpr bool kPair = !kKeep;
+    constexpr bool kPair = NR == 256;
     constexpr int kL = kPair ? Dm::kCols / 2 : Dm::kCols;
     const bool odd = (lane & 1) != 0;
     const uint32_t tS = tmem + (uint32_t(wq * 32) << 16) + col0, tO = tS + NR;
@@ -592,7 +592,8 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
               }
             } else {
 #pragma unroll
-              for (int i = 0; i < kW; i += 2) fadd2(l[i], l[i + 1], l[i], l[i + 1], x[i], x[i + 1]);
+              for (int i = 0; i < kW; i += 2)
+                fadd2(l[w * kW + i], l[w * kW + i + 1], l[w * kW + i], l[w * kW + i + 1], x[i], x[i + 1]);
             }
 #pragma unroll
             for (int i = 0; i < kW / 8; ++i)
