@@ -2,12 +2,11 @@
 // row tile) against the sequence's cached keys, for row tiles of 32 to 256 rows.
 //
 // A row tile's keys stream past it once, so the kernel wants HBM speed: a 128-key tile of K and V
-// (64 KB at d = 128) reaches an SM every ~2700 clocks.  A tcgen05.mma with M = 128, K = 16 costs
-// ~129 clocks for every N from 64 to 256, so both products are transposed, with keys and the head
-// dimension as M and the rows as N:
+// (64 KB at d = 128) reaches an SM every ~2700 clocks.  A tcgen05.mma needs M = 128 (or 64) rows in
+// its A operand, and draft trees have 4 to 256 rows a KV head; so both products are transposed, with
+// keys and the head dimension as M and the rows as N:
 //   S^T [128 keys x N rows] = K Q^T,     O^T [d x N rows] += V^T P^T,
-// 16 instructions a tile at d = 128 whatever the rows (2064 clocks), where rows as M would pay that
-// for every 128 of them.
+// 16 instructions a tile at d = 128, of 40 / 48 / 64 / 128 clocks at N = 32 / 64 / 128 / 256 (measured).
 //
 // In S^T a TMEM lane is a key, so a softmax thread holds one key's scores of 64 rows (32 at a time).
 // Its row maxima would need 128 lanes' agreement at every tile; instead a row keeps a reference, the
@@ -324,7 +323,12 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       constexpr uint32_t kIdS = idesc(kIsF16<T>, kKeys, NR, 0, 0), kIdO = idesc(kIsF16<T>, 128, NR, 1, 1);
-      const uint32_t ring = smem_u32(smem), sQ = smem_u32(smem + Dm::kOffQ), sP = smem_u32(smem + Dm::kOffP);
+      // Operand descriptors of the first tile; a tile's or a step's offset is added to the address field (16-byte
+      // units, no carry out of it).  Building them at each instruction instead made this thread's integer code the
+      // limit: ~200 clocks an instruction, where N = 64 / 128 / 256 take 48 / 64 / 128.
+      const uint64_t dK = smem_desc_sw128(smem_u32(smem), 16, 1024), dV = smem_desc_sw128(smem_u32(smem), kHalf, 1024);
+      const uint64_t dQ = smem_desc_sw128(smem_u32(smem + Dm::kOffQ), 16, 1024);
+      const uint64_t dP = smem_desc_sw128(smem_u32(smem + Dm::kOffP), kHalf, 1024);
       uint32_t c = 0, t = 0, seg = 0;     // ring slots, tiles, segments so far
       bool ok = true;
       // scores of the next tile: S^T = K Q^T once its K has landed and the scores before are read
@@ -333,11 +337,11 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
         if (tile > 0 && !mbar_wait(&bars->s_free, (tile - 1) & 1, wctx, kFile + __LINE__)) return false;
         if (!mbar_wait(&bars->full[slot], (c / Dm::kStages) & 1, wctx, kFile + __LINE__)) return false;
         tc_fence_after();
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t a = smem_desc_sw128(ring + slot * Dm::kTile + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024);
-          const uint64_t b = smem_desc_sw128(sQ + (kk >> 2) * (NR * 128) + (kk & 3) * 32, 16, 1024);
-          mma_ss(tmem, a, b, kIdS, kk > 0 ? 1u : 0u);
-        }
+        const uint64_t a = dK + (uint32_t(slot) * Dm::kTile >> 4);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          mma_ss(tmem, a + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), dQ + (((kk >> 2) * (NR * 128) + (kk & 3) * 32) >> 4),
+                 kIdS, kk > 0 ? 1u : 0u);
         mma_commit(&bars->empty[slot]);
         mma_commit(&bars->s_full);
         ++c;
@@ -358,11 +362,11 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
           if (!mbar_wait(&bars->p_ready[t & 1], (t >> 1) & 1, wctx, kFile + __LINE__)) { ok = false; break; }
           if (!mbar_wait(&bars->full[slot], (c / Dm::kStages) & 1, wctx, kFile + __LINE__)) { ok = false; break; }
           tc_fence_after();
-          for (int kk = 0; kk < kKeys / 16; ++kk) {
-            const uint64_t a = smem_desc_sw128(ring + slot * Dm::kTile + kk * 2048, kHalf, 1024);
-            const uint64_t b = smem_desc_sw128(sP + (Dm::kPBufs == 2 ? (t & 1) * Dm::kP : 0) + kk * 2048, kHalf, 1024);
-            mma_ss(tmem + NR, a, b, kIdO, (j > 0 || kk > 0) ? 1u : 0u);
-          }
+          const uint64_t a = dV + (uint32_t(slot) * Dm::kTile >> 4);
+          const uint64_t b = dP + (Dm::kPBufs == 2 ? (t & 1) * (Dm::kP >> 4) : 0u);
+#pragma unroll
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            mma_ss(tmem + NR, a + (kk * 2048 >> 4), b + (kk * 2048 >> 4), kIdO, kk > 0 ? 1u : (j > 0 ? 1u : 0u));
           mma_commit(&bars->empty[slot]);
           mma_commit(&bars->p_free[t & 1]);
           mma_commit(&bars->o_done);
