@@ -41,10 +41,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kChunk = 1024;            // vocabulary entries of one warp step
+constexpr int kChunk = 512;             // vocabulary entries of one warp step
 constexpr int kPerLane = kChunk / 32;
 constexpr int kMaxNodes = 1024;
-constexpr int kMaxChunks = 2048;        // chunks of one CTA's slice
+constexpr int kMaxVocab = 1 << 21;
+constexpr int kMaxChunks = kMaxVocab / kChunk / 8 + 1;   // chunks of one CTA's slice (a cluster of eight)
 constexpr int kMaxCluster = 8;
 
 struct VerifyParams {
@@ -58,19 +59,37 @@ struct VerifyParams {
   int* status;
   int64_t path_row;
   int Nq, V, max_nodes, max_path, tok64;
-  int chunks_per_cta;
 };
 
 __device__ __forceinline__ float val(float x) { return x; }
 __device__ __forceinline__ float val(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float val(__half x) { return __half2float(x); }
 
-// A probability as it counts: entries that are negative, infinite or NaN have no mass.
+// A probability as it counts: entries that are negative, infinite or NaN have no mass (one unsigned comparison of
+// the bits of 2^-149 .. the largest finite number).
 template <typename T>
-__device__ __forceinline__ double mass(T x) {
+__device__ __forceinline__ float mass(T x) {
   const float f = val(x);
-  return f > 0.f && f < INFINITY ? double(f) : 0.0;
+  return __float_as_uint(f) - 1u < 0x7f7fffffu ? f : 0.f;
 }
+
+// Unevaluated sums hi + lo of two floats, ~48 bits: the vocabulary-long sums need more than float32, and float64
+// conversions run at a sixteenth of the float32 rate here (the same pass in float64 took 19,000 clocks, not 5,000).
+// Knuth's two-sum: a + b = s + e exactly.
+__device__ __forceinline__ void two_sum(float a, float b, float& s, float& e) {
+  s = __fadd_rn(a, b);
+  const float bb = __fsub_rn(s, a);
+  e = __fadd_rn(__fsub_rn(a, __fsub_rn(s, bb)), __fsub_rn(b, bb));
+}
+struct Sum {
+  float hi = 0.f, lo = 0.f;
+  __device__ __forceinline__ void add(float h, float l) {
+    float e;
+    two_sum(hi, h, hi, e);
+    lo = __fadd_rn(lo, __fadd_rn(e, l));
+  }
+  __device__ __forceinline__ double value() const { return double(hi) + double(lo); }
+};
 
 template <typename T, int N>
 struct alignas(sizeof(T) * N) Pack {
@@ -83,51 +102,74 @@ struct Residual {
   const T* p;
   const T* q;          // NULL: certainty drafts, `removed` tokens have no mass left
   double c;
+  float ch, cl;        // c as hi + lo
   const int* removed;
   int n_removed;
-  __device__ __forceinline__ double at(T pv, T qv, int i) const {
-    double r = mass(pv);
+  __device__ __forceinline__ void set_c(double x) {
+    c = x;
+    ch = float(x);
+    cl = float(x - double(ch));
+  }
+  // R of entry i with p = pv, q = qv, as hi + lo
+  __device__ __forceinline__ void at(T pv, T qv, int i, float& h, float& l) const {
+    h = mass(pv);
+    l = 0.f;
     if (q != nullptr) {
-      r = fmax(r - c * mass(qv), 0.0);
+      const float b = mass(qv);
+      const float x = __fmul_rn(ch, b);
+      const float xe = __fmaf_rn(cl, b, __fmaf_rn(ch, b, -x));   // c q = x + xe
+      two_sum(h, -x, h, l);
+      l = __fsub_rn(l, xe);
+      if (!(__fadd_rn(h, l) > 0.f)) h = l = 0.f;
     } else {
       for (int k = 0; k < n_removed; ++k)
-        if (removed[k] == i) r = 0.0;
+        if (removed[k] == i) h = 0.f;
     }
-    return r;
   }
 };
 
-// This lane's share of chunk [base, base + kChunk): N-element vectors, lane-interleaved.
+// This lane's share of the chunk of entries [base, base + kChunk), in N-element vectors that sit on 16-byte
+// boundaries (base may be negative, and the chunk may end behind the row: those entries are not there).
 template <typename T, int N>
 __device__ __forceinline__ double chunk_sum(const Residual<T>& R, int base, int V, int lane) {
-  double s = 0.0;
-  constexpr int kBatch = 8;   // vectors of each row in flight
+  Sum s;
+  constexpr int kSteps = kPerLane / N, kBatch = N == 1 ? 8 : 16 / N;   // vectors of a row in flight
+  const bool both = R.q != nullptr && R.c != 0.0;
 #pragma unroll 1
-  for (int j0 = 0; j0 < kPerLane / N; j0 += kBatch) {
+  for (int j0 = 0; j0 < kSteps; j0 += kBatch) {
     Pack<T, N> a[kBatch], b[kBatch];
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const int i = base + ((j0 + j) * 32 + lane) * N;
-      if (j0 + j < kPerLane / N && i < V) {
+      if (i >= 0 && i + N <= V) {
         a[j] = *reinterpret_cast<const Pack<T, N>*>(R.p + i);
-        if (R.q != nullptr && R.c != 0.0) b[j] = *reinterpret_cast<const Pack<T, N>*>(R.q + i);
+        if (both) b[j] = *reinterpret_cast<const Pack<T, N>*>(R.q + i);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          const bool there = i + e >= 0 && i + e < V;
+          a[j].v[e] = there ? R.p[i + e] : T(0.f);
+          if (both) b[j].v[e] = there ? R.q[i + e] : T(0.f);
+        }
       }
     }
 #pragma unroll
     for (int j = 0; j < kBatch; ++j) {
       const int i = base + ((j0 + j) * 32 + lane) * N;
-      if (j0 + j < kPerLane / N && i < V) {
-        if (R.q != nullptr && R.c == 0.0) {
+      if (R.q != nullptr && !both) {
 #pragma unroll
-          for (int e = 0; e < N; ++e) s += mass(a[j].v[e]);
-        } else {
+        for (int e = 0; e < N; ++e) s.add(mass(a[j].v[e]), 0.f);
+      } else {
 #pragma unroll
-          for (int e = 0; e < N; ++e) s += R.at(a[j].v[e], b[j].v[e], i + e);
+        for (int e = 0; e < N; ++e) {
+          float h, l;
+          R.at(a[j].v[e], b[j].v[e], i + e, h, l);
+          s.add(h, l);
         }
       }
     }
   }
-  return s;
+  return s.value();
 }
 
 __device__ __forceinline__ double warp_sum(double s) {
@@ -136,8 +178,35 @@ __device__ __forceinline__ double warp_sum(double s) {
   return s;
 }
 
+// One warp's values x on top of a running sum: the first lane whose sum exceeds the goal (-1: none) and the last lane
+// with mass (-1: none), with the sums before them and behind all lanes.
+struct Picked {
+  int at, last;
+  double run_at, run_last, run_end;
+};
+__device__ __forceinline__ Picked pick(double x, double goal, double run) {
+  const int lane = threadIdx.x & 31;
+  double inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  double exc = __shfl_up_sync(0xffffffffu, inc, 1);
+  if (lane == 0) exc = 0.0;
+  const unsigned over = __ballot_sync(0xffffffffu, x > 0.0 && run + inc > goal);
+  const unsigned pos = __ballot_sync(0xffffffffu, x > 0.0);
+  Picked r;
+  r.at = over ? __ffs(over) - 1 : -1;
+  r.last = pos ? 31 - __clz(pos) : -1;
+  r.run_at = run + __shfl_sync(0xffffffffu, exc, r.at < 0 ? 0 : r.at);
+  r.run_last = run + __shfl_sync(0xffffffffu, exc, r.last < 0 ? 0 : r.last);
+  r.run_end = run + __shfl_sync(0xffffffffu, inc, 31);
+  return r;
+}
+
 template <typename T, int N>
-__global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyParams p) {
+__global__ void __launch_bounds__(kThreads, 3) tree_verify_kernel(const VerifyParams p) {
   cg::cluster_group cluster = cg::this_cluster();
   const int rank = int(cluster.block_rank()), ranks = int(cluster.num_blocks());
   const int b = int(blockIdx.x) / ranks;
@@ -147,7 +216,9 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyParam
   __shared__ float s_p[kMaxNodes], s_q[kMaxNodes], s_u[kMaxNodes];
   __shared__ double s_chunk[kMaxChunks];
   __shared__ double s_total[2];   // this CTA's slice sum, by pass parity
-  __shared__ int s_found;
+  __shared__ int s_found, s_last;
+  __shared__ double s_warp[kWarps];
+  __shared__ uint8_t s_first[kMaxNodes];   // accepted as its parent's first child
 
   const int n0 = p.node_ptr[b], n1 = p.node_ptr[b + 1];
   int n = n1 - n0;
@@ -169,26 +240,37 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyParam
     }
     float pv = 0.f, qv = 1.f;
     if (i > 0 && par >= 0) {
-      pv = float(mass(target[int64_t(n0 + par) * p.target_row + tok]));
-      if (draft != nullptr) qv = float(mass(draft[int64_t(n0 + par) * p.draft_row + tok]));
+      pv = mass(target[int64_t(n0 + par) * p.target_row + tok]);
+      if (draft != nullptr) qv = mass(draft[int64_t(n0 + par) * p.draft_row + tok]);
     }
     s_parent[i] = par;
     s_tok[i] = int(tok);
     s_p[i] = pv;
     s_q[i] = qv;
-    s_u[i] = p.u_accept[n0 + i];
+    const float u = p.u_accept[n0 + i];
+    s_u[i] = u;
+    s_first[i] = double(u) * double(qv) < double(pv);
   }
-  if (tid == 0) s_found = -1;
+  if (tid == 0) {
+    s_found = 0x7fffffff;
+    s_last = -1;
+  }
   __syncthreads();
 
   Residual<T> R;
   R.removed = s_removed;
   R.p = target + int64_t(n0) * p.target_row;
   R.q = draft ? draft + int64_t(n0) * p.draft_row : nullptr;
-  R.c = 0.0;
+  R.set_c(0.0);
   R.n_removed = 0;
-  const int c0 = rank * p.chunks_per_cta;   // this CTA's chunks
-  const int nc = max(0, min(p.chunks_per_cta, (V + kChunk - 1) / kChunk - c0));
+  // Chunks are cut at 16-byte boundaries: the current row begins `shift` entries behind one (the same in both rows).
+  int shift = 0, c0 = 0, nc = 0;            // this CTA's chunks
+  auto place = [&]() {
+    shift = N == 1 ? 0 : int(reinterpret_cast<uintptr_t>(R.p) / sizeof(T) % N);
+    const int all = (V + shift + kChunk - 1) / kChunk, per = (all + ranks - 1) / ranks;
+    c0 = rank * per;
+    nc = max(0, min(per, all - c0));
+  };
   int pass = 0;
   double before = 0.0;   // mass of the slices before this CTA's
 
@@ -196,8 +278,9 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyParam
   // cluster calls it the same number of times.
   auto total = [&]() -> double {
     __syncthreads();   // the last pass's readers of s_chunk are done
+    place();
     for (int k = warp; k < nc; k += kWarps) {
-      const double s = warp_sum(chunk_sum<T, N>(R, (c0 + k) * kChunk, V, lane));
+      const double s = warp_sum(chunk_sum<T, N>(R, (c0 + k) * kChunk - shift, V, lane));
       if (lane == 0) s_chunk[k] = s;
     }
     __syncthreads();
@@ -208,10 +291,13 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyParam
       if (lane == 0) s_total[pass & 1] = s;
     }
     cluster.sync();
-    double all = 0.0;
-    for (int r = 0; r < ranks; ++r) {
+    double part[kMaxCluster], all = 0.0;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) part[r] = r < ranks ? *cluster.map_shared_rank(&s_total[pass & 1], r) : 0.0;
+#pragma unroll
+    for (int r = 0; r < kMaxCluster; ++r) {
       if (r == rank) before = all;
-      all += *cluster.map_shared_rank(&s_total[pass & 1], r);
+      all += part[r];
     }
     ++pass;
     return all;
@@ -219,6 +305,7 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyParam
 
   int cur = 0, len = n > 0 ? 1 : 0;
   double S = 1.0;
+  bool first = true;     // no child of cur has been rejected
   bool summed = false;   // the chunk sums are those of the current R
   int* path = p.path + b * p.path_row;
   const bool writer = rank == 0 && tid == 0;
@@ -227,27 +314,31 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyParam
   __syncthreads();
   for (int i = 1; i < n && len < p.max_path; ++i) {
     if (s_parent[i] != cur) continue;
-    const double pv = s_p[i], qv = s_q[i];
-    double r;
-    if (R.q != nullptr) {
-      r = fmax(pv - R.c * qv, 0.0);
-    } else {
-      r = pv;
-      for (int k = 0; k < R.n_removed; ++k)
-        if (s_removed[k] == s_tok[i]) r = 0.0;
+    double r = s_p[i];
+    bool taken = s_first[i];
+    if (!first) {
+      const double qv = s_q[i];
+      if (R.q != nullptr) {
+        r = fmax(r - R.c * qv, 0.0);
+      } else {
+        for (int k = 0; k < R.n_removed; ++k)
+          if (s_removed[k] == s_tok[i]) r = 0.0;
+      }
+      taken = double(s_u[i]) * S * qv < r;
     }
-    if (double(s_u[i]) * S * qv < r) {
+    first = taken;
+    if (taken) {
       if (writer) path[len] = i;
       ++len;
       cur = i;
       R.p = target + int64_t(n0 + i) * p.target_row;
       if (R.q != nullptr) R.q = draft + int64_t(n0 + i) * p.draft_row;
-      R.c = 0.0;
+      R.set_c(0.0);
       R.n_removed = 0;
       S = 1.0;
       summed = false;
     } else if (R.q != nullptr) {
-      R.c += S;
+      R.set_c(R.c + S);
       S = total();
       summed = true;
     } else {
@@ -261,11 +352,10 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyParam
   }
 
   // the next token
-  int next = -1;
   if (n > 0) {
     double all = summed ? S : total();
     if (!(all > 0.0) && (R.c != 0.0 || R.n_removed > 0)) {   // nothing left: the target's own row
-      R.c = 0.0;
+      R.set_c(0.0);
       R.n_removed = 0;
       all = total();
     }
@@ -273,53 +363,65 @@ __global__ void __launch_bounds__(kThreads) tree_verify_kernel(const VerifyParam
     double goal = double(p.u_sample[b]) * all;
     goal = fmin(goal, all * (1.0 - 1.2e-16));
     const double mine = *cluster.map_shared_rank(&s_total[(pass - 1) & 1], rank);
-    // the last CTA that starts at or below the goal among those with mass before it ends
-    bool here = all > 0.0 && mine > 0.0 && before <= goal && goal < before + mine;
+    // the CTA in whose slice the goal lies: the slices' sums partition [0, all)
+    const bool here = all > 0.0 && mine > 0.0 && before <= goal && goal < before + mine;
     if (here) {
-      double run = before;
-      int k = 0, last = -1;
-      double last_base = 0.0;
-      for (; k < nc; ++k) {
-        if (s_chunk[k] > 0.0) {
-          last = k;
-          last_base = run;
+      // the first chunk whose running sum exceeds the goal (every warp by itself), then the first of its entries, two
+      // a thread; where rounding leaves none, the last one with mass
+      double run = before, run_k = 0.0;
+      int k = -1;
+      for (int k0 = 0; k0 < nc; k0 += 32) {
+        const Picked f = pick(k0 + lane < nc ? s_chunk[k0 + lane] : 0.0, goal, run);
+        if (f.at >= 0 || f.last >= 0) {
+          k = k0 + (f.at >= 0 ? f.at : f.last);
+          run_k = f.at >= 0 ? f.run_at : f.run_last;
         }
-        if (run + s_chunk[k] > goal) break;
-        run += s_chunk[k];
+        if (f.at >= 0) break;
+        run = f.run_end;
       }
-      if (k == nc) {   // rounding: the slice's running sum stayed below; its last chunk with mass
-        k = last;
-        run = last_base;
-      }
-      if (warp == 0) {
-        const int base = (c0 + k) * kChunk;
-        int found = -1, last_pos = -1;
-        for (int j = 0; j < kPerLane && found < 0; ++j) {
-          const int i = base + j * 32 + lane;
-          double r = 0.0;
-          if (i < V) r = R.at(R.p[i], R.q != nullptr ? R.q[i] : R.p[i], i);
-          double inc = r;
+      constexpr int kEach = kChunk / kThreads;
+      const int i0 = (c0 + k) * kChunk - shift + tid * kEach;
+      T x[kEach], y[kEach];
+      double r[kEach], sum = 0.0;
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o) inc += y;
-          }
-          const unsigned over = __ballot_sync(0xffffffffu, r > 0.0 && run + inc > goal);
-          const unsigned pos = __ballot_sync(0xffffffffu, r > 0.0);
-          if (over) found = base + j * 32 + __ffs(over) - 1;
-          if (pos) last_pos = base + j * 32 + 31 - __clz(pos);
-          run += __shfl_sync(0xffffffffu, inc, 31);
-        }
-        if (lane == 0) s_found = found >= 0 ? found : last_pos;
+      for (int e = 0; e < kEach; ++e) {
+        const bool there = i0 + e >= 0 && i0 + e < V;
+        x[e] = there ? R.p[i0 + e] : T(0.f);
+        y[e] = there && R.q != nullptr ? R.q[i0 + e] : T(0.f);
       }
-    }
-    __syncthreads();
-    if (here) next = s_found;
-    if (here && tid == 0) {
-      if (p.tok64)
-        static_cast<int64_t*>(p.next)[b] = next;
-      else
-        static_cast<int*>(p.next)[b] = next;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        float h, l;
+        R.at(x[e], y[e], i0 + e, h, l);
+        r[e] = double(h) + double(l);
+        sum += r[e];
+      }
+      double inc = sum;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double up = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += up;
+      }
+      if (lane == 31) s_warp[warp] = inc;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) run_k += s_warp[w];
+      run_k += inc - sum;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        run_k += r[e];
+        if (r[e] > 0.0) {
+          if (run_k > goal) atomicMin(&s_found, i0 + e);
+          atomicMax(&s_last, i0 + e);
+        }
+      }
+      __syncthreads();
+      if (tid == 0) {
+        const int token = s_found < V ? s_found : s_last;
+        if (p.tok64)
+          static_cast<int64_t*>(p.next)[b] = token;
+        else
+          static_cast<int*>(p.next)[b] = token;
+      }
     }
     if (writer && !(all > 0.0)) {
       if (p.tok64)
@@ -355,9 +457,9 @@ cudaError_t launch(const VerifyParams& p, int B, int ranks, cudaStream_t s) {
 template <typename T>
 cudaError_t dispatch(const VerifyParams& p, int B, int ranks, cudaStream_t s) {
   constexpr int N = 16 / int(sizeof(T));
-  // 16-byte loads need every row on a 16-byte boundary and whole vectors to its end
-  const bool vec = p.V % N == 0 && p.target_row % N == 0 && splitkv::ptr_aligned(p.target, 16) &&
-                   (!p.draft || (p.draft_row % N == 0 && splitkv::ptr_aligned(p.draft, 16)));
+  // 16-byte loads: a node's two rows have to lie alike about the 16-byte boundaries
+  const auto at = [](const void* x) { return int64_t(reinterpret_cast<uintptr_t>(x) / sizeof(T) % N); };
+  const bool vec = !p.draft || (at(p.target) == at(p.draft) && p.target_row % N == p.draft_row % N);
   return vec ? launch<T, N>(p, B, ranks, s) : launch<T, 1>(p, B, ranks, s);
 }
 
@@ -369,7 +471,7 @@ extern "C" int splitkv_tree_verify(const splitkv_verify_args* a, void* stream) {
     return SPLITKV_ERR_INVALID_ARG;
   if (a->dtype != SPLITKV_DTYPE_F32 && a->dtype != SPLITKV_DTYPE_BF16 && a->dtype != SPLITKV_DTYPE_F16)
     return SPLITKV_ERR_INVALID_ARG;
-  if (a->max_nodes > kMaxNodes || a->vocab > kMaxChunks * kChunk || a->num_seqs > (1 << 24))
+  if (a->max_nodes > kMaxNodes || a->vocab > kMaxVocab || a->num_seqs > (1 << 24))
     return SPLITKV_ERR_UNSUPPORTED;
   if (a->num_seqs == 0) return SPLITKV_OK;
   const int es = a->dtype == SPLITKV_DTYPE_F32 ? 4 : 2;
@@ -398,12 +500,12 @@ extern "C" int splitkv_tree_verify(const splitkv_verify_args* a, void* stream) {
   p.max_nodes = a->max_nodes;
   p.max_path = a->max_path;
   p.tok64 = a->token_int64 ? 1 : 0;
-  // CTAs of a sequence: enough that the batch covers the SMs a few times, not so many that a
-  // CTA has less than four chunks (a cluster of one skips no work, only spreads less).
+  // CTAs of a sequence: no more than run at once (three to an SM), and no CTA with less than eight chunks (one a warp).
   const int chunks = (a->vocab + kChunk - 1) / kChunk;
   int ranks = 1;
-  while (ranks < kMaxCluster && int64_t(a->num_seqs) * ranks < 592 && chunks >= ranks * 2 * 4) ranks *= 2;
-  p.chunks_per_cta = (chunks + ranks - 1) / ranks;
+  while (ranks < kMaxCluster && (chunks >= ranks * kMaxChunks ||
+                                 (int64_t(a->num_seqs) * ranks * 2 <= 444 && chunks >= ranks * 2 * kWarps)))
+    ranks *= 2;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = a->dtype == SPLITKV_DTYPE_F32    ? dispatch<float>(p, a->num_seqs, ranks, s)
                   : a->dtype == SPLITKV_DTYPE_BF16 ? dispatch<__nv_bfloat16>(p, a->num_seqs, ranks, s)
