@@ -7,12 +7,12 @@
 // same m.  Elements from rotary_dim on pass through.  Pairs are (i, i + rotary_dim / 2), or
 // (2i, 2i + 1) in the interleaved layout.
 //
-// HBM-bound: every element is read and written once, 2 * N * (Hq + Hk) * d elements.  A
-// thread owns P pairs of one token -- two 16-byte vectors of a head -- computes their
-// cosines and sines once and walks over heads with them (queries first, then keys: one
-// launch for both), so the angles cost nothing next to the traffic.  The angle is formed in
-// float64 in units of turns and reduced to [-1/2, 1/2] before the float32 sine and cosine:
-// at position 2^20 the float32 product would be off by 0.06 rad, this one by 1e-9.
+// HBM-bound: every element is read and written once, 2 * N * (Hq + Hk) * d elements.  A CTA takes a
+// few tokens: it forms their cosines and sines once in shared memory, then streams the tokens'
+// heads (queries, then keys: one launch for both), a thread two 16-byte vectors of a head -- P pairs
+// -- with neighbouring threads on neighbouring vectors and heads.  The angle is formed in float64 in
+// units of turns and reduced to [-1/2, 1/2] before the float32 sine and cosine: at position 2^20 the
+// float32 product would be off by 0.06 rad, this one by 1e-9.
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -26,8 +26,9 @@
 
 namespace {
 
-constexpr int kThreads = 128;
-constexpr int kUnroll = 4;   // heads whose loads are in flight together
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;     // heads whose loads are in flight together
+constexpr int kMaxPairs = 512; // pairs of one CTA's tokens in shared memory
 
 struct Side {
   const char* in;
@@ -42,10 +43,13 @@ struct RopeParams {
   const double* freqs;
   int64_t n_tokens;
   int half;          // rotary_dim / 2
-  int units;         // threads per token: units that turn, then units that copy
+  int units;         // thread columns a token: units that turn, then units that copy
   int turn_units;
   int copy_vecs;     // 16-byte vectors (or elements) of a head that pass through
-  int heads_per_thread;
+  int cols;          // units of one CTA (blockIdx.y takes cols * blockIdx.y onwards)
+  int rows;          // threads side by side over (token, head)
+  int tokens;        // of one CTA
+  int heads;         // of one CTA (blockIdx.z)
   float m;
   int pos64, adjoint;
 };
@@ -71,7 +75,7 @@ __device__ __forceinline__ __half from_f<__half>(float x) {
 
 // P values of type T, moved as one aligned access (16 bytes, or one element when P = 1).
 template <typename T, int P>
-struct alignas(sizeof(T) * P) Vec {
+struct alignas(sizeof(T) * P < 16 ? sizeof(T) * P : 16) Vec {
   T v[P];
 };
 
@@ -79,28 +83,32 @@ struct alignas(sizeof(T) * P) Vec {
 template <typename T, int P, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
   using V = Vec<T, P>;
-  const int64_t idx = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-  if (idx >= p.n_tokens * p.units) return;
-  const int64_t tok = idx / p.units;
-  const int unit = int(idx - tok * p.units);
+  __shared__ __align__(16) float s_c[kMaxPairs], s_s[kMaxPairs];
+  const int64_t tok0 = int64_t(blockIdx.x) * p.tokens;
+  const int tokens = int(min(int64_t(p.tokens), p.n_tokens - tok0));
+  const int unit0 = blockIdx.y * p.cols;
+  const int turn = min(p.cols, p.turn_units - unit0);          // of this CTA's units (none: <= 0)
+  const int pairs = max(0, turn) * P;
+  for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
+    const int t = i / pairs, j = i - t * pairs;
+    const double pos = p.pos64 ? double(static_cast<const int64_t*>(p.positions)[tok0 + t])
+                               : double(static_cast<const int32_t*>(p.positions)[tok0 + t]);
+    constexpr double kInv2Pi = 0.15915494309189533577;
+    const double turns = pos * (p.freqs[unit0 * P + j] * kInv2Pi);
+    float sn, cs;
+    sincospif(2.0f * float(turns - rint(turns)), &sn, &cs);
+    s_c[i] = cs * p.m;
+    s_s[i] = (p.adjoint ? -sn : sn) * p.m;
+  }
+  __syncthreads();
+  const int col = threadIdx.x % p.cols, row0 = threadIdx.x / p.cols;
+  const int unit = unit0 + col;
+  if (row0 >= p.rows || unit >= p.units) return;
   const bool turns = unit < p.turn_units;
-
-  float c[P], s[P];
   int off0, off1;          // element offsets of the thread's two vectors inside a head
   bool second = true;
   if (turns) {
     const int i0 = unit * P;
-    const double pos = p.pos64 ? double(static_cast<const int64_t*>(p.positions)[tok])
-                               : double(static_cast<const int32_t*>(p.positions)[tok]);
-#pragma unroll
-    for (int j = 0; j < P; ++j) {
-      constexpr double kInv2Pi = 0.15915494309189533577;
-      const double t = pos * (p.freqs[i0 + j] * kInv2Pi);   // turns
-      float sn, cs;
-      sincospif(2.0f * float(t - rint(t)), &sn, &cs);
-      c[j] = cs * p.m;
-      s[j] = (p.adjoint ? -sn : sn) * p.m;
-    }
     off0 = kInterleaved ? 2 * i0 : i0;
     off1 = kInterleaved ? 2 * i0 + P : p.half + i0;
   } else {
@@ -110,45 +118,50 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
     second = v0 + 1 < p.copy_vecs;
   }
 
-  const int total = p.q.heads + p.k.heads;
-  const int h_end = min(total, (int(blockIdx.y) + 1) * p.heads_per_thread);
-  for (int h0 = int(blockIdx.y) * p.heads_per_thread; h0 < h_end; h0 += kUnroll) {
+  const int h_first = blockIdx.z * p.heads, n_heads = min(p.heads, p.q.heads + p.k.heads - h_first);
+  const int n = tokens * n_heads;    // (token, head) rows of this CTA
+  for (int r0 = row0; r0 < n; r0 += kUnroll * p.rows) {
     V a[kUnroll], b[kUnroll];
     char* dst[kUnroll];
+    int tl[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int h = h0 + u;
-      if (h < h_end) {
+      const int r = r0 + u * p.rows;
+      if (r < n) {
+        tl[u] = r / n_heads;
+        const int h = h_first + r - tl[u] * n_heads;
         const bool is_q = h < p.q.heads;
         const Side& sd = is_q ? p.q : p.k;
         const int hh = is_q ? h : h - p.q.heads;
-        const char* src = sd.in + tok * sd.in_tok + hh * sd.in_head;
-        dst[u] = sd.out + tok * sd.out_tok + hh * sd.out_head;
+        const char* src = sd.in + (tok0 + tl[u]) * sd.in_tok + hh * sd.in_head;
+        dst[u] = sd.out + (tok0 + tl[u]) * sd.out_tok + hh * sd.out_head;
         a[u] = *reinterpret_cast<const V*>(src + off0 * sizeof(T));
         if (second) b[u] = *reinterpret_cast<const V*>(src + off1 * sizeof(T));
       }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      if (h0 + u < h_end) {
+      if (r0 + u * p.rows < n) {
         if (turns) {
+          const Vec<float, P> c = *reinterpret_cast<const Vec<float, P>*>(s_c + tl[u] * pairs + col * P);
+          const Vec<float, P> s = *reinterpret_cast<const Vec<float, P>*>(s_s + tl[u] * pairs + col * P);
           if (kInterleaved && P > 1) {
             // element pairs (2j, 2j + 1) over the two vectors
 #pragma unroll
             for (int j = 0; j < P; j += 2) {
               const float x = to_f(a[u].v[j]), y = to_f(a[u].v[j + 1]);
-              a[u].v[j] = from_f<T>(x * c[j / 2] - y * s[j / 2]);
-              a[u].v[j + 1] = from_f<T>(y * c[j / 2] + x * s[j / 2]);
+              a[u].v[j] = from_f<T>(x * c.v[j / 2] - y * s.v[j / 2]);
+              a[u].v[j + 1] = from_f<T>(y * c.v[j / 2] + x * s.v[j / 2]);
               const float z = to_f(b[u].v[j]), w = to_f(b[u].v[j + 1]);
-              b[u].v[j] = from_f<T>(z * c[(P + j) / 2] - w * s[(P + j) / 2]);
-              b[u].v[j + 1] = from_f<T>(w * c[(P + j) / 2] + z * s[(P + j) / 2]);
+              b[u].v[j] = from_f<T>(z * c.v[(P + j) / 2] - w * s.v[(P + j) / 2]);
+              b[u].v[j + 1] = from_f<T>(w * c.v[(P + j) / 2] + z * s.v[(P + j) / 2]);
             }
           } else {
 #pragma unroll
             for (int j = 0; j < P; ++j) {
               const float x = to_f(a[u].v[j]), y = to_f(b[u].v[j]);
-              a[u].v[j] = from_f<T>(x * c[j] - y * s[j]);
-              b[u].v[j] = from_f<T>(y * c[j] + x * s[j]);
+              a[u].v[j] = from_f<T>(x * c.v[j] - y * s.v[j]);
+              b[u].v[j] = from_f<T>(y * c.v[j] + x * s.v[j]);
             }
           }
         }
@@ -269,18 +282,28 @@ extern "C" int splitkv_rope(const splitkv_rope_args* a, void* stream) {
   p.pos64 = pos64;
   p.adjoint = (a->flags & SPLITKV_ROPE_ADJOINT) != 0;
 
-  // Heads per thread: all of them would compute each angle once, but a few tokens then leave
-  // the GPU idle and one thread a long chain of loads.
+  // A CTA's share: columns of units side by side (all of them, unless a head is very wide), then as many tokens as
+  // give every thread about two rounds of loads; with few tokens in all, one token and one round of heads, so that a
+  // short call spreads over the SMs.
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  const int64_t threads = p.n_tokens * p.units;
-  int64_t hpt = threads * heads / (int64_t(sms) * 2048);
-  hpt = hpt < kUnroll ? kUnroll : hpt > 16 ? 16 : hpt / kUnroll * kUnroll;
-  p.heads_per_thread = int(hpt);
-  const int64_t blocks = (threads + kThreads - 1) / kThreads;
-  const int64_t gy = (heads + hpt - 1) / hpt;
-  if (blocks > 0x7fffffff || gy > 65535) return SPLITKV_ERR_UNSUPPORTED;
-  const dim3 grid{unsigned(blocks), unsigned(gy)};
+  p.cols = p.units < 64 ? p.units : 64;
+  p.rows = kThreads / p.cols;
+  const int64_t gy = (p.units + p.cols - 1) / p.cols;
+  const int max_tokens = kMaxPairs / (p.cols * pairs) > 0 ? kMaxPairs / (p.cols * pairs) : 1;
+  int tokens = (2 * kUnroll * p.rows + heads - 1) / heads;
+  tokens = tokens > max_tokens ? max_tokens : tokens;
+  p.tokens = tokens;
+  p.heads = heads;
+  if ((p.n_tokens + tokens - 1) / tokens * gy < int64_t(4) * sms) {
+    p.tokens = 1;
+    const int per = p.n_tokens * gy < 2 * sms ? p.rows : kUnroll * p.rows;
+    p.heads = per < heads ? per : heads;
+  }
+  const int64_t blocks = (p.n_tokens + p.tokens - 1) / p.tokens;
+  const int64_t gz = (heads + p.heads - 1) / p.heads;
+  if (blocks > 0x7fffffff || gy > 65535 || gz > 65535) return SPLITKV_ERR_UNSUPPORTED;
+  const dim3 grid{unsigned(blocks), unsigned(gy), unsigned(gz)};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool il = (a->flags & SPLITKV_ROPE_INTERLEAVED) != 0;
   cudaError_t e;

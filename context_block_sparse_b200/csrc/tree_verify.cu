@@ -96,113 +96,126 @@ struct alignas(sizeof(T) * N) Pack {
   T v[N];
 };
 
-// The residual at the walk's current node.
+// The residual at the walk's current node: the row itself, max(p - c q, 0), or the row without the rejected tokens.
+enum Mode { kRow, kMinus1, kMinus, kWithout };   // (kMinus1: c = 1, after a node's first rejection)
 template <typename T>
 struct Residual {
   const T* p;
-  const T* q;          // NULL: certainty drafts, `removed` tokens have no mass left
+  const T* q;
   double c;
   float ch, cl;        // c as hi + lo
   const int* removed;
   int n_removed;
+  Mode mode;
+  __device__ __forceinline__ void reset() {
+    c = 0.0;
+    ch = cl = 0.f;
+    n_removed = 0;
+    mode = kRow;
+  }
   __device__ __forceinline__ void set_c(double x) {
     c = x;
     ch = float(x);
     cl = float(x - double(ch));
+    mode = x == 1.0 ? kMinus1 : kMinus;
   }
   // R of entry i with p = pv, q = qv, as hi + lo
+  template <Mode kM>
   __device__ __forceinline__ void at(T pv, T qv, int i, float& h, float& l) const {
     h = mass(pv);
     l = 0.f;
-    if (q != nullptr) {
-      const float b = mass(qv);
-      const float x = __fmul_rn(ch, b);
-      const float xe = __fmaf_rn(cl, b, __fmaf_rn(ch, b, -x));   // c q = x + xe
-      two_sum(h, -x, h, l);
-      l = __fsub_rn(l, xe);
-      if (!(__fadd_rn(h, l) > 0.f)) h = l = 0.f;
-    } else {
+    if constexpr (kM == kMinus || kM == kMinus1) {
+      // where p > x the difference's rounding error is (p - d) - x exactly (Dekker); elsewhere nothing is left
+      const float b = mass(qv), x = kM == kMinus1 ? b : __fmul_rn(ch, b), d = __fsub_rn(h, x);
+      l = __fsub_rn(__fsub_rn(h, d), x);
+      bool some = d > 0.f;
+      if constexpr (kM == kMinus) {
+        l = __fsub_rn(l, __fmaf_rn(cl, b, __fmaf_rn(ch, b, -x)));   // c q = x + this
+        some = d >= 0.f && __fadd_rn(d, l) > 0.f;
+      }
+      h = some ? d : 0.f;
+      l = some ? l : 0.f;
+    }
+    if constexpr (kM == kWithout) {
       for (int k = 0; k < n_removed; ++k)
         if (removed[k] == i) h = 0.f;
     }
+  }
+  __device__ __forceinline__ double value(T pv, T qv, int i) const {
+    float h, l;
+    if (mode == kMinus || mode == kMinus1)
+      at<kMinus>(pv, qv, i, h, l);
+    else
+      at<kWithout>(pv, qv, i, h, l);
+    return double(h) + double(l);
   }
 };
 
 // This lane's share of the chunk of entries [base, base + kChunk), in N-element vectors that sit on 16-byte
 // boundaries (base may be negative, and the chunk may end behind the row: those entries are not there).
-template <typename T, int N>
+template <typename T, int N, Mode kM>
 __device__ __forceinline__ double chunk_sum(const Residual<T>& R, int base, int V, int lane) {
-  Sum s;
-  constexpr int kSteps = kPerLane / N, kBatch = N == 1 ? 8 : 16 / N;   // vectors of a row in flight
-  const bool both = R.q != nullptr && R.c != 0.0;
+  Sum s[2];   // two chains of additions
+  constexpr int kSteps = kPerLane / N;
+  if (base >= 0 && base + kChunk <= V) {
+    constexpr int kBatch = N == 1 ? 8 : kSteps;   // vectors of a row in flight
 #pragma unroll 1
-  for (int j0 = 0; j0 < kSteps; j0 += kBatch) {
-    Pack<T, N> a[kBatch], b[kBatch];
+    for (int j0 = 0; j0 < kSteps; j0 += kBatch) {
+      Pack<T, N> a[kBatch], b[kBatch];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int i = base + ((j0 + j) * 32 + lane) * N;
-      if (i >= 0 && i + N <= V) {
+      for (int j = 0; j < kBatch; ++j) {
+        const int i = base + ((j0 + j) * 32 + lane) * N;
         a[j] = *reinterpret_cast<const Pack<T, N>*>(R.p + i);
-        if (both) b[j] = *reinterpret_cast<const Pack<T, N>*>(R.q + i);
-      } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const bool there = i + e >= 0 && i + e < V;
-          a[j].v[e] = there ? R.p[i + e] : T(0.f);
-          if (both) b[j].v[e] = there ? R.q[i + e] : T(0.f);
-        }
+        if constexpr (kM == kMinus || kM == kMinus1) b[j] = *reinterpret_cast<const Pack<T, N>*>(R.q + i);
       }
-    }
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int i = base + ((j0 + j) * 32 + lane) * N;
-      if (R.q != nullptr && !both) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) s.add(mass(a[j].v[e]), 0.f);
-      } else {
+      for (int j = 0; j < kBatch; ++j) {
 #pragma unroll
         for (int e = 0; e < N; ++e) {
           float h, l;
-          R.at(a[j].v[e], b[j].v[e], i + e, h, l);
-          s.add(h, l);
+          R.template at<kM>(a[j].v[e], b[j].v[e], base + ((j0 + j) * 32 + lane) * N + e, h, l);
+          s[(j * N + e) & 1].add(h, l);
         }
       }
     }
+  } else {
+#pragma unroll 1
+    for (int j0 = 0; j0 < kPerLane; j0 += 8) {   // the row's first and last chunk
+      T a[8], b[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int i = base + (j0 + j) * 32 + lane;
+        const bool there = i >= 0 && i < V;
+        a[j] = there ? R.p[i] : T(0.f);
+        if constexpr (kM == kMinus || kM == kMinus1) b[j] = there ? R.q[i] : T(0.f);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float h, l;
+        R.template at<kM>(a[j], b[j], base + (j0 + j) * 32 + lane, h, l);
+        s[j & 1].add(h, l);
+      }
+    }
   }
-  return s.value();
+  return s[0].value() + s[1].value();
 }
 
-__device__ __forceinline__ double warp_sum(double s) {
-#pragma unroll
+// (The steps outside the vocabulary loop run once a launch, on cold instruction caches: rolled loops and shared
+// functions, since fetching a line of straight code costs more than running it several times.)
+__device__ __noinline__ double warp_sum(double s) {
+#pragma unroll 1
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
 }
 
-// One warp's values x on top of a running sum: the first lane whose sum exceeds the goal (-1: none) and the last lane
-// with mass (-1: none), with the sums before them and behind all lanes.
-struct Picked {
-  int at, last;
-  double run_at, run_last, run_end;
-};
-__device__ __forceinline__ Picked pick(double x, double goal, double run) {
+__device__ __noinline__ double warp_scan(double x) {   // inclusive
   const int lane = threadIdx.x & 31;
-  double inc = x;
-#pragma unroll
+#pragma unroll 1
   for (int o = 1; o < 32; o <<= 1) {
-    const double y = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += y;
+    const double y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
-  double exc = __shfl_up_sync(0xffffffffu, inc, 1);
-  if (lane == 0) exc = 0.0;
-  const unsigned over = __ballot_sync(0xffffffffu, x > 0.0 && run + inc > goal);
-  const unsigned pos = __ballot_sync(0xffffffffu, x > 0.0);
-  Picked r;
-  r.at = over ? __ffs(over) - 1 : -1;
-  r.last = pos ? 31 - __clz(pos) : -1;
-  r.run_at = run + __shfl_sync(0xffffffffu, exc, r.at < 0 ? 0 : r.at);
-  r.run_last = run + __shfl_sync(0xffffffffu, exc, r.last < 0 ? 0 : r.last);
-  r.run_end = run + __shfl_sync(0xffffffffu, inc, 31);
-  return r;
+  return x;
 }
 
 template <typename T, int N>
@@ -212,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_verify_kernel(const VerifyPa
   const int b = int(blockIdx.x) / ranks;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-  __shared__ int s_parent[kMaxNodes], s_tok[kMaxNodes], s_removed[kMaxNodes];
+  __shared__ int s_parent[kMaxNodes], s_tok[kMaxNodes], s_removed[kMaxNodes], s_path[kMaxNodes];
   __shared__ float s_p[kMaxNodes], s_q[kMaxNodes], s_u[kMaxNodes];
   __shared__ double s_chunk[kMaxChunks];
   __shared__ double s_total[2];   // this CTA's slice sum, by pass parity
@@ -259,13 +272,13 @@ __global__ void __launch_bounds__(kThreads, 3) tree_verify_kernel(const VerifyPa
 
   Residual<T> R;
   R.removed = s_removed;
-  R.p = target + int64_t(n0) * p.target_row;
-  R.q = draft ? draft + int64_t(n0) * p.draft_row : nullptr;
-  R.set_c(0.0);
-  R.n_removed = 0;
+  R.reset();
+  int cur = 0;
   // Chunks are cut at 16-byte boundaries: the current row begins `shift` entries behind one (the same in both rows).
   int shift = 0, c0 = 0, nc = 0;            // this CTA's chunks
   auto place = [&]() {
+    R.p = target + int64_t(n0 + cur) * p.target_row;
+    R.q = draft ? draft + int64_t(n0 + cur) * p.draft_row : nullptr;
     shift = N == 1 ? 0 : int(reinterpret_cast<uintptr_t>(R.p) / sizeof(T) % N);
     const int all = (V + shift + kChunk - 1) / kChunk, per = (all + ranks - 1) / ranks;
     c0 = rank * per;
@@ -280,7 +293,11 @@ __global__ void __launch_bounds__(kThreads, 3) tree_verify_kernel(const VerifyPa
     __syncthreads();   // the last pass's readers of s_chunk are done
     place();
     for (int k = warp; k < nc; k += kWarps) {
-      const double s = warp_sum(chunk_sum<T, N>(R, (c0 + k) * kChunk - shift, V, lane));
+      const int base = (c0 + k) * kChunk - shift;
+      const double s = warp_sum(R.mode == kRow      ? chunk_sum<T, N, kRow>(R, base, V, lane)
+                                : R.mode == kMinus1 ? chunk_sum<T, N, kMinus1>(R, base, V, lane)
+                                : R.mode == kMinus  ? chunk_sum<T, N, kMinus>(R, base, V, lane)
+                                                    : chunk_sum<T, N, kWithout>(R, base, V, lane));
       if (lane == 0) s_chunk[k] = s;
     }
     __syncthreads();
@@ -291,78 +308,92 @@ __global__ void __launch_bounds__(kThreads, 3) tree_verify_kernel(const VerifyPa
       if (lane == 0) s_total[pass & 1] = s;
     }
     cluster.sync();
-    double part[kMaxCluster], all = 0.0;
-#pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) part[r] = r < ranks ? *cluster.map_shared_rank(&s_total[pass & 1], r) : 0.0;
-#pragma unroll
-    for (int r = 0; r < kMaxCluster; ++r) {
+    // lane r reads rank r's sum; added in rank order
+    const double part = lane < ranks ? *cluster.map_shared_rank(&s_total[pass & 1], lane) : 0.0;
+    double all = 0.0;
+#pragma unroll 1
+    for (int r = 0; r < ranks; ++r) {
       if (r == rank) before = all;
-      all += part[r];
+      all += __shfl_sync(0xffffffffu, part, r);
     }
     ++pass;
     return all;
   };
 
-  int cur = 0, len = n > 0 ? 1 : 0;
+  int len = n > 0 ? 1 : 0;
   double S = 1.0;
   bool first = true;     // no child of cur has been rejected
   bool summed = false;   // the chunk sums are those of the current R
-  int* path = p.path + b * p.path_row;
   const bool writer = rank == 0 && tid == 0;
-  if (rank == 0)
-    for (int i = tid; i < p.max_path; i += kThreads) path[i] = (i == 0 && n > 0) ? 0 : -1;
-  __syncthreads();
-  for (int i = 1; i < n && len < p.max_path; ++i) {
-    if (s_parent[i] != cur) continue;
-    double r = s_p[i];
-    bool taken = s_first[i];
-    if (!first) {
-      const double qv = s_q[i];
-      if (R.q != nullptr) {
-        r = fmax(r - R.c * qv, 0.0);
-      } else {
-        for (int k = 0; k < R.n_removed; ++k)
-          if (s_removed[k] == s_tok[i]) r = 0.0;
+  int at = 0;            // the last node tried
+  bool ended = n == 0;
+  for (;;) {
+    bool rejected = false;
+    while (!ended && !rejected) {
+      // the next child of cur (every warp by itself, 32 nodes at a time)
+      int child = -1;
+      if (len < p.max_path) {
+        for (int j0 = (at + 1) & ~31; j0 < n && child < 0; j0 += 32) {
+          const int j = j0 + lane;
+          const unsigned m = __ballot_sync(0xffffffffu, j > at && j < n && s_parent[j] == cur);
+          if (m) child = j0 + __ffs(m) - 1;
+        }
       }
-      taken = double(s_u[i]) * S * qv < r;
-    }
-    first = taken;
-    if (taken) {
-      if (writer) path[len] = i;
-      ++len;
-      cur = i;
-      R.p = target + int64_t(n0 + i) * p.target_row;
-      if (R.q != nullptr) R.q = draft + int64_t(n0 + i) * p.draft_row;
-      R.set_c(0.0);
-      R.n_removed = 0;
-      S = 1.0;
+      if (child < 0) {
+        ended = true;
+        break;
+      }
+      at = child;
+      bool taken = s_first[at];
+      double r = s_p[at];
+      if (!first) {
+        const double qv = s_q[at];
+        if (draft != nullptr) {
+          r = fmax(r - R.c * qv, 0.0);
+        } else {
+          for (int k = 0; k < R.n_removed; ++k)
+            if (s_removed[k] == s_tok[at]) r = 0.0;
+        }
+        taken = double(s_u[at]) * S * qv < r;
+      }
+      first = taken;
       summed = false;
-    } else if (R.q != nullptr) {
-      R.set_c(R.c + S);
-      S = total();
-      summed = true;
-    } else {
-      __syncthreads();   // every thread has read the removed list
-      if (tid == 0) s_removed[R.n_removed] = s_tok[i];
-      __syncthreads();
-      ++R.n_removed;
-      S = fmax(S - r, 0.0);
-      summed = false;
+      if (taken) {
+        if (tid == 0) s_path[len] = at;
+        ++len;
+        cur = at;
+        R.reset();
+        S = 1.0;
+      } else if (draft != nullptr) {
+        R.set_c(R.c + S);
+        rejected = true;   // S of what is left
+      } else {
+        __syncthreads();   // every thread has read the removed list
+        if (tid == 0) s_removed[R.n_removed] = s_tok[at];
+        __syncthreads();
+        ++R.n_removed;
+        R.mode = kWithout;
+        S = fmax(S - r, 0.0);
+      }
     }
+    if (n == 0 || (summed && (S > 0.0 || R.mode == kRow))) break;
+    if (summed) R.reset();   // nothing left at the end: the target's own row
+    S = total();
+    summed = true;
   }
+
+  // No CTA leaves while another may read its sums.  (Global writes wait until after the last barrier's arrival: its
+  // release would wait for them, 2 us in the middle of the walk.)
+  __syncthreads();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 
   // the next token
   if (n > 0) {
-    double all = summed ? S : total();
-    if (!(all > 0.0) && (R.c != 0.0 || R.n_removed > 0)) {   // nothing left: the target's own row
-      R.set_c(0.0);
-      R.n_removed = 0;
-      all = total();
-    }
+    const double all = S;
     // the first entry whose running sum exceeds the goal; below the total, so one exists
     double goal = double(p.u_sample[b]) * all;
     goal = fmin(goal, all * (1.0 - 1.2e-16));
-    const double mine = *cluster.map_shared_rank(&s_total[(pass - 1) & 1], rank);
+    const double mine = s_total[(pass - 1) & 1];
     // the CTA in whose slice the goal lies: the slices' sums partition [0, all)
     const bool here = all > 0.0 && mine > 0.0 && before <= goal && goal < before + mine;
     if (here) {
@@ -370,14 +401,19 @@ __global__ void __launch_bounds__(kThreads, 3) tree_verify_kernel(const VerifyPa
       // a thread; where rounding leaves none, the last one with mass
       double run = before, run_k = 0.0;
       int k = -1;
+#pragma unroll 1
       for (int k0 = 0; k0 < nc; k0 += 32) {
-        const Picked f = pick(k0 + lane < nc ? s_chunk[k0 + lane] : 0.0, goal, run);
-        if (f.at >= 0 || f.last >= 0) {
-          k = k0 + (f.at >= 0 ? f.at : f.last);
-          run_k = f.at >= 0 ? f.run_at : f.run_last;
+        const double x = k0 + lane < nc ? s_chunk[k0 + lane] : 0.0;
+        const double inc = warp_scan(x);
+        const unsigned over = __ballot_sync(0xffffffffu, x > 0.0 && run + inc > goal);
+        const unsigned some = __ballot_sync(0xffffffffu, x > 0.0);
+        if (some) {
+          const int f = over ? __ffs(over) - 1 : 31 - __clz(some);
+          k = k0 + f;
+          run_k = run + __shfl_sync(0xffffffffu, inc, f) - __shfl_sync(0xffffffffu, x, f);
         }
-        if (f.at >= 0) break;
-        run = f.run_end;
+        if (over) break;
+        run += __shfl_sync(0xffffffffu, inc, 31);
       }
       constexpr int kEach = kChunk / kThreads;
       const int i0 = (c0 + k) * kChunk - shift + tid * kEach;
@@ -391,17 +427,10 @@ __global__ void __launch_bounds__(kThreads, 3) tree_verify_kernel(const VerifyPa
       }
 #pragma unroll
       for (int e = 0; e < kEach; ++e) {
-        float h, l;
-        R.at(x[e], y[e], i0 + e, h, l);
-        r[e] = double(h) + double(l);
+        r[e] = R.value(x[e], y[e], i0 + e);
         sum += r[e];
       }
-      double inc = sum;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double up = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += up;
-      }
+      const double inc = warp_scan(sum);
       if (lane == 31) s_warp[warp] = inc;
       __syncthreads();
       for (int w = 0; w < warp; ++w) run_k += s_warp[w];
@@ -435,8 +464,12 @@ __global__ void __launch_bounds__(kThreads, 3) tree_verify_kernel(const VerifyPa
     else
       static_cast<int*>(p.next)[b] = -1;
   }
-  if (writer) p.count[b] = len;
-  cluster.sync();   // no CTA leaves while another may read its sums
+  if (rank == 0) {
+    int* path = p.path + b * p.path_row;
+    if (tid == 0) p.count[b] = len;
+    for (int i = tid; i < p.max_path; i += kThreads) path[i] = i >= len ? -1 : i == 0 ? 0 : s_path[i];
+  }
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 template <typename T, int N>
@@ -500,11 +533,11 @@ extern "C" int splitkv_tree_verify(const splitkv_verify_args* a, void* stream) {
   p.max_nodes = a->max_nodes;
   p.max_path = a->max_path;
   p.tok64 = a->token_int64 ? 1 : 0;
-  // CTAs of a sequence: no more than run at once (three to an SM), and no CTA with less than eight chunks (one a warp).
+  // CTAs of a sequence: no more than run at once (three to an SM), and no CTA with less than four chunks.
   const int chunks = (a->vocab + kChunk - 1) / kChunk;
   int ranks = 1;
   while (ranks < kMaxCluster && (chunks >= ranks * kMaxChunks ||
-                                 (int64_t(a->num_seqs) * ranks * 2 <= 444 && chunks >= ranks * 2 * kWarps)))
+                                 (int64_t(a->num_seqs) * ranks * 2 <= 444 && chunks >= ranks * kWarps)))
     ranks *= 2;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = a->dtype == SPLITKV_DTYPE_F32    ? dispatch<float>(p, a->num_seqs, ranks, s)
