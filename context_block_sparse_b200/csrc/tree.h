@@ -2,8 +2,9 @@
 // is cut over the CTAs of a launch.  Not part of the public ABI.
 //
 // A unit is one (sequence, KV head, row tile): up to Mt rows (node-major, the G query heads
-// of a node next to each other) against the sequence's whole context.  The units' key tiles
-// of tile_keys keys lie on one line, in (sequence, KV head, row tile, key tile) order, and
+// of a node next to each other) against the sequence's whole context and then its own tree, in
+// key tiles of 64 or 128 keys (a tile holds one kind).  All units' tiles lie on one line, in
+// (sequence, KV head, row tile, key tile) order, and
 // CTA c of C takes the stretch [c W / C, (c + 1) W / C) of its W tiles: every CTA has the same
 // number of tiles to within one, whatever the lengths, and the lengths stay on the device (a
 // captured graph replays with new ones).  A CTA's part of a unit is one record (unnormalised
@@ -13,6 +14,9 @@
 #pragma once
 
 #include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include "splitkv.h"
 #include "splitkv_internal.h"
@@ -42,6 +46,7 @@ struct TreeParams {
   float scale_log2;
   float* rec_o;                    // [C + U][Mt][d]
   float2* rec_ml;                  // [C + U][Mt]: maximum (log2 units), sum
+  int2* unit_rec;                  // [U]: a unit's records [x, y)
 };
 
 #ifdef __CUDACC__
@@ -68,7 +73,8 @@ __device__ __forceinline__ int seq_len(const TreeParams& p, int b, bool& bad) {
 }
 
 struct SeqWork {
-  int n0, n, len, rts, nt;   // first node, nodes, context length, row tiles, key tiles of a unit
+  int n0, n, len, rts;       // first node, nodes, context length, row tiles
+  int ctx, nt;               // context tiles of a unit, and all of them
   long long tiles;           // Hkv * rts * nt
 };
 
@@ -77,7 +83,9 @@ __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b, bool& ba
   w.n = seq_nodes(p, b, w.n0, bad);
   w.len = seq_len(p, b, bad);
   w.rts = (w.n * p.G + p.Mt - 1) / p.Mt;
-  w.nt = (w.len + (1 << p.tile_shift) - 1) >> p.tile_shift;
+  const int round = (1 << p.tile_shift) - 1;
+  w.ctx = (w.len + round) >> p.tile_shift;
+  w.nt = w.ctx + ((w.n + round) >> p.tile_shift);
   w.tiles = (long long)(p.Hkv) * w.rts * w.nt;
   return w;
 }
@@ -108,12 +116,15 @@ __device__ __forceinline__ long long block_prefix(long long mine, long long& bef
 // First tile of CTA c's stretch (c in [0, C]); C never exceeds the line's length W.
 __device__ __forceinline__ long long stretch(long long W, int c, int C) { return W * c / C; }
 
-// The CTA whose stretch holds tile x.
-__device__ __forceinline__ int cta_of(long long x, long long W, int C) {
-  int c = int(x * C / W);
-  while (c > 0 && stretch(W, c, C) > x) --c;
-  while (c + 1 < C && stretch(W, c + 1, C) <= x) ++c;
-  return c;
+template <typename T>
+__device__ __forceinline__ bool not_finite16(uint16_t x);   // bits of a T
+template <>
+__device__ __forceinline__ bool not_finite16<__nv_bfloat16>(uint16_t x) {
+  return (x & 0x7f80u) == 0x7f80u;
+}
+template <>
+__device__ __forceinline__ bool not_finite16<__half>(uint16_t x) {
+  return (x & 0x7c00u) == 0x7c00u;
 }
 
 #endif  // __CUDACC__

@@ -1,6 +1,6 @@
-// Attention of draft trees over a paged cache, on mma.sync: the context kernel (every row of
-// a sequence's nodes against its cached keys, split over the CTAs) and the merge (the
-// in-tree keys, then the context records).
+// Attention of draft trees over a paged cache: the records of every row against its sequence's
+// cached keys and its own tree, split over the CTAs (here on mma.sync, for few rows; on tcgen05 in
+// tree_context_sm100.cu), and the merge of a row's records.
 //
 // Per row (node i, query head h) of sequence b, over the keys j of its context [0, len_b) and
 // the nodes j of its own tree that mask lets i see, with KV head h / G:
@@ -47,14 +47,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi, __nv_bfloat16) { r
 __device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) {
   __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
-}
-
-// Offset of (row r, 16-byte chunk ch) in a [rows][N] tile.  Rows of 64 bytes (N = 32) swizzle their
-// four chunks by row pairs, wider ones as swz: ldmatrix over 8 consecutive rows touches 8 distinct
-// bank groups either way.
-template <int N>
-__device__ __forceinline__ int swz_v(int r, int ch) {
-  return N == 32 ? r * N + ((ch ^ ((r >> 1) & 3)) << 3) : swz<N>(r, ch);
 }
 
 // The A fragments of 16 rows of Q straight from global memory (rows past the tile's are zero):
@@ -167,7 +159,7 @@ __device__ __forceinline__ void softmax_step(Rows<NC>& st, float (&s)[kKeys / 8]
 #pragma unroll
     for (int c = 0; c < NC / 16; ++c) {
       uint32_t b0, b1, b2, b3;
-      ldsm_x4_t(b0, b1, b2, b3, sv + swz_v<NC>(row + 16 * g, c * 2 + (lane >> 4)));
+      ldsm_x4_t(b0, b1, b2, b3, sv + swz<NC>(row + 16 * g, c * 2 + (lane >> 4)));
       mma16816(st.o[2 * c], a, b0, b1, T());
       mma16816(st.o[2 * c + 1], a, b2, b3, T());
     }
@@ -225,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
   __shared__ int s_pg[kPgRing][kTileKeys];
   __shared__ int s_part[kPgRing][2];        // a tile's first and second 32 keys: not all of them are there
   __shared__ float2 s_ml[4][16];
+  __shared__ unsigned long long s_flag;     // nodes of a tree tile whose V is not all finite
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rg = warp / C::kKG, kg = warp % C::kKG;
@@ -253,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
       at += t;
     }
   }
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge may begin its in-tree term
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the merge finds its rows
   __syncthreads();
   Cursor load, use;   // the tile whose pages come next; the tile computed now
   load.bad = use.bad = false;
@@ -261,12 +254,15 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
   load = use;
   Cursor fill = use;  // the tile whose keys and values are requested next
 
-  // page ids of the `load` cursor's tile (-1: no such key), by 64 threads
+  // page ids of the `load` cursor's tile, or rows of the tree (-1: no such key), by 64 threads
   auto resolve = [&](int t) {
     if (tid < kTileKeys) {
-      const int key = load.tile * kTileKeys + tid;
+      int key = load.tile * kTileKeys + tid;
       int page = -1;
-      if (key < load.w.len) {
+      if (load.tile >= load.w.ctx) {           // a tile of the tree: the node's row
+        key -= load.w.ctx * kTileKeys;
+        if (key < load.w.n) page = load.w.n0 + key;
+      } else if (key < load.w.len) {
         page = p.table[load.b * p.table_row + (key >> p.page_shift)];
         if (page < 0 || page >= p.num_pages) {
           page = -1;
@@ -284,8 +280,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
     T* sk = stages + (t % C::kStages) * C::kStageElems;
     T* sv = sk + kTileKeys * D;
     const int ch = tid % kChunks;
-    const char* kbase = p.kc + fill.head * p.kc_head + ch * 16;
-    const char* vbase = p.vc + fill.head * p.vc_head + ch * 16;
+    const bool tree = fill.tile >= fill.w.ctx;
+    const char* kbase = (tree ? p.kb + fill.head * p.kb_head : p.kc + fill.head * p.kc_head) + ch * 16;
+    const char* vbase = (tree ? p.vb + fill.head * p.vb_head : p.vc + fill.head * p.vc_head) + ch * 16;
+    const int64_t kpage = tree ? p.kb_node : p.kc_page, kslot = tree ? 0 : p.kc_slot;
+    const int64_t vpage = tree ? p.vb_node : p.vc_page, vslot = tree ? 0 : p.vc_slot;
     const int slot_mask = (1 << p.page_shift) - 1;
 #pragma unroll
     for (int i = 0; i < kTileKeys / kRowsPer; ++i) {
@@ -294,8 +293,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
       const int slot = (fill.tile * kTileKeys + r) & slot_mask;
       const bool there = page >= 0;
       const int64_t pg = there ? page : 0, sl = there ? slot : 0;
-      cp_async16(sk + swz<D>(r, ch), kbase + pg * p.kc_page + sl * p.kc_slot, there);
-      cp_async16(sv + swz<D>(r, ch), vbase + pg * p.vc_page + sl * p.vc_slot, there);
+      cp_async16(sk + swz<D>(r, ch), kbase + pg * kpage + sl * kslot, there);
+      cp_async16(sv + swz<D>(r, ch), vbase + pg * vpage + sl * vslot, there);
     }
   };
 
@@ -314,7 +313,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
 
   uint32_t qf[D / 16][4];
   Rows<D> st;
-  bool fresh = true;
+  bool fresh = true, from_start = false;   // at the first tile of this CTA's part of a unit; that part is its first
   for (int t = 0; t < n_tiles; ++t) {
     cp_async_wait<C::kStages - 2>();
     __syncthreads();   // tile t has landed; every warp is done with tile t - 1's stage
@@ -331,10 +330,38 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
       load_q<D>(qf, p, use.w.n0, use.w.n, use.head, use.rt * p.Mt + rg * 16);
       st.clear();
       fresh = false;
+      from_start = use.tile == 0;
     }
-    const T* sk = stages + (t % C::kStages) * C::kStageElems;
+    T* sk = stages + (t % C::kStages) * C::kStageElems;
     float s[C::kKeysW / 8][4];
     scores<T, D, C::kKeysW>(s, qf, sk, kg * C::kKeysW);
+    const int tree0 = use.tile >= use.w.ctx ? (use.tile - use.w.ctx) * kTileKeys : -1;   // a tree tile's first node
+    if (tree0 >= 0) {
+      // A node's V may hold infinities or NaN that only the rows which see it may meet, but the product multiplies
+      // every V by P = 0 elsewhere: take such values out here and add them back where they are seen.
+      if (tid == 0) s_flag = 0;
+      __syncthreads();
+      uint16_t* sv = reinterpret_cast<uint16_t*>(sk + kTileKeys * D);
+#pragma unroll 1
+      for (int i = tid; i < kTileKeys * kChunks; i += kThreads) {
+        uint16_t* x = sv + swz<D>(i / kChunks, i % kChunks);
+        bool any = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (not_finite16<T>(x[e])) {
+            x[e] = 0;
+            any = true;
+          }
+        }
+        if (any) atomicOr(&s_flag, 1ull << (i / kChunks));
+      }
+      __syncthreads();
+    }
+    // row r of this thread's two: what it sees of the tree
+    auto sees = [&](int k, int j) -> bool {
+      const int node = (use.rt * p.Mt + rg * 16 + (lane >> 2) + 8 * k) / p.G;
+      return j < use.w.n && (p.mask == nullptr || (node < use.w.n && p.mask[int64_t(use.w.n0 + node) * p.mask_row + j]));
+    };
     const bool part = s_part[t % kPgRing][0] || s_part[t % kPgRing][1];
 #pragma unroll
     for (int i = 0; i < C::kKeysW / 8; ++i) {
@@ -345,8 +372,30 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
         if (s_pg[t % kPgRing][col] < 0) s[i][0] = s[i][2] = -INFINITY;
         if (s_pg[t % kPgRing][col + 1] < 0) s[i][1] = s[i][3] = -INFINITY;
       }
+      if (tree0 >= 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (!sees(e >> 1, tree0 + kg * C::kKeysW + 8 * i + 2 * (lane & 3) + (e & 1))) s[i][e] = -INFINITY;
+      }
     }
     softmax_step<T, D, C::kKeysW>(st, s, sk + kTileKeys * D, kg * C::kKeysW);
+    if (tree0 >= 0) {
+      unsigned long long flag = s_flag >> (kg * C::kKeysW);
+      if (C::kKeysW < 64) flag &= (1ull << (C::kKeysW & 63)) - 1;
+      while (flag) {
+        const int j = tree0 + kg * C::kKeysW + __ffsll(flag) - 1;
+        flag &= flag - 1;
+        const bool see[2] = {sees(0, j), sees(1, j)};
+        const T* v = reinterpret_cast<const T*>(p.vb + int64_t(use.w.n0 + j) * p.vb_node + use.head * p.vb_head);
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = float(v[8 * i + 2 * (lane & 3) + (e & 1)]);
+            if (!isfinite(x) && see[e >> 1]) st.o[i][e] += x;
+          }
+      }
+    }
 
     const bool last = t + 1 == n_tiles || use.tile + 1 == use.w.nt;
     if (last) {
@@ -354,6 +403,10 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
       const int unit = (use.b * p.Hkv + use.head) * p.RT + use.rt;
       const size_t rec = size_t(blockIdx.x) + unit;
       const int rows = min(p.Mt, use.w.n * p.G - use.rt * p.Mt);
+      if (tid == 0) {
+        if (from_start) p.unit_rec[unit].x = int(rec);
+        if (use.tile + 1 == use.w.nt) p.unit_rec[unit].y = int(rec) + 1;
+      }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         st.l[k] += __shfl_xor_sync(0xffffffffu, st.l[k], 1);
@@ -409,222 +462,70 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
 }
 
 // ------------------------------------------------------------------------------------ merge
-// One CTA per (unit, 16 RG rows, 32 columns of the head): the in-tree term first (64 nodes of
-// K and the slice's 32 columns of V at a time, by keys or rows over the four warps as in the
-// context kernel), then the unit's records streamed on top of it, in CTA order.
-constexpr int kSlice = 32;
+// One thread per four elements of a row: the row's records in CTA order, each weighted by
+// exp2(m_x - max m) (a record without keys has m = -inf, l = 0).  A stream over the records, a few
+// microseconds; launched early, it finds its row while the records are still being written.
+constexpr int kMergeThreads = 256;
 
 template <typename T>
-__device__ __forceinline__ bool not_finite16(uint16_t x);
-template <>
-__device__ __forceinline__ bool not_finite16<__nv_bfloat16>(uint16_t x) {
-  return (x & 0x7f80u) == 0x7f80u;
-}
-template <>
-__device__ __forceinline__ bool not_finite16<__half>(uint16_t x) {
-  return (x & 0x7c00u) == 0x7c00u;
-}
-
-template <typename T, int D, int RG>
-__global__ void __launch_bounds__(kThreads) tree_merge_kernel(const TreeParams p) {
-  constexpr int kKG = 4 / RG;
-  constexpr int kKeysW = kTileKeys / kKG;
-  constexpr int kRows = 16 * RG;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  T* s_k = reinterpret_cast<T*>(smem);                       // [64][D]
-  T* s_v = s_k + kTileKeys * D;                              // [64][32]
-  float* s_o = reinterpret_cast<float*>(s_v + kTileKeys * kSlice);   // [4 warps][16][32]
-  __shared__ long long s_scan[kThreads / 32];
-  __shared__ long long s_before;
-  __shared__ float2 s_ml[4][16];
-  __shared__ unsigned long long s_flag;
-
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rg = warp / kKG, kg = warp % kKG;
-  const int subs = p.Mt / kRows;
-  const int unit = blockIdx.x / subs, sub = blockIdx.x % subs;
-  const int rt = unit % p.RT, bh = unit / p.RT;
-  const int head = bh % p.Hkv, b = bh / p.Hkv;
-  const int col0 = blockIdx.y * kSlice;
-  bool bad = false;
-  const SeqWork w = seq_work(p, b, bad);
-  const int row0 = rt * p.Mt + sub * kRows;
-  const int rows = min(kRows, w.n * p.G - row0);
-  if (rows <= 0) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    return;
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeParams p, int d4_shift, int mt_shift) {
+  const unsigned idx = blockIdx.x * kMergeThreads + threadIdx.x;
+  const unsigned unit = idx >> (d4_shift + mt_shift);
+  const int c = int(idx & ((1u << d4_shift) - 1)) * 4, r = int((idx >> d4_shift) & ((1u << mt_shift) - 1));
+  const int rt = unit % p.RT, bh = unit / p.RT, head = bh % p.Hkv, b = bh / p.Hkv;
+  int row = 0, n0 = 0;
+  bool live = b < p.B;
+  if (live) {
+    bool bad = false;
+    const int n = seq_nodes(p, b, n0, bad);
+    row = rt * p.Mt + r;
+    live = row < n * p.G;
   }
-
-  // the in-tree term
-  uint32_t qf[D / 16][4];
-  Rows<kSlice> st;
-  st.clear();
-  load_q<D>(qf, p, w.n0, w.n, head, row0 + rg * 16);
-  const uint8_t* mrow[2];
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    const int r = row0 + rg * 16 + (lane >> 2) + 8 * k;
-    mrow[k] = p.mask && r / p.G < w.n ? p.mask + int64_t(w.n0 + r / p.G) * p.mask_row : nullptr;
-  }
-  for (int j0 = 0; j0 < w.n; j0 += kTileKeys) {
-    constexpr int kChunks = D / 8;
-    __syncthreads();   // the last tile's readers are done
-    if (tid == 0) s_flag = 0;
-    for (int i = tid; i < kTileKeys * kChunks; i += kThreads) {
-      const int r = i / kChunks, ch = i % kChunks;
-      const bool there = j0 + r < w.n;
-      const int64_t node = there ? w.n0 + j0 + r : w.n0;
-      cp_async16(s_k + swz<D>(r, ch), p.kb + node * p.kb_node + head * p.kb_head + ch * 16, there);
-    }
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = tid / 4 + 32 * i, ch = tid % 4;
-      const bool there = j0 + r < w.n;
-      const int64_t node = there ? w.n0 + j0 + r : w.n0;
-      cp_async16(s_v + swz_v<kSlice>(r, ch), p.vb + node * p.vb_node + head * p.vb_head + col0 * 2 + ch * 16, there);
-    }
-    cp_async_commit();
-    cp_async_wait<0>();
-    __syncthreads();
-    // A node's V may hold infinities or NaN that only the rows which see it may meet, but the
-    // product below multiplies every V by P = 0 elsewhere: take such values out (each thread
-    // checks what it loaded) and add them back where they are seen.
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = tid / 4 + 32 * i;
-      uint16_t* x = reinterpret_cast<uint16_t*>(s_v + swz_v<kSlice>(r, tid % 4));
-      bool any = false;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (not_finite16<T>(x[e])) {
-          x[e] = 0;
-          any = true;
-        }
-      if (any) atomicOr(&s_flag, 1ull << r);
-    }
-    __syncthreads();
-    float s[kKeysW / 8][4];
-    scores<T, D, kKeysW>(s, qf, s_k, kg * kKeysW);
-#pragma unroll
-    for (int i = 0; i < kKeysW / 8; ++i) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = j0 + kg * kKeysW + 8 * i + 2 * (lane & 3) + (e & 1);
-        const bool sees = j < w.n && (p.mask == nullptr || (mrow[e >> 1] && mrow[e >> 1][j]));
-        s[i][e] = sees ? s[i][e] * p.scale_log2 : -INFINITY;
-      }
-    }
-    softmax_step<T, kSlice, kKeysW>(st, s, s_v, kg * kKeysW);
-    unsigned long long flag = s_flag >> (kg * kKeysW) & (kKeysW == 64 ? ~0ull : (1ull << (kKeysW & 63)) - 1);
-    while (flag) {
-      const int j = j0 + kg * kKeysW + __ffsll(flag) - 1;
-      flag &= flag - 1;
-      const T* v = reinterpret_cast<const T*>(p.vb + int64_t(w.n0 + j) * p.vb_node + head * p.vb_head) + col0;
-#pragma unroll
-      for (int i = 0; i < kSlice / 8; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = float(v[8 * i + 2 * (lane & 3) + (e & 1)]);
-          if (!isfinite(x) && (p.mask == nullptr || (mrow[e >> 1] && mrow[e >> 1][j]))) st.o[i][e] += x;
-        }
-    }
-  }
-
-  // the four warps' parts to shared memory
-#pragma unroll
-  for (int k = 0; k < 2; ++k) {
-    st.l[k] += __shfl_xor_sync(0xffffffffu, st.l[k], 1);
-    st.l[k] += __shfl_xor_sync(0xffffffffu, st.l[k], 2);
-    if ((lane & 3) == 0) s_ml[warp][(lane >> 2) + 8 * k] = make_float2(st.m[k], st.l[k]);
-  }
-#pragma unroll
-  for (int i = 0; i < kSlice / 8; ++i)
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      *reinterpret_cast<float2*>(s_o + (warp * 16 + (lane >> 2) + 8 * k) * kSlice + 8 * i + 2 * (lane & 3)) =
-          make_float2(st.o[i][2 * k], st.o[i][2 * k + 1]);
-
-  // the line: where this sequence begins, how long it is
-  const int per = (p.B + kThreads - 1) / kThreads;
-  const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-  long long mine = 0, before;
-  for (int i = b0; i < b1; ++i) mine += seq_work(p, i, bad).tiles;
-  const long long W = block_prefix<kThreads>(mine, before, s_scan);
-  if (b >= b0 && b < b1) {
-    for (int i = b0; i < b; ++i) before += seq_work(p, i, bad).tiles;
-    s_before = before;
-  }
-  __syncthreads();
-
-  // the context records: written by the kernel before this one in the stream
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  size_t rec0 = 0, rec1 = 0;
-  if (w.nt > 0) {
-    const int ctas = int(min((long long)(p.ctas), W));
-    const long long u0 = s_before + ((long long)(head) * w.rts + rt) * w.nt;
-    rec0 = size_t(unit) + cta_of(u0, W, ctas);
-    rec1 = size_t(unit) + cta_of(u0 + w.nt - 1, W, ctas) + 1;
-  }
-  constexpr int kVec = kRows * kSlice / 4 / kThreads;   // float4s of a thread
+  if (!live) return;
+  const int2 span = p.unit_rec[unit];
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kBatch = 8;
+#pragma unroll 1
+  for (int r0 = span.x; r0 < span.y; r0 += kBatch) {
+    float2 ml[kBatch];
+    float4 y[kBatch];
+    float nm = m;
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int e = i * kThreads + tid, r = e / (kSlice / 4), c = (e % (kSlice / 4)) * 4;
-    if (r >= rows) continue;
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int wr = (r / 16) * kKG, rr = r % 16;
-#pragma unroll
-    for (int x = 0; x < kKG; ++x) m = fmaxf(m, s_ml[wr + x][rr].x);
-    float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll
-    for (int x = 0; x < kKG; ++x) {
-      const float f = fast_exp2(s_ml[wr + x][rr].x - ref);
-      const float4 y = *reinterpret_cast<const float4*>(s_o + ((wr + x) * 16 + rr) * kSlice + c);
-      l += s_ml[wr + x][rr].y * f;
-      o = make_float4(o.x + y.x * f, o.y + y.y * f, o.z + y.z * f, o.w + y.w * f);
-    }
-    const size_t at = size_t(sub) * kRows + r;
-    constexpr int kBatch = 8;
-    for (size_t r0 = rec0; r0 < rec1; r0 += kBatch) {
-      float2 ml[kBatch];
-      float4 y[kBatch];
-      const int nb = int(min(size_t(kBatch), rec1 - r0));
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        if (k < nb) {
-          ml[k] = p.rec_ml[(r0 + k) * p.Mt + at];
-          y[k] = *reinterpret_cast<const float4*>(p.rec_o + ((r0 + k) * p.Mt + at) * D + col0 + c);
-        }
+    for (int k = 0; k < kBatch; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (r0 + k < span.y) {
+        const size_t at = size_t(r0 + k) * p.Mt + r;
+        ml[k] = p.rec_ml[at];
+        y[k] = *reinterpret_cast<const float4*>(p.rec_o + (at << (d4_shift + 2)) + c);
       }
-      float nm = m;
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k)
-        if (k < nb) nm = fmaxf(nm, ml[k].x);
-      const float nref = nm == -INFINITY ? 0.f : nm;
-      const float f0 = fast_exp2(m - nref);
-      l *= f0;
-      o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        if (k < nb) {
-          const float f = fast_exp2(ml[k].x - nref);
-          l += ml[k].y * f;
-          o = make_float4(o.x + y[k].x * f, o.y + y[k].y * f, o.z + y[k].z * f, o.w + y[k].w * f);
-        }
-      }
-      m = nm;
     }
-    const int row = row0 + r, node = w.n0 + row / p.G, h = head * p.G + row % p.G;
-    const float inv = l == 0.f ? 0.f : 1.f / l;   // no key: o = 0 (a NaN sum stays NaN)
-    o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-    const size_t dst = (size_t(node) * p.Hq + h) * D + col0 + c;
-    if (p.o_f32)
-      *reinterpret_cast<float4*>(p.o + dst * 4) = o;
-    else
-      *reinterpret_cast<uint2*>(p.o + dst * 2) = make_uint2(pack2(o.x, o.y, T()), pack2(o.z, o.w, T()));
-    if (blockIdx.y == 0 && c == 0)
-      p.lse[size_t(node) * p.Hq + h] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) nm = fmaxf(nm, ml[k].x);
+    const float ref = nm == -INFINITY ? 0.f : nm;
+    const float f0 = fast_exp2(m - ref);
+    l *= f0;
+    o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (r0 + k < span.y) {
+        const float f = fast_exp2(ml[k].x - ref);
+        l += ml[k].y * f;
+        o = make_float4(o.x + y[k].x * f, o.y + y[k].y * f, o.z + y[k].z * f, o.w + y[k].w * f);
+      }
+    }
+    m = nm;
   }
+  const int node = n0 + row / p.G, h = head * p.G + row % p.G;
+  const float inv = l == 0.f ? 0.f : 1.f / l;   // no key: o = 0 (a NaN sum stays NaN)
+  o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  const size_t hr = size_t(node) * p.Hq + h, dst = (hr << (d4_shift + 2)) + c;
+  if (p.o_f32)
+    *reinterpret_cast<float4*>(p.o + dst * 4) = o;
+  else
+    *reinterpret_cast<uint2*>(p.o + dst * 2) = make_uint2(pack2(o.x, o.y, T()), pack2(o.z, o.w, T()));
+  if (c == 0) p.lse[hr] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <typename T, int D, int RG>
@@ -642,27 +543,22 @@ cudaError_t context_rows(const TreeParams& p, cudaStream_t s) {
   return p.Mt == 16 ? context<T, D, 1>(p, s) : p.Mt == 32 ? context<T, D, 2>(p, s) : context<T, D, 4>(p, s);
 }
 
-template <typename T, int D, int RG>
+template <typename T>
 cudaError_t merge(const TreeParams& p, cudaStream_t s) {
-  constexpr int kSmem = kTileKeys * (D + kSlice) * 2 + 4 * 16 * kSlice * 4;
-  const int64_t units = int64_t(p.B) * p.Hkv * p.RT * (p.Mt / (16 * RG));
-  if (units > 0x7fffffff) return cudaErrorInvalidValue;
+  int d4_shift = p.d == 128 ? 5 : 4, mt_shift = 4;
+  while ((1 << mt_shift) < p.Mt) ++mt_shift;
+  const int64_t threads = int64_t(p.B) * p.Hkv * p.RT << (d4_shift + mt_shift);
+  if (threads > 0xffffffffll - kMergeThreads) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(units), D / kSlice);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.gridDim = dim3(unsigned((threads + kMergeThreads - 1) / kMergeThreads));
+  cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<T, D, RG>, p);
-}
-
-template <typename T, int D>
-cudaError_t merge_rows(const TreeParams& p, cudaStream_t s) {
-  return p.Mt >= 64 ? merge<T, D, 4>(p, s) : merge<T, D, 1>(p, s);
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<T>, p, d4_shift, mt_shift);
 }
 
 }  // namespace
@@ -674,9 +570,7 @@ cudaError_t launch_tree_context_mma(const TreeParams& p, int dtype, cudaStream_t
 }
 
 cudaError_t launch_tree_merge(const TreeParams& p, int dtype, cudaStream_t s) {
-  if (dtype == SPLITKV_DTYPE_BF16)
-    return p.d == 128 ? merge_rows<__nv_bfloat16, 128>(p, s) : merge_rows<__nv_bfloat16, 64>(p, s);
-  return p.d == 128 ? merge_rows<__half, 128>(p, s) : merge_rows<__half, 64>(p, s);
+  return dtype == SPLITKV_DTYPE_BF16 ? merge<__nv_bfloat16>(p, s) : merge<__half>(p, s);
 }
 
 }  // namespace tree
@@ -689,7 +583,7 @@ using splitkv::tree::TreeParams;
 
 struct TreeSizes {
   int Mt, RT, ctas, tile_shift;
-  size_t units, ml_off, status_off, total;
+  size_t units, ml_off, unit_off, status_off, total;
 };
 
 int sm_count() {
@@ -699,14 +593,17 @@ int sm_count() {
   return sms;
 }
 
-// Whether a tensor map can describe the cache: pages of 8 tokens or more (a swizzle atom), and a
+// Whether tensor maps can describe the cache and the nodes' keys and values: pages of 8 tokens or more (a swizzle atom), and a
 // stride for every dimension longer than one.
 bool maps_ok(const splitkv_tree_args* a) {
   const auto side = [&](const int64_t* s) {
     return (a->num_pages == 1 || s[0] > 0) && s[1] > 0 && (a->num_kv_heads == 1 || s[2] > 0);
   };
+  const auto rows = [&](const int64_t* s) {
+    return (a->num_nodes == 1 || s[0] > 0) && (a->num_kv_heads == 1 || s[1] > 0);
+  };
   return a->page_size >= 8 && a->num_pages > 0 && a->max_pages > 0 && side(a->k_stride) && side(a->v_stride) &&
-         splitkv::tensor_maps_available();
+         rows(a->kb_stride) && rows(a->vb_stride) && splitkv::tensor_maps_available();
 }
 
 // SPLITKV_TREE_KERNEL=mma or =tcgen05 in the environment asks for one of the context kernels.
@@ -736,15 +633,17 @@ int check_sizes(const splitkv_tree_args* a, TreeSizes* z) {
   z->tile_shift = tc ? 7 : 6;
   z->RT = (rows + z->Mt - 1) / z->Mt;
   z->units = size_t(a->num_seqs) * a->num_kv_heads * z->RT;
-  if (z->units > 0x1fffffff) return SPLITKV_ERR_UNSUPPORTED;
+  if (z->units * z->Mt * (a->head_dim / 4) > 0xfff00000u) return SPLITKV_ERR_UNSUPPORTED;   // the merge's threads
   // One tcgen05 CTA to an SM, two of mma.sync, and no more than the longest line has tiles.
-  const size_t tiles =
-      z->units * ((size_t(a->max_pages) * a->page_size + (size_t(1) << z->tile_shift) - 1) >> z->tile_shift);
+  const size_t round = (size_t(1) << z->tile_shift) - 1;
+  const size_t tiles = z->units * (((size_t(a->max_pages) * a->page_size + round) >> z->tile_shift) +
+                                   ((size_t(a->max_nodes) + round) >> z->tile_shift));
   const size_t ctas = size_t(tc ? 1 : 2) * sm_count();
   z->ctas = int(tiles < ctas ? (tiles > 0 ? tiles : 1) : ctas);
   const size_t recs = z->units + z->ctas;
   z->ml_off = splitkv::align_up(recs * z->Mt * a->head_dim * sizeof(float), 256);
-  z->status_off = z->ml_off + splitkv::align_up(recs * z->Mt * sizeof(float2), 256);
+  z->unit_off = z->ml_off + splitkv::align_up(recs * z->Mt * sizeof(float2), 256);
+  z->status_off = z->unit_off + splitkv::align_up(z->units * sizeof(int2), 256);
   z->total = z->status_off + 256;
   return SPLITKV_OK;
 }
@@ -827,6 +726,7 @@ extern "C" int splitkv_tree_attn(const splitkv_tree_args* a, void* ws, size_t ws
   p.scale_log2 = a->scale * splitkv::kLog2e;
   p.rec_o = static_cast<float*>(ws);
   p.rec_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + z.ml_off);
+  p.unit_rec = reinterpret_cast<int2*>(static_cast<char*>(ws) + z.unit_off);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = z.tile_shift == 7 ? splitkv::tree::launch_tree_context_sm100(p, a->dtype, s)
                                     : splitkv::tree::launch_tree_context_mma(p, a->dtype, s);

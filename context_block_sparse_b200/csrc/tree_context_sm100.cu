@@ -39,7 +39,7 @@ using namespace sm100;
 
 constexpr int kKeys = 128;                    // keys of a tile (M of the first product)
 constexpr uint32_t kHalf = kKeys * 128;       // bytes of 128 rows x 64 columns
-constexpr uint32_t kBarBytes = 768;           // barrier block
+constexpr uint32_t kBarBytes = 896;           // barrier block
 constexpr int kMetaRing = 16;                 // page-error masks in flight (K tiles)
 constexpr float kHeadroom = 8.0f;             // log2: P up to 256 (float16 P stays far from its limits)
 constexpr int kFile = 8 * 10000;              // site number of this file's waits
@@ -117,9 +117,9 @@ struct Dims {
 
 // One stretch of a unit's tiles on this CTA, as the loading warp hands it to the others.
 struct Segment {
-  int n0, rows, len;       // first node; rows of the row tile (past NR: a full one); context length
-  int tile0, tiles;        // key tiles; tiles == 0: the end
-  int rt, head, unit;
+  int n0, n, rows, len;    // first node, nodes; rows of the row tile (past NR: a full one); context length
+  int tile0, tiles, ctx;   // key tiles (tiles == 0: the end); tiles from number ctx on are the tree's
+  int rt, head, unit, last;   // last: the unit ends with this segment
 };
 constexpr int kSegRing = 4;
 
@@ -134,6 +134,7 @@ struct Bars {
   uint32_t tmem_base;
   int abort_flag;
   int bad[kMetaRing];
+  uint32_t flag[2][kMaxNodes / 32];   // by segment parity: nodes whose V is not all finite
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
 
@@ -162,11 +163,14 @@ struct Walk {
     s.head = unit / w.rts;
     s.rt = unit % w.rts;
     s.n0 = w.n0;
+    s.n = w.n;
+    s.ctx = w.ctx;
     s.rows = w.n * p.G - s.rt * p.Mt;
     s.len = w.len;
     s.unit = (b * p.Hkv + s.head) * p.RT + s.rt;
     s.tile0 = tile;
     s.tiles = int(min((long long)(w.nt - tile), left));
+    s.last = tile + s.tiles == w.nt;
     left -= s.tiles;
     ++unit;
     tile = 0;
@@ -177,6 +181,7 @@ struct Walk {
 template <typename T, int D, int NR>
 __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
     tree_context_sm100_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                              const __grid_constant__ CUtensorMap tm_kb, const __grid_constant__ CUtensorMap tm_vb,
                               const TreeParams p) {
   using Dm = Dims<D, NR>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -216,6 +221,8 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
   if (warp == kSoftWarps && lane == 0) {
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
+    prefetch_tmap(&tm_kb);
+    prefetch_tmap(&tm_vb);
   }
   // this CTA's stretch of the line, and the sequence it begins in
   const int per = (p.B + Dm::kThreads - 1) / Dm::kThreads;
@@ -256,21 +263,29 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
     Walk walk;
     walk.begin(p, work ? bars->seq : 0, work ? bars->rel : 0, n_tiles);
     const int boxes = kKeys / box;
-    // lane l's page id of a tile (lanes past the tile's pages: none)
+    // lane l's page of a tile
     auto page_of = [&](const Segment& s, int j) -> int {
       const int key = (s.tile0 + j) * kKeys + lane * box;
-      if (lane >= boxes || key >= s.len) return -2;        // no box
-      return p.table[walk.b * p.table_row + (key >> p.page_shift)];
+      if (s.tile0 + j >= s.ctx) return lane == 0 ? -3 : -2;   // a tile of the tree: one box
+      if (lane >= boxes || key >= s.len) return -2;           // no box
+      const int pg = p.table[walk.b * p.table_row + (key >> p.page_shift)];
+      return pg < 0 || pg >= p.num_pages ? -1 : pg;           // -1: a page that does not exist
     };
-    auto load = [&](const CUtensorMap* map, const Segment& s, int j, int pg) -> bool {
+    auto load = [&](const CUtensorMap* map, const CUtensorMap* tree, const Segment& s, int j, int pg) -> bool {
       const int slot = int(c % Dm::kStages);
       if (!warp_wait(&bars->empty[slot], ((c / Dm::kStages) & 1) ^ 1, wctx, kFile + __LINE__)) return false;
+      const bool nodes = s.tile0 + j >= s.ctx;
       const int n = __popc(__ballot_sync(0xffffffffu, pg != -2));
-      if (lane == 0) mbar_expect_tx(&bars->full[slot], uint32_t(n) * box * 128 * (D / 64));
+      if (lane == 0) mbar_expect_tx(&bars->full[slot], nodes ? Dm::kTile : uint32_t(n) * box * 128 * (D / 64));
       __syncwarp();
-      if (pg != -2) {
+      if (pg == -3) {
+        // 128 rows of the nodes' array: rows of other sequences are masked, rows behind the array read as zeros
+        for (int h = 0; h < D / 64; ++h)
+          tma_load_4d(smem + slot * Dm::kTile + h * kHalf, tree, &bars->full[slot], h * 64, s.head,
+                      s.n0 + (s.tile0 + j - s.ctx) * kKeys, 0);
+      } else if (pg != -2) {
         // a page outside the cache reads as zeros: a page coordinate past the last one
-        const int pc = pg < 0 || pg >= p.num_pages ? p.num_pages : pg;
+        const int pc = pg < 0 ? p.num_pages : pg;
         const int at = ((s.tile0 + j) * kKeys + lane * box) & (page - 1);
         for (int h = 0; h < D / 64; ++h)
           tma_load_4d(smem + slot * Dm::kTile + h * kHalf + lane * box * 128, map, &bars->full[slot], h * 64, s.head, at,
@@ -280,7 +295,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
       return true;
     };
     auto note = [&](int pg) {     // pages of a K tile that do not exist, for the softmax
-      const bool wrong = pg != -2 && (pg < 0 || pg >= p.num_pages);
+      const bool wrong = pg == -1;
       const uint32_t m = __ballot_sync(0xffffffffu, wrong);
       if (lane == 0) {
         bars->bad[kc % kMetaRing] = int(m);
@@ -300,14 +315,14 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
       if (!more) break;
       int now = page_of(sg, 0), nxt = sg.tiles > 1 ? page_of(sg, 1) : -2;
       note(now);
-      if (!load(&tm_k, sg, 0, now)) { ok = false; break; }
+      if (!load(&tm_k, &tm_kb, sg, 0, now)) { ok = false; break; }
       for (int j = 0; j < sg.tiles; ++j) {
         const int ahead = j + 2 < sg.tiles ? page_of(sg, j + 2) : -2;
         if (j + 1 < sg.tiles) {
           note(nxt);
-          if (!load(&tm_k, sg, j + 1, nxt)) { ok = false; break; }
+          if (!load(&tm_k, &tm_kb, sg, j + 1, nxt)) { ok = false; break; }
         }
-        if (!load(&tm_v, sg, j, now)) { ok = false; break; }
+        if (!load(&tm_v, &tm_vb, sg, j, now)) { ok = false; break; }
         now = nxt;
         nxt = ahead;
       }
@@ -437,14 +452,28 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
       if ((tid & 127) < Dm::kCols) nref[tid & 127] = -0.0f;
       bool need = live > 0;       // a row has no reference yet
       group_sync(g);
-      int end = (s.tile0 + 1) * kKeys;     // behind the tile's last key
-      for (int j = 0; j < tiles; ++j, ++t, end += kKeys) {
-        const int key = end - kKeys + key_lane;
+      const int tile0 = s.tile0, ctx = s.ctx, nodes = s.n;
+      for (int j = 0; j < tiles; ++j, ++t) {
+        // the tile's keys: how many there are, and which of this thread's rows see its key (bit c: row col0 + c)
+        const bool tree = tile0 + j >= ctx;
+        const int key0 = (tile0 + j - (tree ? ctx : 0)) * kKeys, limit = (tree ? nodes : len) - key0;
+        unsigned long long bits = key_lane < limit ? ~0ull : 0ull;
+        if (tree && bits != 0 && p.mask != nullptr) {
+          bits = 0;
+          const int first = s.rt * NR + col0, last = min(first + Dm::kCols, s.rt * NR + rows);
+          const uint8_t* m = p.mask + int64_t(s.n0) * p.mask_row + key0 + key_lane;
+#pragma unroll 4
+          for (int i = first / p.G; i * p.G < last; ++i) {
+            const int lo = max(i * p.G - first, 0), n_rows = min((i + 1) * p.G - first, 64) - lo;
+            const unsigned long long some = n_rows >= 64 ? ~0ull : (1ull << n_rows) - 1;
+            if (m[i * p.mask_row]) bits |= some << lo;
+          }
+        }
         ok = ok && warp_wait(&bars->s_full, t & 1, wctx, kFile + __LINE__);
         tc_fence_after();
         const uint32_t wrong = uint32_t(bars->bad[t % kMetaRing]);
-        const bool valid = key < len && !((wrong >> (key_lane / box)) & 1u);
-        const bool part = wrong != 0 || end > len;
+        if ((wrong >> (key_lane / box)) & 1u) bits = 0;
+        const bool part = wrong != 0 || limit < kKeys || tree;
         // scores in log2 units, shifted by the rows' references; is one of them past the headroom?
         float x[kW];
         float mx = -INFINITY;
@@ -462,6 +491,13 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
                 float y0, y1, y2, y3;
                 ffma2(y0, y1, __uint_as_float(v[i]), __uint_as_float(v[i + 1]), scale, scale, r.x, r.y);
                 ffma2(y2, y3, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]), scale, scale, r.z, r.w);
+                if (part) {
+                  const uint32_t see = uint32_t(bits >> (e + i));
+                  y0 = see & 1u ? y0 : -INFINITY;
+                  y1 = see & 2u ? y1 : -INFINITY;
+                  y2 = see & 4u ? y2 : -INFINITY;
+                  y3 = see & 8u ? y3 : -INFINITY;
+                }
                 mx = fmax3(mx, y0, y1);
                 mx = fmax3(mx, y2, y3);
                 if constexpr (kKeep) {
@@ -475,7 +511,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
           }
         }
         bool over = need;
-        if (!need && live > 0) over = group_any(g, valid && mx > kHeadroom);
+        if (!need && live > 0) over = group_any(g, mx > kHeadroom);
         if (over) {
           need = false;
 #pragma unroll 1
@@ -492,7 +528,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
               reg_fence<16>(v);
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                const float y = warp_max(valid ? __uint_as_float(v[i]) * scale : -INFINITY);
+                const float y = warp_max((bits >> (ch * 32 + e + i)) & 1 ? __uint_as_float(v[i]) * scale : -INFINITY);
                 m = lane == e + i ? y : m;
               }
             }
@@ -586,7 +622,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
             for (int i = 0; i < kW; ++i) x[i] = fast_exp2(x[i]);
             if (part) {
 #pragma unroll
-              for (int i = 0; i < kW; ++i) x[i] = valid ? x[i] : 0.f;
+              for (int i = 0; i < kW; ++i) x[i] = (bits >> (w * kW + i)) & 1 ? x[i] : 0.f;
             }
             if constexpr (kPair) {
 #pragma unroll
@@ -606,15 +642,34 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
                              pack<T>(x[8 * i + 4], x[8 * i + 5]), pack<T>(x[8 * i + 6], x[8 * i + 7]));
           }
         }
-        if (g == 0 && end > len) {
-          // the context ends inside this tile, the unit's last: V rows behind it become zeros
-          const uint32_t i = ring0 + 2 * tiles - 1;
+        if (g == 0 && part) {
+          // V rows of keys that are not there become zeros: P = 0 does not hide a NaN.  Nor does it in a tree's V, which
+          // may hold infinities or NaN that only the rows that see them may meet: they are taken out here, and added
+          // back in the epilogue to the rows that see them.
+          const uint32_t i = ring0 + (j + 1 < tiles ? 2 * j + 2 : 2 * j + 1);
           ok = ok && warp_wait(&bars->full[i % Dm::kStages], (i / Dm::kStages) & 1, wctx, kFile + __LINE__);
-          if (ok && key >= len) {
+          uint32_t* flag = bars->flag[seg & 1];
+          if (tree) {
+            if (tile0 + j == max(ctx, tile0) && tid < kMaxNodes / 32) flag[tid] = 0;
+            group_sync(0);
+          }
+          uint8_t* row = smem + (i % Dm::kStages) * Dm::kTile + key_lane * 128;
+          if (ok && key_lane >= limit) {
             for (int h = 0; h < D / 64; ++h)
-              for (int e = 0; e < 8; ++e)
-                *reinterpret_cast<uint4*>(smem + (i % Dm::kStages) * Dm::kTile + h * kHalf + key_lane * 128 + e * 16) =
-                    make_uint4(0, 0, 0, 0);
+              for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(row + h * kHalf + e * 16) = make_uint4(0, 0, 0, 0);
+          } else if (ok && tree) {
+            bool any = false;
+#pragma unroll 1
+            for (int e = 0; e < D / 2; ++e) {
+              uint16_t* y = reinterpret_cast<uint16_t*>(row + (e >> 5) * kHalf + (e & 31) * 4);
+#pragma unroll
+              for (int f = 0; f < 2; ++f)
+                if (not_finite16<T>(y[f])) {
+                  y[f] = 0;
+                  any = true;
+                }
+            }
+            if (any) atomicOr(&flag[(key0 + key_lane) >> 5], 1u << (key_lane & 31));
           }
         }
         fence_async_smem();
@@ -628,6 +683,13 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
       ok = ok && warp_wait(&bars->o_done, (t - 1) & 1, wctx, kFile + __LINE__);
       tc_fence_after();
       const size_t rec = size_t(blockIdx.x) + s.unit;
+      if (tid == 0) {
+        if (tile0 == 0) p.unit_rec[s.unit].x = int(rec);
+        if (s.last) p.unit_rec[s.unit].y = int(rec) + 1;
+      }
+      uint32_t odd_v = 0;      // a node whose V is not all finite
+      if (tile0 + tiles > ctx)
+        for (int i = 0; i < kMaxNodes / 32; ++i) odd_v |= bars->flag[seg & 1][i];
       float* dst = p.rec_o + (rec * NR + col0) * D + key_lane;
 #pragma unroll 1
       for (int ch = 0; ch < live; ++ch) {
@@ -636,6 +698,21 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
         tmem_wait_ld();
         reg_fence<32>(o);
         if (D == 128 || wq < D / 32) {
+          if (odd_v) {
+#pragma unroll 1
+            for (int j = max(0, tile0 - ctx) * kKeys; j < min(nodes, (tile0 + tiles - ctx) * kKeys); ++j) {
+              if (!((bars->flag[seg & 1][j >> 5] >> (j & 31)) & 1u)) continue;
+              const float y = float(*reinterpret_cast<const T*>(p.vb + int64_t(s.n0 + j) * p.vb_node +
+                                                                s.head * p.vb_head + key_lane * 2));
+              if (isfinite(y)) continue;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) {
+                const int node = (s.rt * NR + col0 + ch * 32 + i) / p.G;
+                if (node < nodes && (p.mask == nullptr || p.mask[int64_t(s.n0 + node) * p.mask_row + j]))
+                  o[i] = __float_as_uint(__uint_as_float(o[i]) + y);
+              }
+            }
+          }
 #pragma unroll
           for (int i = 0; i < 32; ++i)
             if (col0 + ch * 32 + i < rows) dst[(ch * 32 + i) * D] = __uint_as_float(o[i]);
@@ -687,22 +764,22 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
 }
 
 template <typename T, int D, int NR>
-cudaError_t launch(const TreeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+cudaError_t launch(const TreeParams& p, const CUtensorMap* m, cudaStream_t s) {
   using Dm = Dims<D, NR>;
   cudaError_t e = cudaFuncSetAttribute(tree_context_sm100_kernel<T, D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        int(Dm::kSmem));
   if (e != cudaSuccess) return e;
-  tree_context_sm100_kernel<T, D, NR><<<p.ctas, Dm::kThreads, Dm::kSmem, s>>>(tk, tv, p);
+  tree_context_sm100_kernel<T, D, NR><<<p.ctas, Dm::kThreads, Dm::kSmem, s>>>(m[0], m[1], m[2], m[3], p);
   return cudaGetLastError();
 }
 
 template <typename T, int D>
-cudaError_t rows(const TreeParams& p, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t s) {
+cudaError_t rows(const TreeParams& p, const CUtensorMap* m, cudaStream_t s) {
   switch (p.Mt) {
-    case 32: return launch<T, D, 32>(p, tk, tv, s);
-    case 64: return launch<T, D, 64>(p, tk, tv, s);
-    case 128: return launch<T, D, 128>(p, tk, tv, s);
-    default: return launch<T, D, 256>(p, tk, tv, s);
+    case 32: return launch<T, D, 32>(p, m, s);
+    case 64: return launch<T, D, 64>(p, m, s);
+    case 128: return launch<T, D, 128>(p, m, s);
+    default: return launch<T, D, 256>(p, m, s);
   }
 }
 
@@ -712,12 +789,14 @@ cudaError_t launch_tree_context_sm100(const TreeParams& p, int dtype, cudaStream
   const bool f16 = dtype == SPLITKV_DTYPE_F16;
   const int page = 1 << p.page_shift;
   const uint32_t box = page < kKeys ? page : kKeys;
-  CUtensorMap tk, tv;
-  if (!make_page_map_4d(&tk, p.kc, f16, p.d, p.Hkv, page, p.num_pages, p.kc_head, p.kc_slot, p.kc_page, box) ||
-      !make_page_map_4d(&tv, p.vc, f16, p.d, p.Hkv, page, p.num_pages, p.vc_head, p.vc_slot, p.vc_page, box))
+  CUtensorMap m[4];
+  if (!make_page_map_4d(&m[0], p.kc, f16, p.d, p.Hkv, page, p.num_pages, p.kc_head, p.kc_slot, p.kc_page, box) ||
+      !make_page_map_4d(&m[1], p.vc, f16, p.d, p.Hkv, page, p.num_pages, p.vc_head, p.vc_slot, p.vc_page, box) ||
+      !make_page_map_4d(&m[2], p.kb, f16, p.d, p.Hkv, p.Nq, 1, p.kb_head, p.kb_node, 0, kKeys) ||
+      !make_page_map_4d(&m[3], p.vb, f16, p.d, p.Hkv, p.Nq, 1, p.vb_head, p.vb_node, 0, kKeys))
     return cudaErrorInvalidValue;
-  if (f16) return p.d == 128 ? rows<__half, 128>(p, tk, tv, s) : rows<__half, 64>(p, tk, tv, s);
-  return p.d == 128 ? rows<__nv_bfloat16, 128>(p, tk, tv, s) : rows<__nv_bfloat16, 64>(p, tk, tv, s);
+  if (f16) return p.d == 128 ? rows<__half, 128>(p, m, s) : rows<__half, 64>(p, m, s);
+  return p.d == 128 ? rows<__nv_bfloat16, 128>(p, m, s) : rows<__nv_bfloat16, 64>(p, m, s);
 }
 
 }  // namespace tree

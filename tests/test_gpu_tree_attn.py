@@ -78,6 +78,8 @@ class Case:
     ([40, 64, 1], [200, 333, 50], 4, 1, 256),               # many row tiles
     ([256, 3], [70, 640], 2, 1, 8),                         # the widest tree; pages of 8
     ([2, 2], [129, 5], 3, 1, 1),                            # pages of a single token, three heads
+    ([3, 2], [129, 256], 80, 1, 16),                        # 80 heads on one: a node's rows cross the row groups
+    ([130, 129, 1], [128, 0, 127], 3, 1, 32),               # two tree tiles; rows of a node across row tiles
 ])
 def test_matches_64_bits(splitkv, counts, lens, hq, hkv, page, dt, d):
     c = Case(counts, lens, hq, hkv, d, page, dt, seed=len(counts) + page)
@@ -193,7 +195,7 @@ def test_bad_device_arrays_are_recorded_and_skipped(splitkv):
     tree = SplitKVTreeAttention(4, 2, 64, c.max_nodes)
     good = c.call(tree)
     tree.check()
-    for bad_page in (-1, c.k.shape[0], 2 ** 31 - 1, -2 ** 31):
+    for bad_page in (-1, -2, -3, c.k.shape[0], 2 ** 31 - 1, -2 ** 31):
         table = c.table.clone()
         table[1, 1] = bad_page                                     # keys 16..31 of sequence 1
         got = c.call(tree, page_table=table)
