@@ -116,15 +116,26 @@ __device__ __forceinline__ long long block_prefix(long long mine, long long& bef
 // First tile of CTA c's stretch (c in [0, C]); C never exceeds the line's length W.
 __device__ __forceinline__ long long stretch(long long W, int c, int C) { return W * c / C; }
 
+// Infinities and NaN among the 16-bit values of x are replaced by 0; returns whether there were any.
 template <typename T>
-__device__ __forceinline__ bool not_finite16(uint16_t x);   // bits of a T
-template <>
-__device__ __forceinline__ bool not_finite16<__nv_bfloat16>(uint16_t x) {
-  return (x & 0x7f80u) == 0x7f80u;
+__device__ __forceinline__ bool take_out(uint4& x);
+__device__ __forceinline__ bool take_out_bits(uint4& x, uint32_t exponent) {
+  uint32_t* w = &x.x;
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) any |= __vcmpeq2(w[i] & exponent, exponent);
+  if (any == 0) return false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] &= ~__vcmpeq2(w[i] & exponent, exponent);
+  return true;
 }
 template <>
-__device__ __forceinline__ bool not_finite16<__half>(uint16_t x) {
-  return (x & 0x7c00u) == 0x7c00u;
+__device__ __forceinline__ bool take_out<__nv_bfloat16>(uint4& x) {
+  return take_out_bits(x, 0x7f807f80u);
+}
+template <>
+__device__ __forceinline__ bool take_out<__half>(uint4& x) {
+  return take_out_bits(x, 0x7c007c00u);
 }
 
 #endif  // __CUDACC__

@@ -341,19 +341,15 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
       // every V by P = 0 elsewhere: take such values out here and add them back where they are seen.
       if (tid == 0) s_flag = 0;
       __syncthreads();
-      uint16_t* sv = reinterpret_cast<uint16_t*>(sk + kTileKeys * D);
-#pragma unroll 1
-      for (int i = tid; i < kTileKeys * kChunks; i += kThreads) {
-        uint16_t* x = sv + swz<D>(i / kChunks, i % kChunks);
-        bool any = false;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (not_finite16<T>(x[e])) {
-            x[e] = 0;
-            any = true;
-          }
+      const int here = min(kTileKeys, use.w.n - tree0);
+#pragma unroll 2
+      for (int i = tid; i < here * kChunks; i += kThreads) {
+        uint4* at = reinterpret_cast<uint4*>(sk + kTileKeys * D + swz<D>(i / kChunks, i % kChunks));
+        uint4 x = *at;
+        if (take_out<T>(x)) {
+          *at = x;
+          atomicOr(&s_flag, 1ull << (i / kChunks));
         }
-        if (any) atomicOr(&s_flag, 1ull << (i / kChunks));
       }
       __syncthreads();
     }

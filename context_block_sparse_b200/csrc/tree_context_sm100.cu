@@ -653,23 +653,24 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
             if (tile0 + j == max(ctx, tile0) && tid < kMaxNodes / 32) flag[tid] = 0;
             group_sync(0);
           }
-          uint8_t* row = smem + (i % Dm::kStages) * Dm::kTile + key_lane * 128;
+          uint8_t* v = smem + (i % Dm::kStages) * Dm::kTile;
           if (ok && key_lane >= limit) {
-            for (int h = 0; h < D / 64; ++h)
-              for (int e = 0; e < 8; ++e) *reinterpret_cast<uint4*>(row + h * kHalf + e * 16) = make_uint4(0, 0, 0, 0);
-          } else if (ok && tree) {
-            bool any = false;
-#pragma unroll 1
-            for (int e = 0; e < D / 2; ++e) {
-              uint16_t* y = reinterpret_cast<uint16_t*>(row + (e >> 5) * kHalf + (e & 31) * 4);
 #pragma unroll
-              for (int f = 0; f < 2; ++f)
-                if (not_finite16<T>(y[f])) {
-                  y[f] = 0;
-                  any = true;
-                }
+            for (int e = 0; e < D / 8; ++e)
+              *reinterpret_cast<uint4*>(v + (e >> 3) * kHalf + key_lane * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          if (ok && tree) {
+            const int n16 = min(limit, kKeys) * (D / 8);     // 16-byte pieces of the nodes' rows
+#pragma unroll 2
+            for (int e = tid; e < n16; e += 128) {
+              const int key = e / (D / 8), ch = e % (D / 8);
+              uint4* at = reinterpret_cast<uint4*>(v + (ch >> 3) * kHalf + key * 128 + (ch & 7) * 16);
+              uint4 x = *at;
+              if (take_out<T>(x)) {
+                *at = x;
+                atomicOr(&flag[(key0 + key) >> 5], 1u << (key & 31));
+              }
             }
-            if (any) atomicOr(&flag[(key0 + key_lane) >> 5], 1u << (key_lane & 31));
           }
         }
         fence_async_smem();
