@@ -719,7 +719,8 @@ extern "C" int splitkv_tree_attn(const splitkv_tree_args* a, void* ws, size_t ws
   p.max_pages = a->max_pages;
   p.ctas = z.ctas;
   p.o_f32 = a->o_dtype == SPLITKV_DTYPE_F32;
-  p.scale_log2 = a->scale * splitkv::kLog2e;
+  // (a scale of 0 as a tiny one: scores stay 0 for any finite product, and a masked score can still be -inf)
+  p.scale_log2 = a->scale == 0.f ? 1e-30f : a->scale * splitkv::kLog2e;
   p.rec_o = static_cast<float*>(ws);
   p.rec_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + z.ml_off);
   p.unit_rec = reinterpret_cast<int2*>(static_cast<char*>(ws) + z.unit_off);

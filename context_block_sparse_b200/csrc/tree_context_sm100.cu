@@ -412,25 +412,58 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
     const int pch0 = (col0 & 63) >> 3;
     float* nref = s_nref + col0;
     float* fac = s_f + col0;
+    float* s_x = s_f + NR + g * (4 * Dm::kCols);   // the warps' maxima, then their row sums (not at NR = 256)
     const float scale = p.scale_log2;
     uint32_t t = 0, ring0 = 0;      // tiles and ring slots of the segments before
     bool ok = true;
 
-    auto load_q = [&](const Segment& s) {
-      // rows col0.. of the tile into the K-major operand layout, rows past the tile's end zero
+    // Rows col0.. of a row tile's queries into the K-major operand layout, rows past the tile's end zero: requested
+    // (after the last scores that read the buffer) and, a tile later, handed to the products.
+    auto request_q = [&](const Segment& s) {
       constexpr int kCh = D / 8;
       const int n_rows = s.rows, n0 = s.n0, first = s.rt * NR, h0 = s.head * p.G;
+#pragma unroll 1
       for (int i = tid & 127; i < Dm::kCols * kCh; i += 128) {
         const int r = col0 + i / kCh, ch = i % kCh;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < n_rows) {
-          const int row = first + r, node = row / p.G, h = h0 + row - node * p.G;
-          x = __ldg(reinterpret_cast<const uint4*>(p.q + int64_t(n0 + node) * p.q_node + int64_t(h) * p.q_head + ch * 16));
-        }
-        *reinterpret_cast<uint4*>(smem + Dm::kOffQ + (ch >> 3) * (NR * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = x;
+        const int row = r < n_rows ? first + r : first, node = row / p.G, h = h0 + row - node * p.G;
+        cp_async16(smem + Dm::kOffQ + (ch >> 3) * (NR * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                   p.q + int64_t(n0 + node) * p.q_node + int64_t(h) * p.q_head + ch * 16, r < n_rows);
       }
+      cp_async_commit();
+    };
+    auto deliver_q = [&]() {
+      cp_async_wait<0>();
       fence_async_smem();
       warp_arrive(&bars->q_full);
+    };
+    // A tile with keys that are not there or that not every row sees: their scores in tensor memory become what the
+    // scale turns into -inf, so that nothing after this knows of masks.
+    const float hidden = scale > 0.f ? -INFINITY : INFINITY;
+    auto hide = [&](const Segment& s, bool tree, int key0, int limit, uint32_t wrong) {
+      unsigned long long bits = key_lane < limit && !((wrong >> (key_lane / box)) & 1u) ? ~0ull : 0ull;   // bit c: row col0 + c
+      if (tree && bits != 0 && p.mask != nullptr) {
+        bits = 0;
+        const int first = s.rt * NR + col0, last = min(first + Dm::kCols, s.rt * NR + s.rows);
+        const uint8_t* m = p.mask + int64_t(s.n0) * p.mask_row + key0 + key_lane;
+#pragma unroll 8
+        for (int i = first / p.G; i * p.G < last; ++i) {
+          const int lo = max(i * p.G - first, 0), n = min((i + 1) * p.G - first, 64) - lo;
+          const unsigned long long some = n >= 64 ? ~0ull : (1ull << n) - 1;
+          if (m[i * p.mask_row]) bits |= some << lo;
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < Dm::kCols; e += 16) {
+        uint32_t v[16];
+        tmem_ld16(tS + e, v);
+        tmem_wait_ld();
+        reg_fence<16>(v);
+        const uint32_t see = uint32_t(bits >> e);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = see >> i & 1u ? v[i] : __float_as_uint(hidden);
+        tmem_st16(tS + e, v);
+      }
+      tmem_wait_st();
     };
     // After a wait gave up (ok is false, the kernel winds down) a warp goes on without waiting to the end of its segment,
     // where the group leaves together: its barriers always meet.  What is written until then lies inside its records.
@@ -441,7 +474,10 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
     };
     uint32_t seg = 0;
     bool more = open(0);
-    if (more) load_q(bars->seg[0]);
+    if (more) {
+      request_q(bars->seg[0]);
+      deliver_q();
+    }
     while (more) {
       const Segment& s = bars->seg[seg % kSegRing];
       const int rows = min(NR, s.rows), len = s.len, tiles = s.tiles;
@@ -454,26 +490,18 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
       group_sync(g);
       const int tile0 = s.tile0, ctx = s.ctx, nodes = s.n;
       for (int j = 0; j < tiles; ++j, ++t) {
-        // the tile's keys: how many there are, and which of this thread's rows see its key (bit c: row col0 + c)
         const bool tree = tile0 + j >= ctx;
-        const int key0 = (tile0 + j - (tree ? ctx : 0)) * kKeys, limit = (tree ? nodes : len) - key0;
-        unsigned long long bits = key_lane < limit ? ~0ull : 0ull;
-        if (tree && bits != 0 && p.mask != nullptr) {
-          bits = 0;
-          const int first = s.rt * NR + col0, last = min(first + Dm::kCols, s.rt * NR + rows);
-          const uint8_t* m = p.mask + int64_t(s.n0) * p.mask_row + key0 + key_lane;
-#pragma unroll 4
-          for (int i = first / p.G; i * p.G < last; ++i) {
-            const int lo = max(i * p.G - first, 0), n_rows = min((i + 1) * p.G - first, 64) - lo;
-            const unsigned long long some = n_rows >= 64 ? ~0ull : (1ull << n_rows) - 1;
-            if (m[i * p.mask_row]) bits |= some << lo;
-          }
-        }
+        const int key0 = (tile0 + j - (tree ? ctx : 0)) * kKeys, limit = (tree ? nodes : len) - key0;   // keys there are
         ok = ok && warp_wait(&bars->s_full, t & 1, wctx, kFile + __LINE__);
         tc_fence_after();
+        if (j + 1 == tiles) {
+          // the unit's last scores are formed: the next unit's queries may come
+          more = open(seg + 1);
+          if (more) request_q(bars->seg[(seg + 1) % kSegRing]);
+        }
         const uint32_t wrong = uint32_t(bars->bad[t % kMetaRing]);
-        if ((wrong >> (key_lane / box)) & 1u) bits = 0;
         const bool part = wrong != 0 || limit < kKeys || tree;
+        if (part && live > 0) hide(s, tree, key0, limit, wrong);
         // scores in log2 units, shifted by the rows' references; is one of them past the headroom?
         float x[kW];
         float mx = -INFINITY;
@@ -491,13 +519,6 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
                 float y0, y1, y2, y3;
                 ffma2(y0, y1, __uint_as_float(v[i]), __uint_as_float(v[i + 1]), scale, scale, r.x, r.y);
                 ffma2(y2, y3, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]), scale, scale, r.z, r.w);
-                if (part) {
-                  const uint32_t see = uint32_t(bits >> (e + i));
-                  y0 = see & 1u ? y0 : -INFINITY;
-                  y1 = see & 2u ? y1 : -INFINITY;
-                  y2 = see & 4u ? y2 : -INFINITY;
-                  y3 = see & 8u ? y3 : -INFINITY;
-                }
                 mx = fmax3(mx, y0, y1);
                 mx = fmax3(mx, y2, y3);
                 if constexpr (kKeep) {
@@ -528,30 +549,39 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
               reg_fence<16>(v);
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
-                const float y = warp_max((bits >> (ch * 32 + e + i)) & 1 ? __uint_as_float(v[i]) * scale : -INFINITY);
+                const float y = warp_max(__uint_as_float(v[i]) * scale);
                 m = lane == e + i ? y : m;
               }
             }
-            // exchanged through the factors' and shifts' slots of this chunk, two warps at a time
             const uint32_t was = __float_as_uint(nr[lane]);
             const float old = was == 0x80000000u ? -INFINITY : -__uint_as_float(was);
-            group_sync(g);
-            if (wq == 0) fc[lane] = m;
-            if (wq == 1) nr[lane] = m;
-            group_sync(g);
-            if (wq == 2) fc[lane] = fmaxf(fc[lane], m);
-            if (wq == 3) nr[lane] = fmaxf(nr[lane], m);
-            group_sync(g);
-            m = fmaxf(fc[lane], nr[lane]);
+            if constexpr (Dm::kPBufs == 2) {
+              s_x[wq * Dm::kCols + ch * 32 + lane] = m;
+              group_sync(g);
+#pragma unroll
+              for (int w = 0; w < 4; ++w) m = fmaxf(m, s_x[w * Dm::kCols + ch * 32 + lane]);
+            } else {
+              // (no room: through the factors' and shifts' slots of this chunk, two warps at a time)
+              group_sync(g);
+              if (wq == 0) fc[lane] = m;
+              if (wq == 1) nr[lane] = m;
+              group_sync(g);
+              if (wq == 2) fc[lane] = fmaxf(fc[lane], m);
+              if (wq == 3) nr[lane] = fmaxf(nr[lane], m);
+              group_sync(g);
+              m = fmaxf(fc[lane], nr[lane]);
+              group_sync(g);
+            }
+            // (the four warps hold the same values, so their votes agree)
             const float to = old == -INFINITY ? m : (m > old + kHeadroom ? m : old);
             const float f = old == -INFINITY ? 1.f : fast_exp2(old - to);
-            group_sync(g);
             if (wq == 0) {
               nr[lane] = to == -INFINITY ? -0.0f : 0.f - to;
               fc[lane] = f;
             }
-            const bool moved = group_any(g, f != 1.f);
-            need |= group_any(g, to == -INFINITY);
+            const bool moved = __any_sync(0xffffffffu, f != 1.f);
+            need |= __any_sync(0xffffffffu, to == -INFINITY) != 0;
+            group_sync(g);
             if (moved) {
 #pragma unroll
               for (int c = 0; c < kChunks; ++c) {
@@ -620,10 +650,6 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
             }
 #pragma unroll
             for (int i = 0; i < kW; ++i) x[i] = fast_exp2(x[i]);
-            if (part) {
-#pragma unroll
-              for (int i = 0; i < kW; ++i) x[i] = (bits >> (w * kW + i)) & 1 ? x[i] : 0.f;
-            }
             if constexpr (kPair) {
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
@@ -678,9 +704,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
         warp_arrive(&bars->p_ready[t & 1]);
       }
       ring0 += 2 * tiles;
-      // the next unit's queries (the last scores of this one are done), so that its first scores overlap this epilogue
-      more = open(seg + 1);
-      if (more) load_q(bars->seg[(seg + 1) % kSegRing]);
+      if (more) deliver_q();   // the next unit's first scores overlap this epilogue
       ok = ok && warp_wait(&bars->o_done, (t - 1) & 1, wctx, kFile + __LINE__);
       tc_fence_after();
       const size_t rec = size_t(blockIdx.x) + s.unit;
@@ -734,7 +758,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
           }
           r += up ? n : 0;
         }
-        float* s_l = Dm::kPBufs == 2 ? s_f + NR + g * (4 * Dm::kCols)
+        float* s_l = Dm::kPBufs == 2 ? s_x
                                      : reinterpret_cast<float*>(smem + Dm::kOffP + g * kHalf);   // read by no product now
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {
