@@ -4,9 +4,10 @@
 // A unit is one (sequence, KV head, row tile): up to Mt rows (node-major, the G query heads
 // of a node next to each other) against the sequence's whole context and then its own tree, in
 // key tiles of 64 or 128 keys (a tile holds one kind).  All units' tiles lie on one line, in
-// (sequence, KV head, row tile, key tile) order, and
-// CTA c of C takes the stretch [c W / C, (c + 1) W / C) of its W tiles: every CTA has the same
-// number of tiles to within one, whatever the lengths, and the lengths stay on the device (a
+// (sequence, KV head, row tile, key tile) order, each unit behind `lead` empty places that stand
+// for what a unit costs besides its tiles, and
+// CTA c of C takes the stretch [c W / C, (c + 1) W / C) of its W places: every CTA has the same
+// work to within a tile, whatever the lengths, and the lengths stay on the device (a
 // captured graph replays with new ones).  A CTA's part of a unit is one record (unnormalised
 // O, row maximum, row sum).  Walking the line, either the CTA or the unit number steps at
 // each boundary, so record (c, u) is number c + u: C + U - 1 records at most, no atomics and a
@@ -39,6 +40,7 @@ struct TreeParams {
   int64_t mask_row, table_row;     // elements
   int B, Nq, T, Hq, Hkv, G, d;
   int Mt, RT;                      // rows of a row tile; row tiles of max_nodes nodes
+  int lead;                        // empty places before a unit's tiles
   int tile_shift;                  // log2 of the keys of a tile: 6 (mma.sync) or 7 (tcgen05)
   int page_shift, num_pages, max_pages;
   int ctas;                        // C: CTAs of the context kernel
@@ -75,7 +77,7 @@ __device__ __forceinline__ int seq_len(const TreeParams& p, int b, bool& bad) {
 struct SeqWork {
   int n0, n, len, rts;       // first node, nodes, context length, row tiles
   int ctx, nt;               // context tiles of a unit, and all of them
-  long long tiles;           // Hkv * rts * nt
+  long long places;          // Hkv * rts * (lead + nt)
 };
 
 __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b, bool& bad) {
@@ -86,7 +88,7 @@ __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b, bool& ba
   const int round = (1 << p.tile_shift) - 1;
   w.ctx = (w.len + round) >> p.tile_shift;
   w.nt = w.ctx + ((w.n + round) >> p.tile_shift);
-  w.tiles = (long long)(p.Hkv) * w.rts * w.nt;
+  w.places = (long long)(p.Hkv) * w.rts * (p.lead + w.nt);
   return w;
 }
 
@@ -113,7 +115,7 @@ __device__ __forceinline__ long long block_prefix(long long mine, long long& bef
   return all;
 }
 
-// First tile of CTA c's stretch (c in [0, C]); C never exceeds the line's length W.
+// First place of CTA c's stretch (c in [0, C]); C never exceeds the line's length W.
 __device__ __forceinline__ long long stretch(long long W, int c, int C) { return W * c / C; }
 
 // Infinities and NaN among the 16-bit values of x are replaced by 0; returns whether there were any.

@@ -192,7 +192,7 @@ struct Cursor {
       ++b;
       if (b >= p.B) return;
       w = seq_work(p, b, bad);
-    } while (w.tiles == 0);
+    } while (w.places == 0);
   }
 };
 
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   long long mine = 0, before;
   bool bad = false;
-  for (int b = b0; b < b1; ++b) mine += seq_work(p, b, bad).tiles;
+  for (int b = b0; b < b1; ++b) mine += seq_work(p, b, bad).places;
   if (bad && blockIdx.x == 0) atomicCAS(p.status, 0, SPLITKV_ERR_INVALID_ARG);
   const long long W = block_prefix<kThreads>(mine, before, s_scan);
   const int ctas = int(min((long long)(p.ctas), W));
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
   if (x0 >= before && x0 < before + mine) {
     long long at = before;
     for (int b = b0; b < b1; ++b) {
-      const long long t = seq_work(p, b, bad).tiles;
+      const long long t = seq_work(p, b, bad).places;
       if (x0 < at + t) {
         s_seq = b;
         s_rel = x0 - at;
@@ -630,11 +630,11 @@ int check_sizes(const splitkv_tree_args* a, TreeSizes* z) {
   z->RT = (rows + z->Mt - 1) / z->Mt;
   z->units = size_t(a->num_seqs) * a->num_kv_heads * z->RT;
   if (z->units * z->Mt * (a->head_dim / 4) > 0xfff00000u) return SPLITKV_ERR_UNSUPPORTED;   // the merge's threads
-  // One tcgen05 CTA to an SM, two of mma.sync, and no more than the longest line has tiles.
+  // One tcgen05 CTA to an SM (two at d = 64 and few rows), two of mma.sync, and no more than the longest line has tiles.
   const size_t round = (size_t(1) << z->tile_shift) - 1;
   const size_t tiles = z->units * (((size_t(a->max_pages) * a->page_size + round) >> z->tile_shift) +
                                    ((size_t(a->max_nodes) + round) >> z->tile_shift));
-  const size_t ctas = size_t(tc ? 1 : 2) * sm_count();
+  const size_t ctas = size_t(tc && !(a->head_dim == 64 && z->Mt <= 64) ? 1 : 2) * sm_count();
   z->ctas = int(tiles < ctas ? (tiles > 0 ? tiles : 1) : ctas);
   const size_t recs = z->units + z->ctas;
   z->ml_off = splitkv::align_up(recs * z->Mt * a->head_dim * sizeof(float), 256);
@@ -713,6 +713,9 @@ extern "C" int splitkv_tree_attn(const splitkv_tree_args* a, void* ws, size_t ws
   p.Mt = z.Mt;
   p.RT = z.RT;
   p.tile_shift = z.tile_shift;
+  // A unit on tcgen05 costs about as much as three tiles more than its tiles (first references, queries, record): 16 ragged
+  // trees over 1k-8k took LEADNUM.  The mma.sync kernel's units are cheap.
+  p.lead = z.tile_shift == 7 ? 3 : 0;
   p.page_shift = 0;
   while ((1 << p.page_shift) < a->page_size) ++p.page_shift;
   p.num_pages = a->num_pages;

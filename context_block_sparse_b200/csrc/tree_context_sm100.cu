@@ -98,13 +98,17 @@ struct Dims {
   static constexpr int kCols = NR <= 128 ? 32 : 64;
   static constexpr int kGroups = NR / kCols;
   static constexpr int kThreads = 128 * kGroups + 64;
-  static constexpr int kPBufs = NR <= 128 ? 2 : 1;           // P^T buffers
+  // Two CTAs to an SM at d = 64 and few rows (a tile is half as long there as one CTA's chain of products, softmax and
+  // barriers), else one with P^T double-buffered where it fits.
+  static constexpr int kPerSm = D == 64 && NR <= 64 ? 2 : 1;
+  static constexpr int kPBufs = NR <= 128 && kPerSm == 1 ? 2 : 1;
+  static constexpr bool kRoomX = NR <= 128;                  // room for the warps' maxima and row sums
   static constexpr uint32_t kTile = uint32_t(D / 64) * kHalf;
   static constexpr uint32_t kQ = uint32_t(D / 64) * NR * 128;
   static constexpr uint32_t kP = uint32_t((NR + 63) / 64) * kHalf;
   // barriers, shifts, factors, and the warps' row sums (at NR = 256 these take a group's own half of P^T)
-  static constexpr uint32_t kMeta = kBarBytes + NR * 8 + (kPBufs == 2 ? NR * 16 : 0);
-  static constexpr int kFit = int((232448 - kMeta - kQ - kPBufs * kP) / kTile);
+  static constexpr uint32_t kMeta = kBarBytes + NR * 8 + (kRoomX ? NR * 16 : 0);
+  static constexpr int kFit = int(((kPerSm == 2 ? 115712 : 232448) - kMeta - kQ - kPBufs * kP) / kTile);
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static_assert(kStages >= 3, "ring");
   // the ring comes first: at d = 64 the second half of the V^T operand's M is whatever follows the tile
@@ -125,7 +129,7 @@ constexpr int kSegRing = 4;
 
 struct Bars {
   uint64_t full[8], empty[8];
-  uint64_t q_full, s_full, s_free, p_ready[2], p_free[2], o_done, mma_done;
+  uint64_t q_full, s_full, s_free, p_ready[2], p_free[2], mma_done;
   uint64_t seg_full[kSegRing], seg_empty[kSegRing];   // one arrival of the loading warp; of every reader
   Segment seg[kSegRing];
   long long scan[20];
@@ -140,8 +144,8 @@ static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
 
 // The segments of a CTA's stretch of the line, in order.
 struct Walk {
-  long long left;   // tiles not yet handed out
-  int b, unit, tile;
+  long long left;   // places not yet handed out
+  int b, unit, at;  // the next place: `at` of unit `unit` of sequence b
   SeqWork w;
   bool bad;
   __device__ void begin(const TreeParams& p, int seq, long long rel, long long n) {
@@ -150,36 +154,40 @@ struct Walk {
     bad = false;
     if (n <= 0) return;
     w = seq_work(p, b, bad);
-    unit = int(rel / w.nt);
-    tile = int(rel % w.nt);
+    unit = int(rel / (p.lead + w.nt));
+    at = int(rel % (p.lead + w.nt));
   }
   __device__ bool next(const TreeParams& p, Segment& s) {
-    if (left <= 0) return false;
-    while (unit >= p.Hkv * w.rts || w.tiles == 0) {
-      if (++b >= p.B) return false;
-      w = seq_work(p, b, bad);
-      unit = tile = 0;
+    while (left > 0) {
+      while (unit >= p.Hkv * w.rts || w.places == 0) {
+        if (++b >= p.B) return false;
+        w = seq_work(p, b, bad);
+        unit = at = 0;
+      }
+      const int take = int(min((long long)(p.lead + w.nt - at), left));
+      s.head = unit / w.rts;
+      s.rt = unit % w.rts;
+      s.tile0 = max(0, at - p.lead);
+      s.tiles = max(0, at + take - p.lead) - s.tile0;
+      s.last = at + take == p.lead + w.nt;
+      left -= take;
+      ++unit;
+      at = 0;
+      if (s.tiles == 0) continue;      // (only the places before a unit's tiles)
+      s.n0 = w.n0;
+      s.n = w.n;
+      s.ctx = w.ctx;
+      s.rows = w.n * p.G - s.rt * p.Mt;
+      s.len = w.len;
+      s.unit = (b * p.Hkv + s.head) * p.RT + s.rt;
+      return true;
     }
-    s.head = unit / w.rts;
-    s.rt = unit % w.rts;
-    s.n0 = w.n0;
-    s.n = w.n;
-    s.ctx = w.ctx;
-    s.rows = w.n * p.G - s.rt * p.Mt;
-    s.len = w.len;
-    s.unit = (b * p.Hkv + s.head) * p.RT + s.rt;
-    s.tile0 = tile;
-    s.tiles = int(min((long long)(w.nt - tile), left));
-    s.last = tile + s.tiles == w.nt;
-    left -= s.tiles;
-    ++unit;
-    tile = 0;
-    return true;
+    return false;
   }
 };
 
 template <typename T, int D, int NR>
-__global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
+__global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
     tree_context_sm100_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                               const __grid_constant__ CUtensorMap tm_kb, const __grid_constant__ CUtensorMap tm_vb,
                               const TreeParams p) {
@@ -205,7 +213,6 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
       mbar_init(&bars->p_ready[i], kSoftWarps);   // by tile parity: a group may be a tile ahead of another
       mbar_init(&bars->p_free[i], 1);
     }
-    mbar_init(&bars->o_done, 1);
     mbar_init(&bars->mma_done, 1);
     for (int i = 0; i < kSegRing; ++i) {
       mbar_init(&bars->seg_full[i], 1);
@@ -229,17 +236,17 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   long long mine = 0, before;
   bool bad = false;
-  for (int b = b0; b < b1; ++b) mine += seq_work(p, b, bad).tiles;
+  for (int b = b0; b < b1; ++b) mine += seq_work(p, b, bad).places;
   if (bad && blockIdx.x == 0) atomicCAS(p.status, 0, SPLITKV_ERR_INVALID_ARG);
   const long long W = block_prefix<Dm::kThreads>(mine, before, bars->scan);
   const int ctas = int(min((long long)(p.ctas), W));
   const bool work = int(blockIdx.x) < ctas;
   const long long x0 = work ? stretch(W, blockIdx.x, ctas) : 0;
-  const long long n_tiles = work ? stretch(W, blockIdx.x + 1, ctas) - x0 : 0;
+  const long long n_places = work ? stretch(W, blockIdx.x + 1, ctas) - x0 : 0;
   if (work && x0 >= before && x0 < before + mine) {
     long long at = before;
     for (int b = b0; b < b1; ++b) {
-      const long long t = seq_work(p, b, bad).tiles;
+      const long long t = seq_work(p, b, bad).places;
       if (x0 < at + t) {
         bars->seq = b;
         bars->rel = x0 - at;
@@ -261,7 +268,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
     uint32_t c = 0, kc = 0, seg = 0;
     bool ok = true;
     Walk walk;
-    walk.begin(p, work ? bars->seq : 0, work ? bars->rel : 0, n_tiles);
+    walk.begin(p, work ? bars->seq : 0, work ? bars->rel : 0, n_places);
     const int boxes = kKeys / box;
     // lane l's page of a tile
     auto page_of = [&](const Segment& s, int j) -> int {
@@ -384,7 +391,6 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
             mma_ss(tmem + NR, a + (kk * 2048 >> 4), b + (kk * 2048 >> 4), kIdO, kk > 0 ? 1u : (j > 0 ? 1u : 0u));
           mma_commit(&bars->empty[slot]);
           mma_commit(&bars->p_free[t & 1]);
-          mma_commit(&bars->o_done);
           ++c;
         }
       }
@@ -472,6 +478,11 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
       if (group_any(g, !ok)) return false;
       return bars->seg[i % kSegRing].tiles > 0;
     };
+    // Tile i's second product is done.  (By tile parity: with one barrier for all tiles, this wait could meet it two
+    // phases back and take that for done.  The product of tile i - 2 is known to be: tile i's P^T waited for it.)
+    auto done = [&](uint32_t i) -> bool {
+      return warp_wait(&bars->p_free[i & 1], (i >> 1) & 1, wctx, kFile + __LINE__);
+    };
     uint32_t seg = 0;
     bool more = open(0);
     if (more) {
@@ -555,7 +566,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
             }
             const uint32_t was = __float_as_uint(nr[lane]);
             const float old = was == 0x80000000u ? -INFINITY : -__uint_as_float(was);
-            if constexpr (Dm::kPBufs == 2) {
+            if constexpr (Dm::kRoomX) {
               s_x[wq * Dm::kCols + ch * 32 + lane] = m;
               group_sync(g);
 #pragma unroll
@@ -592,7 +603,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
                 }
               }
               if (j > 0) {
-                ok = ok && warp_wait(&bars->o_done, (t - 1) & 1, wctx, kFile + __LINE__);
+                ok = ok && done(t - 1);
                 tc_fence_after();
 #pragma unroll 1
                 for (int e = 0; e < 32; e += 16) {
@@ -627,7 +638,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
         // this P^T buffer may be rewritten once the product that read it is done
         constexpr uint32_t kB = Dm::kPBufs;
         if (t >= kB)
-          ok = ok && warp_wait(&bars->p_free[(t - kB) & 1], ((t - kB) >> 1) & 1, wctx, kFile + __LINE__);
+          ok = ok && done(t - kB);
         uint8_t* pp = my_p + (kB == 2 ? (t & 1) * Dm::kP : 0);
 #pragma unroll
         for (int w = 0; w < Dm::kCols / kW; ++w) {
@@ -705,7 +716,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
       }
       ring0 += 2 * tiles;
       if (more) deliver_q();   // the next unit's first scores overlap this epilogue
-      ok = ok && warp_wait(&bars->o_done, (t - 1) & 1, wctx, kFile + __LINE__);
+      ok = ok && done(t - 1);
       tc_fence_after();
       const size_t rec = size_t(blockIdx.x) + s.unit;
       if (tid == 0) {
@@ -758,7 +769,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, 1)
           }
           r += up ? n : 0;
         }
-        float* s_l = Dm::kPBufs == 2 ? s_x
+        float* s_l = Dm::kRoomX ? s_x
                                      : reinterpret_cast<float*>(smem + Dm::kOffP + g * kHalf);   // read by no product now
 #pragma unroll
         for (int i = 0; i < kChunks; ++i) {

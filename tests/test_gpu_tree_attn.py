@@ -58,9 +58,9 @@ class Case:
         return tree_ref(self.q, self.kb, self.vb, self.ptr, self.mask, self.k, self.v, self.table, self.lens,
                         self.d ** -0.5)
 
-    def check(self, got, out_dtype=None, ref=None):
+    def check(self, got, out_dtype=None, ref=None, rows=None):
         o, lse, to, tl = ref or self.ref()
-        n = int(self.ptr[-1])
+        n = int(self.ptr[-1]) if rows is None else rows
         assert_within("o", got[0][:n], o[:n], to[:n], out_dtype or self.q.dtype)
         assert_within("lse", got[1][:n], lse[:n], tl[:n], torch.float32)
 
@@ -220,13 +220,14 @@ def test_bad_device_arrays_are_recorded_and_skipped(splitkv):
     got = c.call(tree, context_lens=lens)
     with pytest.raises(splitkv.SplitKVError):
         tree.check()
-    assert torch.equal(got[0][:8], good[0][:8])
+    # (another length moves the cuts between the CTAs: the other sequences' results keep their values, not their bits)
+    c.check(got, rows=8)
     ptr = c.ptr.clone()
     ptr[3] = 99                            # past the rows: the last sequence has no nodes
     got = c.call(tree, node_ptr=ptr)
     with pytest.raises(splitkv.SplitKVError):
         tree.check()
-    assert torch.equal(got[0][:8], good[0][:8])
+    c.check(got, rows=8)
     tree.check()
 
 
@@ -242,6 +243,24 @@ def test_offsets_past_32_bits(splitkv):
         k[table[0, i]], v[table[0, i]] = c.k[c.table[0, i]].cuda(), c.v[c.table[0, i]].cuda()
     got = c.call(page_table=table.cuda(), k_cache=k, v_cache=v)
     c.check(got, ref=ref)
+
+
+@pytest.mark.parametrize("args", [([6], [300], 8, 8, 128, 128), ([16, 9], [900, 257], 8, 2, 128, 64),
+                                  ([40], [2000], 4, 1, 64, 16)])
+def test_cold_caches(splitkv, args):
+    """Late keys and values (nothing in L2, the GPU just woken): products queue up behind the softmax's waits."""
+    import time
+    c = Case(*args, seed=12)
+    from context_block_sparse_b200.draft_tree import SplitKVTreeAttention
+    tree = SplitKVTreeAttention(c.hq, c.hkv, c.d, c.max_nodes)
+    a = [x.cuda() for x in (c.q, c.kb, c.vb, c.ptr, c.mask, c.k, c.v, c.table, c.lens)]
+    ref = c.ref()
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for k in range(6):
+        flush.fill_(k)
+        torch.cuda.synchronize()
+        time.sleep(0.02)
+        c.check(tree.forward(*a, c.d ** -0.5), ref=ref)
 
 
 def test_streams_graphs_and_determinism(splitkv):

@@ -1,0 +1,189 @@
+"""Barrier protocol of the tcgen05 tree-attention kernel (tree_context_sm100.cu), on randomised schedules (CPU only).
+
+Roles: a loading warp (segments through a ring of four, then K0, K1, V0, K2, V1, ... through a ring of tiles), a thread
+that issues the products (S of the next tile before PV of this one), and softmax groups that share S, P^T and O by
+columns.  Same model and checks as the training kernels': no wait outside the one-phase window that a parity wait can
+tell apart, every buffer holds what its reader expects, every role finishes; and a wait left out is caught.
+"""
+
+import pytest
+
+from test_kernel_protocols import Bar, Core, Hazard
+
+RING = 4
+
+
+class Tree(Core):
+    def __init__(self, segs, seed, stages=5, bufs=2, groups=2, drop=None):
+        names = ([f"full{i}" for i in range(stages)] + [f"empty{i}" for i in range(stages)] +
+                 ["q_full", "s_full", "s_free", "p_ready0", "p_ready1", "p_free0", "p_free1", "o_done"] +
+                 [f"seg_full{i}" for i in range(RING)] + [f"seg_empty{i}" for i in range(RING)])
+        super().__init__(seed, names)
+        for n in ("q_full", "s_free", "p_ready0", "p_ready1"):
+            self.B[n] = Bar(groups)
+        for i in range(RING):
+            self.B[f"seg_empty{i}"] = Bar(groups + 1)
+        self.segs, self.stages, self.bufs, self.groups, self.drop = segs, stages, bufs, groups, drop
+        self.ring = [None] * stages
+        self.info = [None] * RING
+        self.Q = [None] * groups
+        self.S, self.S_unread = None, 0
+        self.P = [[None] * groups for _ in range(bufs)]
+        self.PV = -1                      # the last tile whose second product has executed
+        self.O, self.O_unread = None, 0
+        self.has_rows = [self.rng.random() < 0.8 or g == 0 for g in range(groups)]
+
+    def w(self, bar, n, name):
+        if self.drop != name and n >= 0:
+            yield from self.wait(bar, n)
+
+    # ---------------------------------------------------------------- the loading warp
+    def loader(self):
+        c = 0
+        for s in range(len(self.segs) + 1):
+            yield from self.w(f"seg_empty{s % RING}", s // RING - 1, "seg_empty")
+            self.info[s % RING] = s
+            self.B[f"seg_full{s % RING}"].arrive()
+            if s == len(self.segs):
+                return
+            n = self.segs[s]
+            order = [("K", 0)]
+            for j in range(n):
+                order += ([("K", j + 1)] if j + 1 < n else []) + [("V", j)]
+            for kind, j in order:
+                slot = c % self.stages
+                yield from self.w(f"empty{slot}", c // self.stages - 1, "empty")
+                self.load(f"full{slot}", lambda slot=slot, x=(kind, s, j): self.land(slot, x))
+                c += 1
+                yield
+
+    def land(self, slot, x):
+        self.check(self.ring[slot] is None, f"{x} lands on {self.ring[slot]}")
+        self.ring[slot] = x
+
+    # ---------------------------------------------------------------- the products
+    def products(self):
+        c, t = 0, 0
+
+        def scores(s, j, t, slot):
+            self.check(self.ring[slot] == ("K", s, j), "K")
+            self.check(all(q == s for q in self.Q), "Q")
+            self.check(self.S_unread == 0, "S overwritten before it was read")
+            self.ring[slot] = None
+            self.S, self.S_unread = t, self.groups
+
+        def second(s, j, t, slot):
+            self.check(self.ring[slot] == ("V", s, j), "V")
+            self.check(all(p == t for p, r in zip(self.P[t % self.bufs], self.has_rows) if r), "P")
+            self.check(self.O == (s, j - 1) if j else self.O_unread == 0, "O")
+            self.ring[slot] = None
+            self.PV = t
+            self.O, self.O_unread = (s, j), self.groups
+
+        def issue_s(s, j, t):
+            nonlocal c
+            yield from self.w("s_free", t - 1, "s_free")
+            yield from self.w(f"full{c % self.stages}", c // self.stages, "K full")
+            self.mma(lambda slot=c % self.stages: scores(s, j, t, slot))
+            self.commit(f"empty{c % self.stages}")
+            self.commit("s_full")
+            c += 1
+
+        for s in range(len(self.segs) + 1):
+            yield from self.w(f"seg_full{s % RING}", s // RING, "seg_full")
+            self.check(self.info[s % RING] == s, "segment")
+            if s == len(self.segs):
+                return
+            self.B[f"seg_empty{s % RING}"].arrive()
+            yield from self.w("q_full", s, "q_full")
+            yield from issue_s(s, 0, t)
+            for j in range(self.segs[s]):
+                if j + 1 < self.segs[s]:
+                    yield from issue_s(s, j + 1, t + 1)
+                yield from self.w(f"p_ready{t % 2}", t // 2, "p_ready")
+                yield from self.w(f"full{c % self.stages}", c // self.stages, "V full")
+                self.mma(lambda slot=c % self.stages, a=(s, j, t): second(*a, slot))
+                self.commit(f"empty{c % self.stages}")
+                self.commit(f"p_free{t % 2}")
+                self.commit("o_done")
+                c, t = c + 1, t + 1
+                yield
+
+    # ---------------------------------------------------------------- a softmax group
+    def done(self, i):
+        if self.drop == "one barrier":
+            yield from self.wait("o_done", i)
+        else:
+            yield from self.w(f"p_free{i % 2}", i // 2, "p_free")
+
+    def group(self, g):
+        def open_(s):
+            yield from self.w(f"seg_full{s % RING}", s // RING, "seg_full")
+            self.check(self.info[s % RING] == s, "segment")
+
+        t, ring0 = 0, 0
+        yield from open_(0)
+        self.Q[g] = 0
+        self.B["q_full"].arrive()
+        for s, n in enumerate(self.segs):
+            for j in range(n):
+                yield from self.w("s_full", t, "s_full")
+                self.check(self.S == t, "S")
+                if j + 1 == n:
+                    yield from open_(s + 1)
+                    if self.drop != "early Q":
+                        self.Q[g] = s + 1
+                elif self.drop == "early Q" and j + 2 == n:
+                    self.Q[g] = s + 1
+                if j and self.has_rows[g] and self.rng.random() < 0.3:     # a reference moves: O is rescaled
+                    yield from self.done(t - 1)
+                    self.check(self.O == (s, j - 1), "O rescaled")
+                yield
+                self.S_unread -= 1
+                self.B["s_free"].arrive()
+                if t >= self.bufs:
+                    yield from self.done(t - self.bufs)
+                    self.check(self.PV >= t - self.bufs, "P rewritten before it was read")
+                self.P[t % self.bufs][g] = t
+                yield
+                if g == 0 and self.rng.random() < 0.4:                     # V rows are zeroed
+                    i = ring0 + (2 * j + 2 if j + 1 < n else 2 * j + 1)
+                    yield from self.w(f"full{i % self.stages}", i // self.stages, "V zeroed")
+                    self.check(self.ring[i % self.stages] == ("V", s, j), "V zeroed")
+                self.B[f"p_ready{t % 2}"].arrive()
+                t += 1
+            ring0 += 2 * n
+            if s + 1 < len(self.segs):
+                self.B["q_full"].arrive()
+            yield from self.done(t - 1)
+            self.check(self.O == (s, n - 1), "O read")
+            self.O_unread -= 1
+            self.B[f"seg_empty{s % RING}"].arrive()
+            yield
+
+    def go(self):
+        roles = {"loader": self.loader(), "products": self.products()}
+        roles.update({f"group{g}": self.group(g) for g in range(self.groups)})
+        self.run(roles)
+
+
+SEGS = [[1], [2, 1], [1, 1, 1, 1, 1, 1, 1], [7], [3, 1, 4, 1, 5], [9, 2, 6]]
+
+
+@pytest.mark.parametrize("stages,bufs,groups", [(5, 2, 2), (3, 1, 4), (5, 1, 2), (8, 2, 1), (4, 2, 4)])
+def test_tree_protocol(stages, bufs, groups):
+    for seed in range(60):
+        Tree(SEGS[seed % len(SEGS)], seed, stages, bufs, groups).go()
+
+
+# (waits that another one implies are not listed: full before the zeroing of V and before the products order different
+# things, but K's arrival is only ever seen by the products)
+@pytest.mark.parametrize("drop", ["seg_empty", "empty", "s_free", "K full", "V full", "p_ready", "s_full", "p_free", "q_full",
+                                  "one barrier", "early Q", "V zeroed"])
+def test_a_missing_wait_is_caught(drop):
+    for seed in range(400):
+        try:
+            Tree(SEGS[seed % len(SEGS)], seed, 8 if drop == "seg_empty" else 5, 2, 2, drop).go()
+        except Hazard:
+            return
+    pytest.fail(f"no schedule shows the hazard that {drop} guards")
