@@ -12,6 +12,11 @@
 // O, row maximum, row sum).  Walking the line, either the CTA or the unit number steps at
 // each boundary, so record (c, u) is number c + u: C + U - 1 records at most, no atomics and a
 // fixed order of the merge.
+//
+// A key of d = 64 is a 128-byte row beside its neighbouring heads', and HBM brings more than that at a
+// time (64 sequences of 8 heads over 4k read 804 MB for 537 MB of keys and values).  So at d = 64 two
+// neighbouring heads are walked by two CTAs in step (`hg` = 2): the line is cut over pairs of heads, and
+// CTA 2 c + e takes head e of each pair in stretch c.
 #pragma once
 
 #include <cstdint>
@@ -43,11 +48,13 @@ struct TreeParams {
   int lead;                        // empty places before a unit's tiles
   int tile_shift;                  // log2 of the keys of a tile: 6 (mma.sync) or 7 (tcgen05)
   int page_shift, num_pages, max_pages;
-  int ctas;                        // C: CTAs of the context kernel
+  int hg;                          // neighbouring heads that as many CTAs walk in step: 1 or 2
+  int ctas;                        // C: stretches; the context kernel has C hg CTAs
+  int recs;                        // records of one of the hg CTAs of every stretch: C + U / hg
   int o_f32;
   float scale_log2;
-  float* rec_o;                    // [C + U][Mt][d]
-  float2* rec_ml;                  // [C + U][Mt]: maximum (log2 units), sum
+  float* rec_o;                    // [hg recs][Mt][d]
+  float2* rec_ml;                  // [hg recs][Mt]: maximum (log2 units), sum
   int2* unit_rec;                  // [U]: a unit's records [x, y)
 };
 
@@ -77,7 +84,7 @@ __device__ __forceinline__ int seq_len(const TreeParams& p, int b, bool& bad) {
 struct SeqWork {
   int n0, n, len, rts;       // first node, nodes, context length, row tiles
   int ctx, nt;               // context tiles of a unit, and all of them
-  long long places;          // Hkv * rts * (lead + nt)
+  long long places;          // Hkv / hg * rts * (lead + nt)
 };
 
 __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b, bool& bad) {
@@ -88,7 +95,7 @@ __device__ __forceinline__ SeqWork seq_work(const TreeParams& p, int b, bool& ba
   const int round = (1 << p.tile_shift) - 1;
   w.ctx = (w.len + round) >> p.tile_shift;
   w.nt = w.ctx + ((w.n + round) >> p.tile_shift);
-  w.places = (long long)(p.Hkv) * w.rts * (p.lead + w.nt);
+  w.places = (long long)(p.Hkv / p.hg) * w.rts * (p.lead + w.nt);
   return w;
 }
 
@@ -113,6 +120,11 @@ __device__ __forceinline__ long long block_prefix(long long mine, long long& bef
   }
   before = add + inc - mine;
   return all;
+}
+
+// The record of this CTA's part of a unit: number c + u among the CTAs of its place e in the pairs.
+__device__ __forceinline__ size_t record(const TreeParams& p, int b, int pair, int rt) {
+  return size_t(blockIdx.x % p.hg) * p.recs + blockIdx.x / p.hg + (size_t(b) * (p.Hkv / p.hg) + pair) * p.RT + rt;
 }
 
 // First place of CTA c's stretch (c in [0, C]); C never exceeds the line's length W.

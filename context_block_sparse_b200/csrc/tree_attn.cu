@@ -170,7 +170,7 @@ __device__ __forceinline__ void softmax_step(Rows<NC>& st, float (&s)[kKeys / 8]
 // A CTA's place on the line: the unit and key tile of the tile it points at.
 struct Cursor {
   SeqWork w;
-  int b, head, rt, tile;
+  int b, head, rt, tile;     // head: pair of heads where they are walked in pairs
   bool bad;
   __device__ __forceinline__ void enter(const TreeParams& p, int seq, long long rel) {
     b = seq;
@@ -186,7 +186,7 @@ struct Cursor {
     tile = 0;
     if (++rt < w.rts) return;
     rt = 0;
-    if (++head < p.Hkv) return;
+    if (++head < p.Hkv / p.hg) return;
     head = 0;
     do {
       ++b;
@@ -230,10 +230,10 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
   for (int b = b0; b < b1; ++b) mine += seq_work(p, b, bad).places;
   if (bad && blockIdx.x == 0) atomicCAS(p.status, 0, SPLITKV_ERR_INVALID_ARG);
   const long long W = block_prefix<kThreads>(mine, before, s_scan);
-  const int ctas = int(min((long long)(p.ctas), W));
-  if (int(blockIdx.x) >= ctas) return;
-  const long long x0 = stretch(W, blockIdx.x, ctas);
-  const int n_tiles = int(stretch(W, blockIdx.x + 1, ctas) - x0);
+  const int ctas = int(min((long long)(p.ctas), W)), mine_c = blockIdx.x / p.hg, sub = blockIdx.x % p.hg;
+  if (mine_c >= ctas) return;
+  const long long x0 = stretch(W, mine_c, ctas);
+  const int n_tiles = int(stretch(W, mine_c + 1, ctas) - x0);
   if (x0 >= before && x0 < before + mine) {
     long long at = before;
     for (int b = b0; b < b1; ++b) {
@@ -281,8 +281,9 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
     T* sv = sk + kTileKeys * D;
     const int ch = tid % kChunks;
     const bool tree = fill.tile >= fill.w.ctx;
-    const char* kbase = (tree ? p.kb + fill.head * p.kb_head : p.kc + fill.head * p.kc_head) + ch * 16;
-    const char* vbase = (tree ? p.vb + fill.head * p.vb_head : p.vc + fill.head * p.vc_head) + ch * 16;
+    const int head = fill.head * p.hg + sub;
+    const char* kbase = (tree ? p.kb + head * p.kb_head : p.kc + head * p.kc_head) + ch * 16;
+    const char* vbase = (tree ? p.vb + head * p.vb_head : p.vc + head * p.vc_head) + ch * 16;
     const int64_t kpage = tree ? p.kb_node : p.kc_page, kslot = tree ? 0 : p.kc_slot;
     const int64_t vpage = tree ? p.vb_node : p.vc_page, vslot = tree ? 0 : p.vc_slot;
     const int slot_mask = (1 << p.page_shift) - 1;
@@ -327,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
       if (t + C::kStages + 1 < n_tiles) load.step(p);
     }
     if (fresh) {
-      load_q<D>(qf, p, use.w.n0, use.w.n, use.head, use.rt * p.Mt + rg * 16);
+      load_q<D>(qf, p, use.w.n0, use.w.n, use.head * p.hg + sub, use.rt * p.Mt + rg * 16);
       st.clear();
       fresh = false;
       from_start = use.tile == 0;
@@ -382,7 +383,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
         const int j = tree0 + kg * C::kKeysW + __ffsll(flag) - 1;
         flag &= flag - 1;
         const bool see[2] = {sees(0, j), sees(1, j)};
-        const T* v = reinterpret_cast<const T*>(p.vb + int64_t(use.w.n0 + j) * p.vb_node + use.head * p.vb_head);
+        const T* v = reinterpret_cast<const T*>(p.vb + int64_t(use.w.n0 + j) * p.vb_node +
+                                                (use.head * p.hg + sub) * p.vb_head);
 #pragma unroll
         for (int i = 0; i < D / 8; ++i)
 #pragma unroll
@@ -396,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
     const bool last = t + 1 == n_tiles || use.tile + 1 == use.w.nt;
     if (last) {
       // the unit's part of this CTA is complete: add the key groups, write the record
-      const int unit = (use.b * p.Hkv + use.head) * p.RT + use.rt;
-      const size_t rec = size_t(blockIdx.x) + unit;
+      const int unit = (use.b * p.Hkv + use.head * p.hg + sub) * p.RT + use.rt;
+      const size_t rec = record(p, use.b, use.head, use.rt);
       const int rows = min(p.Mt, use.w.n * p.G - use.rt * p.Mt);
       if (tid == 0) {
         if (from_start) p.unit_rec[unit].x = int(rec);
@@ -530,7 +532,7 @@ cudaError_t context(const TreeParams& p, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(tree_context_mma_kernel<T, D, RG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        kSmem);
   if (e != cudaSuccess) return e;
-  tree_context_mma_kernel<T, D, RG><<<p.ctas, kThreads, kSmem, s>>>(p);
+  tree_context_mma_kernel<T, D, RG><<<p.ctas * p.hg, kThreads, kSmem, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -578,7 +580,8 @@ namespace {
 using splitkv::tree::TreeParams;
 
 struct TreeSizes {
-  int Mt, RT, ctas, tile_shift;
+  int Mt, RT, hg, ctas, tile_shift;
+  size_t recs;
   size_t units, ml_off, unit_off, status_off, total;
 };
 
@@ -631,12 +634,14 @@ int check_sizes(const splitkv_tree_args* a, TreeSizes* z) {
   z->units = size_t(a->num_seqs) * a->num_kv_heads * z->RT;
   if (z->units * z->Mt * (a->head_dim / 4) > 0xfff00000u) return SPLITKV_ERR_UNSUPPORTED;   // the merge's threads
   // One tcgen05 CTA to an SM (two at d = 64 and few rows), two of mma.sync, and no more than the longest line has tiles.
+  z->hg = a->head_dim == 64 && a->num_kv_heads % 2 == 0 ? 2 : 1;
   const size_t round = (size_t(1) << z->tile_shift) - 1;
-  const size_t tiles = z->units * (((size_t(a->max_pages) * a->page_size + round) >> z->tile_shift) +
-                                   ((size_t(a->max_nodes) + round) >> z->tile_shift));
-  const size_t ctas = size_t(tc && !(a->head_dim == 64 && z->Mt <= 64) ? 1 : 2) * sm_count();
+  const size_t tiles = z->units / z->hg * (((size_t(a->max_pages) * a->page_size + round) >> z->tile_shift) +
+                                           ((size_t(a->max_nodes) + round) >> z->tile_shift));
+  const size_t ctas = size_t(tc && !(a->head_dim == 64 && z->Mt <= 64) ? 1 : 2) * sm_count() / z->hg;
   z->ctas = int(tiles < ctas ? (tiles > 0 ? tiles : 1) : ctas);
-  const size_t recs = z->units + z->ctas;
+  z->recs = z->units / z->hg + z->ctas;
+  const size_t recs = z->recs * z->hg;
   z->ml_off = splitkv::align_up(recs * z->Mt * a->head_dim * sizeof(float), 256);
   z->unit_off = z->ml_off + splitkv::align_up(recs * z->Mt * sizeof(float2), 256);
   z->status_off = z->unit_off + splitkv::align_up(z->units * sizeof(int2), 256);
@@ -720,7 +725,9 @@ extern "C" int splitkv_tree_attn(const splitkv_tree_args* a, void* ws, size_t ws
   while ((1 << p.page_shift) < a->page_size) ++p.page_shift;
   p.num_pages = a->num_pages;
   p.max_pages = a->max_pages;
+  p.hg = z.hg;
   p.ctas = z.ctas;
+  p.recs = int(z.recs);
   p.o_f32 = a->o_dtype == SPLITKV_DTYPE_F32;
   // (a scale of 0 as a tiny one: scores stay 0 for any finite product, and a masked score can still be -inf)
   p.scale_log2 = a->scale == 0.f ? 1e-30f : a->scale * splitkv::kLog2e;

@@ -123,7 +123,7 @@ struct Dims {
 struct Segment {
   int n0, n, rows, len;    // first node, nodes; rows of the row tile (past NR: a full one); context length
   int tile0, tiles, ctx;   // key tiles (tiles == 0: the end); tiles from number ctx on are the tree's
-  int rt, head, unit, last;   // last: the unit ends with this segment
+  int rt, head, unit, rec, last;   // its number and this part's record; last: the unit ends with this segment
 };
 constexpr int kSegRing = 4;
 
@@ -159,13 +159,14 @@ struct Walk {
   }
   __device__ bool next(const TreeParams& p, Segment& s) {
     while (left > 0) {
-      while (unit >= p.Hkv * w.rts || w.places == 0) {
+      while (unit >= p.Hkv / p.hg * w.rts || w.places == 0) {
         if (++b >= p.B) return false;
         w = seq_work(p, b, bad);
         unit = at = 0;
       }
       const int take = int(min((long long)(p.lead + w.nt - at), left));
-      s.head = unit / w.rts;
+      const int pair = unit / w.rts;
+      s.head = pair * p.hg + blockIdx.x % p.hg;
       s.rt = unit % w.rts;
       s.tile0 = max(0, at - p.lead);
       s.tiles = max(0, at + take - p.lead) - s.tile0;
@@ -180,6 +181,7 @@ struct Walk {
       s.rows = w.n * p.G - s.rt * p.Mt;
       s.len = w.len;
       s.unit = (b * p.Hkv + s.head) * p.RT + s.rt;
+      s.rec = int(record(p, b, pair, s.rt));
       return true;
     }
     return false;
@@ -240,9 +242,10 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
   if (bad && blockIdx.x == 0) atomicCAS(p.status, 0, SPLITKV_ERR_INVALID_ARG);
   const long long W = block_prefix<Dm::kThreads>(mine, before, bars->scan);
   const int ctas = int(min((long long)(p.ctas), W));
-  const bool work = int(blockIdx.x) < ctas;
-  const long long x0 = work ? stretch(W, blockIdx.x, ctas) : 0;
-  const long long n_places = work ? stretch(W, blockIdx.x + 1, ctas) - x0 : 0;
+  const int mine_c = blockIdx.x / p.hg;
+  const bool work = mine_c < ctas;
+  const long long x0 = work ? stretch(W, mine_c, ctas) : 0;
+  const long long n_places = work ? stretch(W, mine_c + 1, ctas) - x0 : 0;
   if (work && x0 >= before && x0 < before + mine) {
     long long at = before;
     for (int b = b0; b < b1; ++b) {
@@ -718,7 +721,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
       if (more) deliver_q();   // the next unit's first scores overlap this epilogue
       ok = ok && done(t - 1);
       tc_fence_after();
-      const size_t rec = size_t(blockIdx.x) + s.unit;
+      const size_t rec = s.rec;
       if (tid == 0) {
         if (tile0 == 0) p.unit_rec[s.unit].x = int(rec);
         if (s.last) p.unit_rec[s.unit].y = int(rec) + 1;
@@ -805,7 +808,7 @@ cudaError_t launch(const TreeParams& p, const CUtensorMap* m, cudaStream_t s) {
   cudaError_t e = cudaFuncSetAttribute(tree_context_sm100_kernel<T, D, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        int(Dm::kSmem));
   if (e != cudaSuccess) return e;
-  tree_context_sm100_kernel<T, D, NR><<<p.ctas, Dm::kThreads, Dm::kSmem, s>>>(m[0], m[1], m[2], m[3], p);
+  tree_context_sm100_kernel<T, D, NR><<<p.ctas * p.hg, Dm::kThreads, Dm::kSmem, s>>>(m[0], m[1], m[2], m[3], p);
   return cudaGetLastError();
 }
 
