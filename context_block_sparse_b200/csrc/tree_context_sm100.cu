@@ -408,7 +408,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
     const int key_lane = wq * 32 + lane;               // key of a tile = TMEM lane; head element in O^T
     const int col0 = g * Dm::kCols;                    // this group's rows
     constexpr int kChunks = Dm::kCols / 32;
-    constexpr bool kKeep = NR <= 64;                   // scores stay in registers between the check and the exponentials
+    constexpr bool kKeep = NR <= 64 && (NR == 32 || Dm::kPerSm == 1);   // scores stay in registers between the check and the exponentials
     constexpr int kW = kKeep ? Dm::kCols : 16;         // rows of one pass of exponentials
     // Row sums of a thread: its own share of every row of the group; at NR = 256 two neighbouring lanes add theirs at
     // every tile and each keeps half.
