@@ -485,8 +485,7 @@ def library_path() -> str:
 
 
 # The rotary and draft-tree entry points are bound in draft_calls.py, which needs torch at import.
-_DRAFT_CALLS = ("splitkv_rope_freqs", "splitkv_rope", "splitkv_tree_workspace_size", "splitkv_tree_attn",
-                "splitkv_tree_verify", "splitkv_tree_commit")
+_DRAFT_CALLS = ("splitkv_rope_freqs", "splitkv_rope", "splitkv_tree_attn", "splitkv_tree_verify", "splitkv_tree_commit")
 
 
 def __getattr__(name):

@@ -8,7 +8,6 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libsplitkv.so")
 
@@ -151,20 +150,6 @@ class CommitArgs(ctypes.Structure):
         l kb_stride[3] vb_stride[3] k_stride[4] v_stride[4] path_stride table_stride""")
 
 
-def packer(cls):
-    """A function that packs one value per scalar (arrays spread out, NULL pointers as 0) into the bytes of a
-    `cls`, laid out as the C struct: several times faster than filling the ctypes structure field by field."""
-    codes = {ctypes.c_int32: "i", ctypes.c_uint32: "I", ctypes.c_int64: "q", ctypes.c_float: "f",
-             ctypes.c_double: "d", ctypes.c_void_p: "P"}
-    fmt = "@"
-    for _, kind in cls._fields_:
-        n = getattr(kind, "_length_", 1)
-        fmt += codes[getattr(kind, "_type_", kind) if n > 1 else kind] * n
-    s = struct.Struct(fmt)
-    assert s.size == ctypes.sizeof(cls), cls
-    return s.pack
-
-
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
@@ -204,11 +189,11 @@ SIGNATURES = {
     "splitkv_selftest_wait_timeout": (_I, [ctypes.POINTER(ctypes.c_int32), _P]),
     "splitkv_rope_freqs": (_I, [ctypes.c_int32, ctypes.c_double, _I, ctypes.c_double, ctypes.c_double, ctypes.c_double,
                                 ctypes.c_double, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_double)]),
-    "splitkv_rope": (_I, [_P, _P]),
-    "splitkv_tree_workspace_size": (_I, [_P, ctypes.POINTER(_SZ)]),
-    "splitkv_tree_attn": (_I, [_P, _P, _SZ, _P]),
-    "splitkv_tree_verify": (_I, [_P, _P]),
-    "splitkv_tree_commit": (_I, [_P, _P]),
+    "splitkv_rope": (_I, [ctypes.POINTER(RopeArgs), _P]),
+    "splitkv_tree_workspace_size": (_I, [ctypes.POINTER(TreeArgs), ctypes.POINTER(_SZ)]),
+    "splitkv_tree_attn": (_I, [ctypes.POINTER(TreeArgs), _P, _SZ, _P]),
+    "splitkv_tree_verify": (_I, [ctypes.POINTER(VerifyArgs), _P]),
+    "splitkv_tree_commit": (_I, [ctypes.POINTER(CommitArgs), _P]),
     "splitkv_read_cta_times": (_I, [_P, _I, ctypes.POINTER(ctypes.c_int64), ctypes.c_int64, _P]),
 }
 

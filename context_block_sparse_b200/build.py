@@ -5,7 +5,8 @@
 (Run it as a script: importing the package itself needs the built library.)
 
 Objects go to _build/ at the repository root; the shared library lands next
-to this file so the Python binding finds it.  Only splitkv_* symbols are
+to this file so the Python binding finds it, and beside it the torch extension
+_draft_ext.so (the bindings of the rotary and draft-tree calls).  Only splitkv_* symbols are
 exported.  Nothing here needs a GPU: nvcc cross-compiles.
 """
 
@@ -22,6 +23,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libsplitkv.so")
+EXT_SRC = os.path.join(PKG, "ext", "draft_ext.cpp")   # torch bindings of the rotary and draft-tree calls
+EXT = os.path.join(PKG, "_draft_ext.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-O3", "-I", INCLUDE, "-I", CSRC]
@@ -68,7 +71,30 @@ def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False) 
     if verbose:
         print(" ".join(link), flush=True)
     subprocess.run(link, check=True)
+    build_ext(verbose, force)
     return LIB
+
+
+def build_ext(verbose: bool = False, force: bool = False) -> str:
+    """The torch extension _draft_ext.so beside libsplitkv.so, which it links against."""
+    newest = max(os.path.getmtime(EXT_SRC), os.path.getmtime(os.path.join(INCLUDE, "splitkv.h")))
+    if not force and os.path.exists(EXT) and os.path.getmtime(EXT) >= newest:
+        return EXT
+    import sysconfig
+    import torch
+    from torch.utils import cpp_extension
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
+           "-I", sysconfig.get_paths()["include"], "-isystem", os.path.join(os.path.dirname(os.path.dirname(_nvcc())), "include")]
+    for path in cpp_extension.include_paths():
+        cmd += ["-isystem", path]
+    cmd += [EXT_SRC, "-o", EXT, "-L", PKG, "-l:libsplitkv.so", "-Wl,-rpath,$ORIGIN", "-L", lib, "-lc10", "-lc10_cuda",
+            "-ltorch_cpu", "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.run(cmd, check=True)
+    return EXT
 
 
 if __name__ == "__main__":

@@ -25,9 +25,7 @@ import numpy as np
 import torch
 
 from . import SplitKVError, _with_site
-from .draft_calls import (
-    splitkv_tree_args, splitkv_tree_attn, splitkv_tree_commit, splitkv_tree_verify, splitkv_tree_workspace_size,
-)
+from .draft_calls import splitkv_tree_attn, splitkv_tree_commit, splitkv_tree_verify
 
 
 def new_status(device=None) -> torch.Tensor:
@@ -85,16 +83,8 @@ class SplitKVTreeAttention:
             raise ValueError(f"q must be [nodes, {self.num_q_heads}, {self.head_dim}]")
         if k_cache.dim() != 4 or k_cache.shape[2] != self.num_kv_heads:
             raise ValueError(f"k_cache must be [pages, page_size, {self.num_kv_heads}, {self.head_dim}]")
-        if o is None:
-            o = q.new_empty(shape) if out_dtype is None else q.new_empty(shape, dtype=out_dtype)
-        if lse is None:
-            lse = q.new_empty((shape[0], shape[1]), dtype=torch.float32)
-        args, dev = splitkv_tree_args(q, kb, vb, node_ptr, mask, k_cache, v_cache, page_table, context_lens, scale,
-                                      self.max_nodes, o, lse, self.status)
-        # the workspace is this call's own: calls on other streams and captured graphs share nothing
-        ws = q.new_empty((splitkv_tree_workspace_size(args, dev),), dtype=torch.uint8)
-        splitkv_tree_attn(args, ws, dev)
-        return o, lse
+        return splitkv_tree_attn(q, kb, vb, node_ptr, mask, k_cache, v_cache, page_table, context_lens, scale,
+                                 self.max_nodes, out_dtype, o, lse, self.status)
 
     def check(self) -> None:
         """Raise if a call recorded an error about its device arrays (a bad page, length or node range)."""
@@ -111,13 +101,8 @@ def verify_draft(target_probs, draft_probs, tokens, parents, node_ptr, u_accept,
     u_accept float32 [nodes] and u_sample float32 [B] uniform in [0, 1).
     Returns path int32 [B, max_path] (local nodes from node 0 on, -1 behind them; max_path defaults to max_nodes,
     and the walk ends there), count int32 [B], next_token [B] (as tokens; -1 where there is none)."""
-    B = node_ptr.shape[0] - 1
-    path = node_ptr.new_empty((B, max_nodes if max_path is None else max_path))
-    count = node_ptr.new_empty((B,))
-    next_token = tokens.new_empty((B,))
-    splitkv_tree_verify(target_probs, draft_probs, tokens, parents, node_ptr, u_accept, u_sample, max_nodes, path,
-                        count, next_token, status)
-    return path, count, next_token
+    return splitkv_tree_verify(target_probs, draft_probs, tokens, parents, node_ptr, u_accept, u_sample, max_nodes,
+                               max_nodes if max_path is None else max_path, status)
 
 
 def commit_draft(k_cache, v_cache, page_table, context_lens, kb, vb, node_ptr, path=None, count=None,

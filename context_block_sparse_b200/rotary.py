@@ -63,12 +63,8 @@ class Rotary:
         dev = q.get_device()
         if dev < 0:
             raise ValueError("q must be a CUDA tensor")
-        if out is None:
-            q_out, k_out = torch.empty_like(q), None if k is None else torch.empty_like(k)
-        else:
-            q_out, k_out = out if k is not None else (out[0], None)
-        splitkv_rope(positions, self._table(dev), self.scale, q, k, q_out, k_out, self.interleaved, adjoint)
-        return q_out if k is None else (q_out, k_out)
+        q_out, k_out = (None, None) if out is None else out if k is not None else (out[0], None)
+        return splitkv_rope(positions, self._table(dev), self.scale, q, k, q_out, k_out, self.interleaved, adjoint)
 
     def forward(self, positions, q, k=None, out=None):
         """q [n, Hq, d] (and k [n, Hk, d]) at positions [n] (int32 or int64); float32, bfloat16 or float16, the
