@@ -78,6 +78,8 @@ class Case:
     ([40, 64, 1], [200, 333, 50], 4, 1, 256),               # many row tiles
     ([256, 3], [70, 640], 2, 1, 8),                         # the widest tree; pages of 8
     ([2, 2], [129, 5], 3, 1, 1),                            # pages of a single token, three heads
+    ([20, 32, 17], [130, 700, 0], 4, 1, 64),                # one full row tile, ragged
+    ([33, 64, 20], [1000, 127, 300], 16, 4, 128),           # pairs of row tiles, some with one of them empty
     ([3, 2], [129, 256], 80, 1, 16),                        # 80 heads on one: a node's rows cross the row groups
     ([130, 129, 1], [128, 0, 127], 3, 1, 32),               # two tree tiles; rows of a node across row tiles
 ])
@@ -181,7 +183,11 @@ def test_strides(splitkv):
 
 @pytest.mark.parametrize("scale", [0.0, -0.3])
 def test_scale_of_any_sign(splitkv, scale):
-    c = Case([5], [140], 4, 2, 64, 16, seed=9)
+    for nodes in (5, 60):
+        _check_scale(Case([nodes], [140], 4, 2, 64, 16, seed=9), scale)
+
+
+def _check_scale(c, scale):
     from context_block_sparse_b200.draft_tree import SplitKVTreeAttention
     tree = SplitKVTreeAttention(4, 2, 64, c.max_nodes)
     got = tree.forward(*(x.cuda() for x in (c.q, c.kb, c.vb, c.ptr, c.mask, c.k, c.v, c.table, c.lens)), scale)

@@ -53,7 +53,7 @@ class Tree(Core):
             for kind, j in order:
                 slot = c % self.stages
                 yield from self.w(f"empty{slot}", c // self.stages - 1, "empty")
-                self.load(f"full{slot}", lambda slot=slot, x=(kind, s, j): self.land(slot, x))
+                self.load(f"full{slot}", lambda a=(slot, (kind, s, j)): self.land(*a))
                 c += 1
                 yield
 
@@ -84,7 +84,7 @@ class Tree(Core):
             nonlocal c
             yield from self.w("s_free", t - 1, "s_free")
             yield from self.w(f"full{c % self.stages}", c // self.stages, "K full")
-            self.mma(lambda slot=c % self.stages: scores(s, j, t, slot))
+            self.mma(lambda a=(s, j, t, c % self.stages): scores(*a))
             self.commit(f"empty{c % self.stages}")
             self.commit("s_full")
             c += 1
@@ -102,7 +102,7 @@ class Tree(Core):
                     yield from issue_s(s, j + 1, t + 1)
                 yield from self.w(f"p_ready{t % 2}", t // 2, "p_ready")
                 yield from self.w(f"full{c % self.stages}", c // self.stages, "V full")
-                self.mma(lambda slot=c % self.stages, a=(s, j, t): second(*a, slot))
+                self.mma(lambda a=(s, j, t, c % self.stages): second(*a))
                 self.commit(f"empty{c % self.stages}")
                 self.commit(f"p_free{t % 2}")
                 self.commit("o_done")
@@ -184,6 +184,162 @@ def test_a_missing_wait_is_caught(drop):
     for seed in range(400):
         try:
             Tree(SEGS[seed % len(SEGS)], seed, 8 if drop == "seg_empty" else 5, 2, 2, drop).go()
+        except Hazard:
+            return
+    pytest.fail(f"no schedule shows the hazard that {drop} guards")
+
+
+class Rows(Core):
+    """tree_rows_sm100.cu: one or two row tiles a segment (nx), each with a softmax group of its own; K0, V0, K1, ..."""
+
+    def __init__(self, segs, seed, stages=5, drop=None):
+        names = ([f"full{i}" for i in range(stages)] + [f"empty{i}" for i in range(stages)] + ["q_full"] +
+                 [f"{n}{x}" for n in ("s_full", "p_ready", "o_full") for x in range(2)] +
+                 [f"seg_full{i}" for i in range(RING)] + [f"seg_empty{i}" for i in range(RING)])
+        super().__init__(seed, names)
+        self.B["q_full"] = Bar(2)
+        for i in range(RING):
+            self.B[f"seg_empty{i}"] = Bar(3)
+        self.segs, self.stages, self.drop = segs, stages, drop     # segs: (tiles, nx)
+        self.ring, self.info = [None] * stages, [None] * RING
+        self.Q, self.S, self.O, self.unread = [None] * 2, [None] * 2, [None] * 2, [False] * 2
+
+    w, land = Tree.w, Tree.land
+
+    def loader(self):
+        c = 0
+        for s in range(len(self.segs) + 1):
+            yield from self.w(f"seg_empty{s % RING}", s // RING - 1, "seg_empty")
+            self.info[s % RING] = s
+            self.B[f"seg_full{s % RING}"].arrive()
+            if s == len(self.segs):
+                return
+            for j in range(self.segs[s][0]):
+                for kind in "KV":
+                    slot = c % self.stages
+                    yield from self.w(f"empty{slot}", c // self.stages - 1, "empty")
+                    self.load(f"full{slot}", lambda a=(slot, (kind, s, j)): self.land(*a))
+                    c += 1
+                    yield
+
+    def products(self):
+        c, np = 0, [0, 0]
+
+        def scores(x, s, j, slot, last):
+            self.check(self.ring[slot] == ("K", s, j) and self.Q[x] == s, "K or Q")
+            self.check(self.S[x] is None, "S overwritten")
+            self.S[x] = ("S", s, j)
+            if last:
+                self.ring[slot] = None
+
+        def second(x, s, j, slot, last):
+            self.check(self.ring[slot] == ("V", s, j), "V")
+            self.check(self.S[x] == ("P", s, j), "P")
+            self.check(self.O[x] == (s, j - 1) if j else not self.unread[x], "O")
+            self.S[x], self.O[x], self.unread[x] = None, (s, j), True
+            if last:
+                self.ring[slot] = None
+
+        for s in range(len(self.segs) + 1):
+            yield from self.w(f"seg_full{s % RING}", s // RING, "seg_full")
+            self.check(self.info[s % RING] == s, "segment")
+            if s == len(self.segs):
+                return
+            tiles, nx = self.segs[s]
+            self.B[f"seg_empty{s % RING}"].arrive()
+            yield from self.w("q_full", s, "q_full")
+            full = lambda i, n: self.w(f"full{i % self.stages}", i // self.stages, n)  # noqa: E731
+            yield from full(c, "K full")
+            for x in range(nx):
+                self.mma(lambda a=(x, s, 0, c % self.stages, x == nx - 1): scores(*a))
+                self.commit(f"s_full{x}")
+            self.commit(f"empty{c % self.stages}")
+            for j in range(tiles):
+                v, k = c + 2 * j + 1, c + 2 * j + 2
+                for x in range(nx):
+                    yield from self.w(f"p_ready{x}", np[x], "p_ready")
+                    np[x] += 1
+                    if x == 0:
+                        yield from full(v, "V full")
+                    self.mma(lambda a=(x, s, j, v % self.stages, x == nx - 1): second(*a))
+                    if x == nx - 1:
+                        self.commit(f"empty{v % self.stages}")
+                    if j + 1 < tiles:
+                        if x == 0:
+                            yield from full(k, "K full")
+                        self.mma(lambda a=(x, s, j + 1, k % self.stages, x == nx - 1): scores(*a))
+                        self.commit(f"s_full{x}")
+                        if x == nx - 1:
+                            self.commit(f"empty{k % self.stages}")
+                    else:
+                        self.commit(f"o_full{x}")
+                yield
+            c += 2 * tiles
+
+    def group(self, x):
+        def open_(s):
+            yield from self.w(f"seg_full{s % RING}", s // RING, "seg_full")
+            self.check(self.info[s % RING] == s, "segment")
+
+        ns, no, ring0 = 0, 0, 0
+        yield from open_(0)
+        self.Q[x] = 0
+        self.B["q_full"].arrive()
+        for s, (tiles, nx) in enumerate(self.segs):
+            more = s + 1 < len(self.segs)
+            if x >= nx:
+                yield from open_(s + 1)
+                yield from self.w("o_full0", s, "skip")
+                if more:
+                    self.Q[x] = s + 1
+                    self.B["q_full"].arrive()
+            else:
+                for j in range(tiles):
+                    yield from self.w(f"s_full{x}", ns, "s_full")
+                    ns += 1
+                    self.check(self.S[x] == ("S", s, j), "S")
+                    if j + 1 == tiles:
+                        yield from open_(s + 1)
+                        self.Q[x] = s + 1
+                    if j:
+                        self.check(self.O[x] == (s, j - 1), "O rescaled")
+                    yield
+                    if x == 0 and self.rng.random() < 0.4:
+                        i = ring0 + 2 * j + 1
+                        yield from self.w(f"full{i % self.stages}", i // self.stages, "V zeroed")
+                        self.check(self.ring[i % self.stages] == ("V", s, j), "V zeroed")
+                    self.S[x] = ("P", s, j)
+                    self.B[f"p_ready{x}"].arrive()
+                if more:
+                    self.B["q_full"].arrive()
+                yield from self.w(f"o_full{x}", no, "o_full")
+                no += 1
+                self.check(self.O[x] == (s, tiles - 1), "O read")
+                self.unread[x] = False
+            ring0 += 2 * tiles
+            self.B[f"seg_empty{s % RING}"].arrive()
+            yield
+
+    def go(self):
+        self.run({"loader": self.loader(), "products": self.products(), "group0": self.group(0), "group1": self.group(1)})
+
+
+ROW_SEGS = [[(1, 2)], [(2, 1), (1, 2)], [(1, 1), (1, 2), (1, 1), (1, 1), (2, 2), (1, 2)], [(7, 2)],
+            [(3, 2), (1, 1), (4, 2), (1, 2), (5, 1)], [(1, 1)] * 6 + [(2, 2)] * 3]
+
+
+@pytest.mark.parametrize("stages", [4, 5, 8])
+def test_rows_protocol(stages):
+    for seed in range(80):
+        Rows(ROW_SEGS[seed % len(ROW_SEGS)], seed, stages).go()
+
+
+@pytest.mark.parametrize("drop", ["seg_empty", "empty", "K full", "V full", "p_ready", "s_full", "q_full", "o_full", "skip",
+                                  "V zeroed"])
+def test_a_missing_wait_of_the_rows_kernel_is_caught(drop):
+    for seed in range(400):
+        try:
+            Rows(ROW_SEGS[seed % len(ROW_SEGS)], seed, 8 if drop == "seg_empty" else 5, drop).go()
         except Hazard:
             return
     pytest.fail(f"no schedule shows the hazard that {drop} guards")
