@@ -8,10 +8,12 @@
 // for what a unit costs besides its tiles, and
 // CTA c of C takes the stretch [c W / C, (c + 1) W / C) of its W places: every CTA has the same
 // work to within a tile, whatever the lengths, and the lengths stay on the device (a
-// captured graph replays with new ones).  A CTA's part of a unit is one record (unnormalised
-// O, row maximum, row sum).  Walking the line, either the CTA or the unit number steps at
-// each boundary, so record (c, u) is number c + u: C + U - 1 records at most, no atomics and a
-// fixed order of the merge.
+// captured graph replays with new ones).  A unit that lies in one stretch is finished there.  Of the
+// others, at most one that begins earlier and one that ends later in a stretch, a CTA writes its part as
+// a record (unnormalised O, row maximum, row sum), number 2 c for the former and 2 c + 1 for the latter;
+// the CTA where a unit begins notes it in `split`, and the merge joins the records of at most C units, in
+// a fixed order and without atomics.  (With a record for every unit and a merge of all of them, 256
+// sequences of 4 nodes over 256 keys took 148 us, 26 of them in the merge.)
 //
 // A key of d = 64 is a 128-byte row beside its neighbouring heads', and HBM brings more than that at a
 // time (64 sequences of 8 heads over 4k read 804 MB for 537 MB of keys and values).  So at d = 64 two
@@ -44,18 +46,18 @@ struct TreeParams {
   int64_t kc_page, kc_slot, kc_head, vc_page, vc_slot, vc_head;
   int64_t mask_row, table_row;     // elements
   int B, Nq, T, Hq, Hkv, G, d;
-  int Mt, RT;                      // rows of a row tile; row tiles of max_nodes nodes
+  int Mt;                          // rows of a row tile
   int lead;                        // empty places before a unit's tiles
   int tile_shift;                  // log2 of the keys of a tile: 6 (mma.sync) or 7 (tcgen05)
   int page_shift, num_pages, max_pages;
   int hg;                          // neighbouring heads that as many CTAs walk in step: 1 or 2
   int ctas;                        // C: stretches; the context kernel has C hg CTAs
-  int recs;                        // records of one of the hg CTAs of every stretch: C + U / hg
   int o_f32;
   float scale_log2;
-  float* rec_o;                    // [hg recs][Mt][d]
-  float2* rec_ml;                  // [hg recs][Mt]: maximum (log2 units), sum
-  int2* unit_rec;                  // [U]: a unit's records [x, y)
+  float* rec_o;                    // [2 hg C][Mt][d]
+  float2* rec_ml;                  // [2 hg C][Mt]: maximum (log2 units), sum
+  int4* split;                     // [hg C]: the unit that begins in this CTA's stretch and ends in a later one:
+                                   // first node, nodes, head + (row tile << 16), the last stretch (-1: none)
 };
 
 #ifdef __CUDACC__
@@ -122,13 +124,20 @@ __device__ __forceinline__ long long block_prefix(long long mine, long long& bef
   return all;
 }
 
-// The record of this CTA's part of a unit: number c + u among the CTAs of its place e in the pairs.
-__device__ __forceinline__ size_t record(const TreeParams& p, int b, int pair, int rt) {
-  return size_t(blockIdx.x % p.hg) * p.recs + blockIdx.x / p.hg + (size_t(b) * (p.Hkv / p.hg) + pair) * p.RT + rt;
-}
-
 // First place of CTA c's stretch (c in [0, C]); C never exceeds the line's length W.
 __device__ __forceinline__ long long stretch(long long W, int c, int C) { return W * c / C; }
+
+// The CTA whose stretch holds place x - 1: the last c with c W < x C.
+__device__ __forceinline__ int cta_before(long long W, long long x, int C) {
+  long long c = (long long)(float(x) * float(C) / float(W));   // (off by one at most)
+  while (c * W >= x * C) --c;
+  while ((c + 1) * W < x * C) ++c;
+  return int(c);
+}
+
+// A finished row: what O's sums are multiplied by, and its lse.
+__device__ __forceinline__ float row_inv(float l) { return l == 0.f ? 0.f : 1.f / l; }   // no key: o = 0 (a NaN stays NaN)
+__device__ __forceinline__ float row_lse(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f; }
 
 // Infinities and NaN among the 16-bit values of x are replaced by 0; returns whether there were any.
 template <typename T>

@@ -166,6 +166,16 @@ __device__ __forceinline__ void softmax_step(Rows<NC>& st, float (&s)[kKeys / 8]
   }
 }
 
+// Four elements of a finished row of O.
+template <typename T>
+__device__ __forceinline__ void store4(const TreeParams& p, size_t at, float4 o, float inv) {
+  o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  if (p.o_f32)
+    *reinterpret_cast<float4*>(p.o + at * 4) = o;
+  else
+    *reinterpret_cast<uint2*>(p.o + at * 2) = make_uint2(pack2(o.x, o.y, T()), pack2(o.z, o.w, T()));
+}
+
 // ---------------------------------------------------------------------------- context kernel
 // A CTA's place on the line: the unit and key tile of the tile it points at.
 struct Cursor {
@@ -213,16 +223,19 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
   float* s_o = reinterpret_cast<float*>(smem + C::kStages * C::kStageElems * 2);   // [16][D]
   __shared__ long long s_scan[kThreads / 32];
   __shared__ long long s_rel;
-  __shared__ int s_seq;
+  __shared__ long long s_line[2];           // places of the line, the stretch's end
+  __shared__ int s_seq, s_ctas;
   __shared__ int s_pg[kPgRing][kTileKeys];
   __shared__ int s_part[kPgRing][2];        // a tile's first and second 32 keys: not all of them are there
   __shared__ float2 s_ml[4][16];
+  __shared__ float s_inv[64];               // a finished unit's 1 / sum by row
   __shared__ unsigned long long s_flag;     // nodes of a tree tile whose V is not all finite
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int rg = warp / C::kKG, kg = warp % C::kKG;
 
   // this CTA's stretch of the line, and the sequence it begins in
+  if (tid == 0) p.split[blockIdx.x].w = -1;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   long long mine = 0, before;
@@ -234,6 +247,11 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
   if (mine_c >= ctas) return;
   const long long x0 = stretch(W, mine_c, ctas);
   const int n_tiles = int(stretch(W, mine_c + 1, ctas) - x0);
+  if (tid == 0) {
+    s_line[0] = W;
+    s_line[1] = x0 + n_tiles;
+    s_ctas = ctas;
+  }
   if (x0 >= before && x0 < before + mine) {
     long long at = before;
     for (int b = b0; b < b1; ++b) {
@@ -274,6 +292,14 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
       if (lane == 0) s_part[t % kPgRing][warp] = part;
     }
   };
+  // with `load` at the stretch's last tile: does its unit begin here and end in a later stretch?  Then the merge finds it
+  // in `split`
+  auto note_split = [&]() {
+    const int rest = load.w.nt - load.tile - 1;
+    if (tid == kThreads - 1 && load.tile < n_tiles && rest > 0)
+      p.split[blockIdx.x] = make_int4(load.w.n0, load.w.n, (load.head * p.hg + sub) | load.rt << 16,
+                                      cta_before(s_line[0], s_line[1] + rest, s_ctas));
+  };
   constexpr int kChunks = D / 8;                    // 16-byte chunks of a key row
   constexpr int kRowsPer = kThreads / kChunks;      // rows of one pass of the CTA
   auto request = [&](int t) {
@@ -311,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
     }
     cp_async_commit();
   }
+  if (n_tiles <= C::kStages) note_split();
 
   uint32_t qf[D / 16][4];
   Rows<D> st;
@@ -325,7 +352,10 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
     cp_async_commit();
     if (t + C::kStages < n_tiles) {
       resolve(t + C::kStages);
-      if (t + C::kStages + 1 < n_tiles) load.step(p);
+      if (t + C::kStages + 1 < n_tiles)
+        load.step(p);
+      else
+        note_split();
     }
     if (fresh) {
       load_q<D>(qf, p, use.w.n0, use.w.n, use.head * p.hg + sub, use.rt * p.Mt + rg * 16);
@@ -397,14 +427,14 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
 
     const bool last = t + 1 == n_tiles || use.tile + 1 == use.w.nt;
     if (last) {
-      // the unit's part of this CTA is complete: add the key groups, write the record
-      const int unit = (use.b * p.Hkv + use.head * p.hg + sub) * p.RT + use.rt;
-      const size_t rec = record(p, use.b, use.head, use.rt);
-      const int rows = min(p.Mt, use.w.n * p.G - use.rt * p.Mt);
-      if (tid == 0) {
-        if (from_start) p.unit_rec[unit].x = int(rec);
-        if (use.tile + 1 == use.w.nt) p.unit_rec[unit].y = int(rec) + 1;
-      }
+      // the unit's part of this CTA is complete: add the key groups; write the record, or, of a whole unit, the rows
+      const int rest = use.w.nt - use.tile - 1, head = use.head * p.hg + sub, row0 = use.rt * p.Mt;
+      const int rec = from_start ? (rest > 0 ? 2 * int(blockIdx.x) + 1 : -1) : 2 * int(blockIdx.x);
+      const int rows = min(p.Mt, use.w.n * p.G - row0);
+      auto place = [&](int r) -> size_t {      // row r's (node, query head)
+        const int node = (row0 + r) / p.G;
+        return size_t(use.w.n0 + node) * p.Hq + head * p.G + row0 + r - node * p.G;
+      };
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         st.l[k] += __shfl_xor_sync(0xffffffffu, st.l[k], 1);
@@ -423,7 +453,14 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
 #pragma unroll
         for (int x = 0; x < C::kKG; ++x) l += s_ml[rg * C::kKG + x][r].y * fast_exp2(s_ml[rg * C::kKG + x][r].x - ref);
         f[k] = fast_exp2(st.m[k] - ref);
-        if (kg == 0 && (lane & 3) == 0 && rg * 16 + r < rows) p.rec_ml[rec * p.Mt + rg * 16 + r] = make_float2(m, l);
+        if (kg == 0 && (lane & 3) == 0 && rg * 16 + r < rows) {
+          if (rec >= 0)
+            p.rec_ml[size_t(rec) * p.Mt + rg * 16 + r] = make_float2(m, l);
+          else {
+            p.lse[place(rg * 16 + r)] = row_lse(m, l);
+            s_inv[rg * 16 + r] = row_inv(l);
+          }
+        }
       }
       float4 acc[D / 32];   // this thread's float4s of the [16][D] block
 #pragma unroll 1
@@ -447,7 +484,12 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
             acc[i] = make_float4(acc[i].x + x.x, acc[i].y + x.y, acc[i].z + x.z, acc[i].w + x.w);
           if (w % C::kKG == C::kKG - 1) {
             const int row = (w / C::kKG) * 16 + r;
-            if (row < rows) *reinterpret_cast<float4*>(p.rec_o + (rec * p.Mt + row) * D + c) = acc[i];
+            if (row < rows) {
+              if (rec >= 0)
+                *reinterpret_cast<float4*>(p.rec_o + (size_t(rec) * p.Mt + row) * D + c) = acc[i];
+              else
+                store4<T>(p, place(row) * D + c, acc[i], s_inv[row]);
+            }
           }
         }
         __syncthreads();
@@ -460,70 +502,59 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
 }
 
 // ------------------------------------------------------------------------------------ merge
-// One thread per four elements of a row: the row's records in CTA order, each weighted by
-// exp2(m_x - max m) (a record without keys has m = -inf, l = 0).  A stream over the records, a few
-// microseconds; launched early, it finds its row while the records are still being written.
-constexpr int kMergeThreads = 256;
+// A block per split unit and kMergeRows of its rows, a thread per four elements of a row: the row's records in
+// CTA order, each weighted by exp2(m_x - max m) (a record without keys has m = -inf, l = 0).  A stream over
+// the records, a few microseconds; launched early, it waits while the records are still being written.  (16 ragged trees of 16
+// nodes: blocks of 128 threads and 8 rows 64.2 us a call, 16 rows 66.4, 4 rows 65.0; of 256 threads 67.0, of 64 71.0.)
+constexpr int kMergeThreads = 128, kMergeRows = 8;
 
-template <typename T>
-__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeParams p, int d4_shift, int mt_shift) {
-  const unsigned idx = blockIdx.x * kMergeThreads + threadIdx.x;
-  const unsigned unit = idx >> (d4_shift + mt_shift);
-  const int c = int(idx & ((1u << d4_shift) - 1)) * 4, r = int((idx >> d4_shift) & ((1u << mt_shift) - 1));
-  const int rt = unit % p.RT, bh = unit / p.RT, head = bh % p.Hkv, b = bh / p.Hkv;
-  int row = 0, n0 = 0;
-  bool live = b < p.B;
-  if (live) {
-    bool bad = false;
-    const int n = seq_nodes(p, b, n0, bad);
-    row = rt * p.Mt + r;
-    live = row < n * p.G;
-  }
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeParams p) {
+  constexpr int kPass = kMergeThreads / (D / 4);
+  const int first = blockIdx.x, c = threadIdx.x % (D / 4) * 4;       // the CTA in whose stretch the unit begins
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (!live) return;
-  const int2 span = p.unit_rec[unit];
-  float m = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  constexpr int kBatch = 8;
+  const int4 u = p.split[first];
+  if (u.w < 0) return;
+  const int head = u.z & 0xffff, row0 = (u.z >> 16) * p.Mt, n_rec = u.w - first / p.hg + 1;
+  const int rows = min(int(blockIdx.y + 1) * kMergeRows, min(p.Mt, u.y * p.G - row0));
+  for (int r = blockIdx.y * kMergeRows + threadIdx.x / (D / 4); r < rows; r += kPass) {
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kBatch = 8;
 #pragma unroll 1
-  for (int r0 = span.x; r0 < span.y; r0 += kBatch) {
-    float2 ml[kBatch];
-    float4 y[kBatch];
-    float nm = m;
+    for (int k0 = 0; k0 < n_rec; k0 += kBatch) {
+      float2 ml[kBatch];
+      float4 y[kBatch];
+      float nm = m;
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      ml[k] = make_float2(-INFINITY, 0.f);
-      if (r0 + k < span.y) {
-        const size_t at = size_t(r0 + k) * p.Mt + r;
-        ml[k] = p.rec_ml[at];
-        y[k] = *reinterpret_cast<const float4*>(p.rec_o + (at << (d4_shift + 2)) + c);
+      for (int k = 0; k < kBatch; ++k) {
+        ml[k] = make_float2(-INFINITY, 0.f);
+        if (k0 + k < n_rec) {
+          const size_t at = size_t(k0 + k == 0 ? 2 * first + 1 : 2 * (first + (k0 + k) * p.hg)) * p.Mt + r;
+          ml[k] = p.rec_ml[at];
+          y[k] = *reinterpret_cast<const float4*>(p.rec_o + at * D + c);
+        }
       }
-    }
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) nm = fmaxf(nm, ml[k].x);
-    const float ref = nm == -INFINITY ? 0.f : nm;
-    const float f0 = fast_exp2(m - ref);
-    l *= f0;
-    o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+      for (int k = 0; k < kBatch; ++k) nm = fmaxf(nm, ml[k].x);
+      const float ref = nm == -INFINITY ? 0.f : nm;
+      const float f0 = fast_exp2(m - ref);
+      l *= f0;
+      o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (r0 + k < span.y) {
-        const float f = fast_exp2(ml[k].x - ref);
-        l += ml[k].y * f;
-        o = make_float4(o.x + y[k].x * f, o.y + y[k].y * f, o.z + y[k].z * f, o.w + y[k].w * f);
+      for (int k = 0; k < kBatch; ++k) {
+        if (k0 + k < n_rec) {
+          const float f = fast_exp2(ml[k].x - ref);
+          l += ml[k].y * f;
+          o = make_float4(o.x + y[k].x * f, o.y + y[k].y * f, o.z + y[k].z * f, o.w + y[k].w * f);
+        }
       }
+      m = nm;
     }
-    m = nm;
+    const size_t hr = size_t(u.x + (row0 + r) / p.G) * p.Hq + head * p.G + (row0 + r) % p.G;
+    store4<T>(p, hr * D + c, o, row_inv(l));
+    if (c == 0) p.lse[hr] = row_lse(m, l);
   }
-  const int node = n0 + row / p.G, h = head * p.G + row % p.G;
-  const float inv = l == 0.f ? 0.f : 1.f / l;   // no key: o = 0 (a NaN sum stays NaN)
-  o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-  const size_t hr = size_t(node) * p.Hq + h, dst = (hr << (d4_shift + 2)) + c;
-  if (p.o_f32)
-    *reinterpret_cast<float4*>(p.o + dst * 4) = o;
-  else
-    *reinterpret_cast<uint2*>(p.o + dst * 2) = make_uint2(pack2(o.x, o.y, T()), pack2(o.z, o.w, T()));
-  if (c == 0) p.lse[hr] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <typename T, int D, int RG>
@@ -541,14 +572,10 @@ cudaError_t context_rows(const TreeParams& p, cudaStream_t s) {
   return p.Mt == 16 ? context<T, D, 1>(p, s) : p.Mt == 32 ? context<T, D, 2>(p, s) : context<T, D, 4>(p, s);
 }
 
-template <typename T>
+template <typename T, int D>
 cudaError_t merge(const TreeParams& p, cudaStream_t s) {
-  int d4_shift = p.d == 128 ? 5 : 4, mt_shift = 4;
-  while ((1 << mt_shift) < p.Mt) ++mt_shift;
-  const int64_t threads = int64_t(p.B) * p.Hkv * p.RT << (d4_shift + mt_shift);
-  if (threads > 0xffffffffll - kMergeThreads) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned((threads + kMergeThreads - 1) / kMergeThreads));
+  cfg.gridDim = dim3(p.ctas * p.hg, p.Mt / kMergeRows);
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -556,7 +583,7 @@ cudaError_t merge(const TreeParams& p, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<T>, p, d4_shift, mt_shift);
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<T, D>, p);
 }
 
 }  // namespace
@@ -568,7 +595,8 @@ cudaError_t launch_tree_context_mma(const TreeParams& p, int dtype, cudaStream_t
 }
 
 cudaError_t launch_tree_merge(const TreeParams& p, int dtype, cudaStream_t s) {
-  return dtype == SPLITKV_DTYPE_BF16 ? merge<__nv_bfloat16>(p, s) : merge<__half>(p, s);
+  if (dtype == SPLITKV_DTYPE_BF16) return p.d == 128 ? merge<__nv_bfloat16, 128>(p, s) : merge<__nv_bfloat16, 64>(p, s);
+  return p.d == 128 ? merge<__half, 128>(p, s) : merge<__half, 64>(p, s);
 }
 
 }  // namespace tree
@@ -580,9 +608,8 @@ namespace {
 using splitkv::tree::TreeParams;
 
 struct TreeSizes {
-  int Mt, RT, hg, ctas, tile_shift;
-  size_t recs;
-  size_t units, ml_off, unit_off, status_off, total;
+  int Mt, hg, ctas, tile_shift;
+  size_t ml_off, split_off, status_off, total;
 };
 
 int sm_count() {
@@ -623,28 +650,30 @@ int check_sizes(const splitkv_tree_args* a, TreeSizes* z) {
     return SPLITKV_ERR_UNSUPPORTED;
   if (int64_t(a->max_pages) * a->page_size > 0x7fffffff - 128) return SPLITKV_ERR_UNSUPPORTED;
   const int rows = a->num_q_heads / a->num_kv_heads * a->max_nodes;
+  // Up to 16 rows both kernels are fit: mma.sync starts sooner and its units are cheap, tcgen05 streams faster.  The
+  // lengths are on the device, so the choice goes by the longest context the tables can name: 64 sequences of one node
+  // and 8 heads of d = 128 took (mma.sync / tcgen05) 70 / 74 us over 1k keys, 205 / 175 us over 4k; at d = 64
+  // 33 / 34 us over 512 and 148 / 95 us over 4k; one sequence over 1k 12.4 / 14.5 us.
+  const bool far = int64_t(a->max_pages) * a->page_size >= 2048;
   const char ask = asked_kernel();
-  const bool tc = maps_ok(a) && ask != 'm' && (rows > 16 || ask == 't');
+  const bool tc = maps_ok(a) && ask != 'm' && (rows > 16 || far || ask == 't');
   if (tc)
     z->Mt = rows <= 32 ? 32 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
   else
     z->Mt = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   z->tile_shift = tc ? 7 : 6;
-  z->RT = (rows + z->Mt - 1) / z->Mt;
-  z->units = size_t(a->num_seqs) * a->num_kv_heads * z->RT;
-  if (z->units * z->Mt * (a->head_dim / 4) > 0xfff00000u) return SPLITKV_ERR_UNSUPPORTED;   // the merge's threads
+  const size_t units = size_t(a->num_seqs) * a->num_kv_heads * ((rows + z->Mt - 1) / z->Mt);
   // One tcgen05 CTA to an SM (two at d = 64 and few rows), two of mma.sync, and no more than the longest line has tiles.
   z->hg = a->head_dim == 64 && a->num_kv_heads % 2 == 0 ? 2 : 1;
   const size_t round = (size_t(1) << z->tile_shift) - 1;
-  const size_t tiles = z->units / z->hg * (((size_t(a->max_pages) * a->page_size + round) >> z->tile_shift) +
+  const size_t tiles = units / z->hg * (((size_t(a->max_pages) * a->page_size + round) >> z->tile_shift) +
                                            ((size_t(a->max_nodes) + round) >> z->tile_shift));
   const size_t ctas = size_t(tc && !(a->head_dim == 64 && z->Mt <= 64) ? 1 : 2) * sm_count() / z->hg;
   z->ctas = int(tiles < ctas ? (tiles > 0 ? tiles : 1) : ctas);
-  z->recs = z->units / z->hg + z->ctas;
-  const size_t recs = z->recs * z->hg;
-  z->ml_off = splitkv::align_up(recs * z->Mt * a->head_dim * sizeof(float), 256);
-  z->unit_off = z->ml_off + splitkv::align_up(recs * z->Mt * sizeof(float2), 256);
-  z->status_off = z->unit_off + splitkv::align_up(z->units * sizeof(int2), 256);
+  const size_t ctas_all = size_t(z->ctas) * z->hg;
+  z->ml_off = splitkv::align_up(2 * ctas_all * z->Mt * a->head_dim * sizeof(float), 256);
+  z->split_off = z->ml_off + splitkv::align_up(2 * ctas_all * z->Mt * sizeof(float2), 256);
+  z->status_off = z->split_off + splitkv::align_up(ctas_all * sizeof(int4), 256);
   z->total = z->status_off + 256;
   return SPLITKV_OK;
 }
@@ -716,10 +745,9 @@ extern "C" int splitkv_tree_attn(const splitkv_tree_args* a, void* ws, size_t ws
   p.G = a->num_q_heads / a->num_kv_heads;
   p.d = a->head_dim;
   p.Mt = z.Mt;
-  p.RT = z.RT;
   p.tile_shift = z.tile_shift;
   // A unit on tcgen05 costs about as much as three tiles more than its tiles (first references, queries, record): 16 ragged
-  // trees over 1k-8k took LEADNUM.  The mma.sync kernel's units are cheap.
+  // trees over 1k-8k took 75 us with none, 68 with three.  The mma.sync kernel's units are cheap.
   p.lead = z.tile_shift == 7 ? 3 : 0;
   p.page_shift = 0;
   while ((1 << p.page_shift) < a->page_size) ++p.page_shift;
@@ -727,13 +755,12 @@ extern "C" int splitkv_tree_attn(const splitkv_tree_args* a, void* ws, size_t ws
   p.max_pages = a->max_pages;
   p.hg = z.hg;
   p.ctas = z.ctas;
-  p.recs = int(z.recs);
   p.o_f32 = a->o_dtype == SPLITKV_DTYPE_F32;
   // (a scale of 0 as a tiny one: scores stay 0 for any finite product, and a masked score can still be -inf)
   p.scale_log2 = a->scale == 0.f ? 1e-30f : a->scale * splitkv::kLog2e;
   p.rec_o = static_cast<float*>(ws);
   p.rec_ml = reinterpret_cast<float2*>(static_cast<char*>(ws) + z.ml_off);
-  p.unit_rec = reinterpret_cast<int2*>(static_cast<char*>(ws) + z.unit_off);
+  p.split = reinterpret_cast<int4*>(static_cast<char*>(ws) + z.split_off);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = z.tile_shift == 7 ? splitkv::tree::launch_tree_context_sm100(p, a->dtype, s)
                                     : splitkv::tree::launch_tree_context_mma(p, a->dtype, s);

@@ -1,22 +1,22 @@
-// The context part of draft-tree attention on tcgen05: every row of a unit (sequence, KV head,
-// row tile) against the sequence's cached keys, for row tiles of 32 to 256 rows.
+// The records of draft-tree attention on tcgen05 for row tiles of 32 to 128 rows (of 256: tree_rows_sm100.cu): every row
+// of a unit (sequence, KV head, row tile) against the sequence's cached keys and the tree's.
 //
 // A row tile's keys stream past it once, so the kernel wants HBM speed: a 128-key tile of K and V
 // (64 KB at d = 128) reaches an SM every ~2700 clocks.  A tcgen05.mma needs M = 128 (or 64) rows in
-// its A operand, and draft trees have 4 to 256 rows a KV head; so both products are transposed, with
+// its A operand, and most draft trees have 4 to 128 rows a KV head; so both products are transposed, with
 // keys and the head dimension as M and the rows as N:
 //   S^T [128 keys x N rows] = K Q^T,     O^T [d x N rows] += V^T P^T,
-// 16 instructions a tile at d = 128, of 40 / 48 / 64 / 128 clocks at N = 32 / 64 / 128 / 256 (measured).
+// 16 instructions a tile at d = 128, of 40 / 48 / 64 clocks at N = 32 / 64 / 128 (measured).
 //
-// In S^T a TMEM lane is a key, so a softmax thread holds one key's scores of 64 rows (32 at a time).
+// In S^T a TMEM lane is a key, so a softmax thread holds one key's scores of 32 rows.
 // Its row maxima would need 128 lanes' agreement at every tile; instead a row keeps a reference, the
 // maximum of its first tile, and P = exp2(s - reference) may grow up to 2^kHeadroom before the
 // reference moves (O^T and the sums are then rescaled): a tile costs one barrier vote instead of a
-// reduction.  Row sums stay in registers, one lane's share of 64 rows, and are reduced when the unit
-// ends.  A thread's 64 probabilities are one 128-byte row of P^T in the swizzled layout that the
+// reduction.  Row sums stay in registers, one lane's share of 32 rows, and are reduced when the unit
+// ends.  A thread's 32 probabilities are half a 128-byte row of P^T in the swizzled layout that the
 // second product reads as its MN-major B operand.
 //
-// The first warps are softmax groups of four, 64 rows each, which also load Q and write the
+// The first warps are softmax groups of four, 32 rows each, which also load Q and write the
 // records.  Behind them one warp loads pages by TMA (one box a page and 64 columns) into a ring of
 // tiles in the order in which the products take them: K0, K1, V0, K2, V1, ...; the last issues the
 // products, S(j + 1) before PV(j), so that scores are formed while the softmax of the tile before
@@ -46,19 +46,18 @@ template <int D, int NR>
 struct Dims {
   // Rows (TMEM columns) of a softmax group.  With one or two groups a thread keeps its scores in registers from the
   // check to the exponentials; with four it has 96 registers, and scores are read twice, 16 at a time.
-  static constexpr int kCols = NR <= 128 ? 32 : 64;
+  static constexpr int kCols = 32;
   static constexpr int kGroups = NR / kCols;
   static constexpr int kThreads = 128 * kGroups + 64;
   // Two CTAs to an SM at d = 64 and few rows (a tile is half as long there as one CTA's chain of products, softmax and
   // barriers), else one with P^T double-buffered where it fits.
   static constexpr int kPerSm = D == 64 && NR <= 64 ? 2 : 1;
-  static constexpr int kPBufs = NR <= 128 && kPerSm == 1 ? 2 : 1;
-  static constexpr bool kRoomX = NR <= 128;                  // room for the warps' maxima and row sums
+  static constexpr int kPBufs = kPerSm == 1 ? 2 : 1;
   static constexpr uint32_t kTile = uint32_t(D / 64) * kHalf;
   static constexpr uint32_t kQ = uint32_t(D / 64) * NR * 128;
   static constexpr uint32_t kP = uint32_t((NR + 63) / 64) * kHalf;
-  // barriers, shifts, factors, and the warps' row sums (at NR = 256 these take a group's own half of P^T)
-  static constexpr uint32_t kMeta = kBarBytes + NR * 8 + (kRoomX ? NR * 16 : 0);
+  // barriers, shifts, factors, and the warps' maxima and row sums
+  static constexpr uint32_t kMeta = kBarBytes + NR * 8 + NR * 16;
   static constexpr int kFit = int(((kPerSm == 2 ? 115712 : 232448) - kMeta - kQ - kPBufs * kP) / kTile);
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static_assert(kStages >= 3, "ring");
@@ -67,7 +66,7 @@ struct Dims {
   static constexpr uint32_t kOffP = kOffQ + kQ;
   static constexpr uint32_t kOffMeta = kOffP + kPBufs * kP;
   static constexpr uint32_t kSmem = kOffMeta + kMeta;
-  static constexpr uint32_t kTmem = NR * 2 < 32 ? 32 : NR * 2;
+  static constexpr uint32_t kTmem = NR * 2;
 };
 
 struct Bars : CommonBars {
@@ -84,7 +83,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
   // a row's shift: minus its reference (log2 units); -0.0: it has none yet (a reference of 0 is stored as +0.0)
   float* s_nref = reinterpret_cast<float*>(smem + Dm::kOffMeta + kBarBytes);
   float* s_f = s_nref + NR;   // factor of a moved reference
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const WaitCtx wctx{&bars->abort_flag, p.status, kWaitLimitNs};
   constexpr int kSoftWarps = 4 * Dm::kGroups;
 
@@ -131,58 +130,65 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
     load_tiles<D, Dm::kStages, true>(bars, smem, tm_k, tm_v, tm_kb, tm_vb, p, n_places, wctx);
   } else if (warp == kSoftWarps + 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t kIdS = idesc(kIsF16<T>, kKeys, NR, 0, 0), kIdO = idesc(kIsF16<T>, 128, NR, 1, 1);
-      // Operand descriptors of the first tile; a tile's or a step's offset is added to the address field (16-byte
-      // units, no carry out of it).  Building them at each instruction instead made this thread's integer code the
-      // limit: ~200 clocks an instruction, where N = 64 / 128 / 256 take 48 / 64 / 128.
-      const uint64_t dK = smem_desc_sw128(smem_u32(smem), 16, 1024), dV = smem_desc_sw128(smem_u32(smem), kHalf, 1024);
-      const uint64_t dQ = smem_desc_sw128(smem_u32(smem + Dm::kOffQ), 16, 1024);
-      const uint64_t dP = smem_desc_sw128(smem_u32(smem + Dm::kOffP), kHalf, 1024);
-      uint32_t c = 0, t = 0, seg = 0;     // ring slots, tiles, segments so far
-      bool ok = true;
-      // scores of the next tile: S^T = K Q^T once its K has landed and the scores before are read
-      auto issue_s = [&](uint32_t tile) -> bool {
-        const int slot = int(c % Dm::kStages);
-        if (tile > 0 && !mbar_wait(&bars->s_free, (tile - 1) & 1, wctx, kFile + __LINE__)) return false;
-        if (!mbar_wait(&bars->full[slot], (c / Dm::kStages) & 1, wctx, kFile + __LINE__)) return false;
-        tc_fence_after();
-        const uint64_t a = dK + (uint32_t(slot) * Dm::kTile >> 4);
+    const bool one = elect_one();
+    constexpr uint32_t kIdS = idesc(kIsF16<T>, kKeys, NR, 0, 0), kIdO = idesc(kIsF16<T>, 128, NR, 1, 1);
+    // Operand descriptors of the first tile; a tile's or a step's offset is added to the address field (16-byte
+    // units, no carry out of it).  Building them at each instruction instead made this thread's integer code the
+    // limit: ~200 clocks an instruction, where N = 32 / 64 / 128 take 40 / 48 / 64.
+    const uint64_t dK = smem_desc_sw128(smem_u32(smem), 16, 1024), dV = smem_desc_sw128(smem_u32(smem), kHalf, 1024);
+    const uint64_t dQ = smem_desc_sw128(smem_u32(smem + Dm::kOffQ), 16, 1024);
+    const uint64_t dP = smem_desc_sw128(smem_u32(smem + Dm::kOffP), kHalf, 1024);
+    uint32_t c = 0, t = 0, seg = 0;     // ring slots, tiles, segments so far
+    bool ok = true;
+    // scores of the next tile: S^T = K Q^T once its K has landed and the scores before are read
+    auto issue_s = [&](uint32_t tile) -> bool {
+      const int slot = int(c % Dm::kStages);
+      if (tile > 0 && !warp_wait(&bars->s_free, (tile - 1) & 1, wctx, kFile + __LINE__)) return false;
+      if (!warp_wait(&bars->full[slot], (c / Dm::kStages) & 1, wctx, kFile + __LINE__)) return false;
+      tc_fence_after();
+      const uint64_t a = dK + (uint32_t(slot) * Dm::kTile >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-          mma_ss(tmem, a + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4), dQ + (((kk >> 2) * (NR * 128) + (kk & 3) * 32) >> 4),
-                 kIdS, kk > 0 ? 1u : 0u);
+      for (int kk = 0; kk < D / 16; ++kk)
+        if (one)
+          mma_ss(tmem, a + (((kk >> 2) * kHalf + (kk & 3) * 32) >> 4),
+                 dQ + (((kk >> 2) * (NR * 128) + (kk & 3) * 32) >> 4), kIdS, kk > 0 ? 1u : 0u);
+      if (one) {
         mma_commit(&bars->empty[slot]);
         mma_commit(&bars->s_full);
-        ++c;
-        return true;
-      };
-      while (ok) {
-        const int at = int(seg % kSegRing);
-        if (!mbar_wait(&bars->seg_full[at], (seg / kSegRing) & 1, wctx, kFile + __LINE__)) { ok = false; break; }
-        const int tiles = bars->seg[at].tiles;
-        if (tiles == 0) break;
-        mbar_arrive(&bars->seg_empty[at]);
-        if (!mbar_wait(&bars->q_full, seg & 1, wctx, kFile + __LINE__)) { ok = false; break; }
-        ++seg;
-        if (!issue_s(t)) { ok = false; break; }
-        for (int j = 0; j < tiles; ++j, ++t) {
-          if (j + 1 < tiles && !issue_s(t + 1)) { ok = false; break; }
-          const int slot = int(c % Dm::kStages);
-          if (!mbar_wait(&bars->p_ready[t & 1], (t >> 1) & 1, wctx, kFile + __LINE__)) { ok = false; break; }
-          if (!mbar_wait(&bars->full[slot], (c / Dm::kStages) & 1, wctx, kFile + __LINE__)) { ok = false; break; }
-          tc_fence_after();
-          const uint64_t a = dV + (uint32_t(slot) * Dm::kTile >> 4);
-          const uint64_t b = dP + (Dm::kPBufs == 2 ? (t & 1) * (Dm::kP >> 4) : 0u);
+      }
+      ++c;
+      return true;
+    };
+    while (ok) {
+      const int at = int(seg % kSegRing);
+      if (!warp_wait(&bars->seg_full[at], (seg / kSegRing) & 1, wctx, kFile + __LINE__)) { ok = false; break; }
+      const int tiles = __shfl_sync(0xffffffffu, bars->seg[at].tiles, 0);
+      if (tiles == 0) break;
+      warp_arrive(&bars->seg_empty[at]);
+      if (!warp_wait(&bars->q_full, seg & 1, wctx, kFile + __LINE__)) { ok = false; break; }
+      ++seg;
+      if (!issue_s(t)) { ok = false; break; }
+      for (int j = 0; j < tiles; ++j, ++t) {
+        if (j + 1 < tiles && !issue_s(t + 1)) { ok = false; break; }
+        const int slot = int(c % Dm::kStages);
+        if (!warp_wait(&bars->p_ready[t & 1], (t >> 1) & 1, wctx, kFile + __LINE__)) { ok = false; break; }
+        if (!warp_wait(&bars->full[slot], (c / Dm::kStages) & 1, wctx, kFile + __LINE__)) { ok = false; break; }
+        tc_fence_after();
+        const uint64_t a = dV + (uint32_t(slot) * Dm::kTile >> 4);
+        const uint64_t b = dP + (Dm::kPBufs == 2 ? (t & 1) * (Dm::kP >> 4) : 0u);
 #pragma unroll
-          for (int kk = 0; kk < kKeys / 16; ++kk)
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          if (one)
             mma_ss(tmem + NR, a + (kk * 2048 >> 4), b + (kk * 2048 >> 4), kIdO, kk > 0 ? 1u : (j > 0 ? 1u : 0u));
+        if (one) {
           mma_commit(&bars->empty[slot]);
           mma_commit(&bars->p_free[t & 1]);
-          ++c;
         }
+        ++c;
       }
-      if (!ok) bars->abort_flag = 1;
+    }
+    if (!ok) bars->abort_flag = 1;
+    if (one) {
       mma_commit(&bars->mma_done);   // every product ends before tensor memory is released
       mbar_drain(&bars->mma_done, 0, wctx, kFile + __LINE__);
     }
@@ -192,21 +198,15 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
     const int g = warp >> 2, wq = warp & 3;
     const int key_lane = wq * 32 + lane;               // key of a tile = TMEM lane; head element in O^T
     const int col0 = g * Dm::kCols;                    // this group's rows
-    constexpr int kChunks = Dm::kCols / 32;
     constexpr bool kKeep = NR <= 64 && (NR == 32 || Dm::kPerSm == 1);   // scores stay in registers between the check and the exponentials
     constexpr int kW = kKeep ? Dm::kCols : 16;         // rows of one pass of exponentials
-    // Row sums of a thread: its own share of every row of the group; at NR = 256 two neighbouring lanes add theirs at
-    // every tile and each keeps half.
-    constexpr bool kPair = NR == 256;
-    constexpr int kL = kPair ? Dm::kCols / 2 : Dm::kCols;
-    const bool odd = (lane & 1) != 0;
     const uint32_t tS = tmem + (uint32_t(wq * 32) << 16) + col0, tO = tS + NR;
     // this thread's key row of P^T: 128 bytes of 64 rows, 16-byte chunks swizzled
     uint8_t* my_p = smem + Dm::kOffP + (col0 >> 6) * kHalf + key_lane * 128;
     const int pch0 = (col0 & 63) >> 3;
     float* nref = s_nref + col0;
     float* fac = s_f + col0;
-    float* s_x = s_f + NR + g * (4 * Dm::kCols);   // the warps' maxima, then their row sums (not at NR = 256)
+    float* s_x = s_f + NR + g * (4 * Dm::kCols);   // the warps' maxima, then their row sums
     const float scale = p.scale_log2;
     uint32_t t = 0, ring0 = 0;      // tiles and ring slots of the segments before
     bool ok = true;
@@ -234,15 +234,15 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
     // scale turns into -inf, so that nothing after this knows of masks.
     const float hidden = scale > 0.f ? -INFINITY : INFINITY;
     auto hide = [&](const Segment& s, bool tree, int key0, int limit, uint32_t wrong) {
-      unsigned long long bits = key_lane < limit && !((wrong >> (key_lane / box)) & 1u) ? ~0ull : 0ull;   // bit c: row col0 + c
+      uint32_t bits = key_lane < limit && !((wrong >> (key_lane / box)) & 1u) ? 0xffffffffu : 0u;   // bit c: row col0 + c
       if (tree && bits != 0 && p.mask != nullptr) {
         bits = 0;
         const int first = s.rt * NR + col0, last = min(first + Dm::kCols, s.rt * NR + s.rows);
         const uint8_t* m = p.mask + int64_t(s.n0) * p.mask_row + key0 + key_lane;
 #pragma unroll 8
         for (int i = first / p.G; i * p.G < last; ++i) {
-          const int lo = max(i * p.G - first, 0), n = min((i + 1) * p.G - first, 64) - lo;
-          const unsigned long long some = n >= 64 ? ~0ull : (1ull << n) - 1;
+          const int lo = max(i * p.G - first, 0), n = min((i + 1) * p.G - first, 32) - lo;
+          const uint32_t some = n >= 32 ? 0xffffffffu : (1u << n) - 1;
           if (m[i * p.mask_row]) bits |= some << lo;
         }
       }
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
         tmem_ld16(tS + e, v);
         tmem_wait_ld();
         reg_fence<16>(v);
-        const uint32_t see = uint32_t(bits >> e);
+        const uint32_t see = bits >> e;
 #pragma unroll
         for (int i = 0; i < 16; ++i) v[i] = see >> i & 1u ? v[i] : __float_as_uint(hidden);
         tmem_st16(tS + e, v);
@@ -280,12 +280,12 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
     while (more) {
       const Segment& s = bars->seg[seg % kSegRing];
       const int rows = min(NR, s.rows), len = s.len, tiles = s.tiles;
-      const int live = max(0, min(kChunks, (rows - col0 + 31) / 32));   // chunks of 32 with rows
-      float l[kL];
+      const bool live = rows > col0;   // this group has rows
+      float l[Dm::kCols];              // a thread's own share of its rows' sums
 #pragma unroll
-      for (int i = 0; i < kL; ++i) l[i] = 0.f;
+      for (int i = 0; i < Dm::kCols; ++i) l[i] = 0.f;
       if ((tid & 127) < Dm::kCols) nref[tid & 127] = -0.0f;
-      bool need = live > 0;       // a row has no reference yet
+      bool need = live;           // a row has no reference yet
       group_sync(g);
       const int tile0 = s.tile0, ctx = s.ctx, nodes = s.n;
       for (int j = 0; j < tiles; ++j, ++t) {
@@ -300,111 +300,85 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
         }
         const uint32_t wrong = uint32_t(bars->bad[t % kMetaRing]);
         const bool part = wrong != 0 || limit < kKeys || tree;
-        if (part && live > 0) hide(s, tree, key0, limit, wrong);
+        if (part && live) hide(s, tree, key0, limit, wrong);
         // scores in log2 units, shifted by the rows' references; is one of them past the headroom?
         float x[kW];
         float mx = -INFINITY;
-        if (!need) {
+        if (live && !need) {
 #pragma unroll
           for (int e = 0; e < Dm::kCols; e += 16) {
-            if (e < live * 32) {
-              uint32_t v[16];
-              tmem_ld16(tS + e, v);
-              tmem_wait_ld();
-              reg_fence<16>(v);
+            uint32_t v[16];
+            tmem_ld16(tS + e, v);
+            tmem_wait_ld();
+            reg_fence<16>(v);
 #pragma unroll
-              for (int i = 0; i < 16; i += 4) {
-                const float4 r = *reinterpret_cast<const float4*>(nref + e + i);
-                float y0, y1, y2, y3;
-                ffma2(y0, y1, __uint_as_float(v[i]), __uint_as_float(v[i + 1]), scale, scale, r.x, r.y);
-                ffma2(y2, y3, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]), scale, scale, r.z, r.w);
-                mx = fmax3(mx, y0, y1);
-                mx = fmax3(mx, y2, y3);
-                if constexpr (kKeep) {
-                  x[e + i] = y0;
-                  x[e + i + 1] = y1;
-                  x[e + i + 2] = y2;
-                  x[e + i + 3] = y3;
-                }
+            for (int i = 0; i < 16; i += 4) {
+              const float4 r = *reinterpret_cast<const float4*>(nref + e + i);
+              float y0, y1, y2, y3;
+              ffma2(y0, y1, __uint_as_float(v[i]), __uint_as_float(v[i + 1]), scale, scale, r.x, r.y);
+              ffma2(y2, y3, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]), scale, scale, r.z, r.w);
+              mx = fmax3(mx, y0, y1);
+              mx = fmax3(mx, y2, y3);
+              if constexpr (kKeep) {
+                x[e + i] = y0;
+                x[e + i + 1] = y1;
+                x[e + i + 2] = y2;
+                x[e + i + 3] = y3;
               }
             }
           }
         }
         bool over = need;
-        if (!need && live > 0) over = group_any(g, mx > kHeadroom);
+        if (!need && live) over = group_any(g, mx > kHeadroom);
         if (over) {
           need = false;
+          // new references of the group's rows: lane i of every warp gets column i's maximum
+          float m = -INFINITY;
+#pragma unroll
+          for (int e = 0; e < 32; e += 16) {
+            uint32_t v[16];
+            tmem_ld16(tS + e, v);
+            tmem_wait_ld();
+            reg_fence<16>(v);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float y = warp_max(__uint_as_float(v[i]) * scale);
+              m = lane == e + i ? y : m;
+            }
+          }
+          const uint32_t was = __float_as_uint(nref[lane]);
+          const float old = was == 0x80000000u ? -INFINITY : -__uint_as_float(was);
+          s_x[wq * Dm::kCols + lane] = m;
+          group_sync(g);
+#pragma unroll
+          for (int w = 0; w < 4; ++w) m = fmaxf(m, s_x[w * Dm::kCols + lane]);
+          // (the four warps hold the same values, so their votes agree)
+          const float to = old == -INFINITY ? m : (m > old + kHeadroom ? m : old);
+          const float f = old == -INFINITY ? 1.f : fast_exp2(old - to);
+          if (wq == 0) {
+            nref[lane] = to == -INFINITY ? -0.0f : 0.f - to;
+            fac[lane] = f;
+          }
+          const bool moved = __any_sync(0xffffffffu, f != 1.f);
+          need = __any_sync(0xffffffffu, to == -INFINITY) != 0;
+          group_sync(g);
+          if (moved) {
+#pragma unroll
+            for (int i = 0; i < Dm::kCols; ++i) l[i] *= fac[i];
+            if (j > 0) {
+              ok = ok && done(t - 1);
+              tc_fence_after();
 #pragma unroll 1
-          for (int ch = 0; ch < live; ++ch) {
-            float* nr = nref + ch * 32;
-            float* fc = fac + ch * 32;
-            // new references of this chunk's rows: lane i of every warp gets column i's maximum
-            float m = -INFINITY;
+              for (int e = 0; e < 32; e += 16) {
+                uint32_t o[16];
+                tmem_ld16(tO + e, o);
+                tmem_wait_ld();
+                reg_fence<16>(o);
 #pragma unroll
-            for (int e = 0; e < 32; e += 16) {
-              uint32_t v[16];
-              tmem_ld16(tS + ch * 32 + e, v);
-              tmem_wait_ld();
-              reg_fence<16>(v);
-#pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float y = warp_max(__uint_as_float(v[i]) * scale);
-                m = lane == e + i ? y : m;
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fac[e + i]);
+                tmem_st16(tO + e, o);
               }
-            }
-            const uint32_t was = __float_as_uint(nr[lane]);
-            const float old = was == 0x80000000u ? -INFINITY : -__uint_as_float(was);
-            if constexpr (Dm::kRoomX) {
-              s_x[wq * Dm::kCols + ch * 32 + lane] = m;
-              group_sync(g);
-#pragma unroll
-              for (int w = 0; w < 4; ++w) m = fmaxf(m, s_x[w * Dm::kCols + ch * 32 + lane]);
-            } else {
-              // (no room: through the factors' and shifts' slots of this chunk, two warps at a time)
-              group_sync(g);
-              if (wq == 0) fc[lane] = m;
-              if (wq == 1) nr[lane] = m;
-              group_sync(g);
-              if (wq == 2) fc[lane] = fmaxf(fc[lane], m);
-              if (wq == 3) nr[lane] = fmaxf(nr[lane], m);
-              group_sync(g);
-              m = fmaxf(fc[lane], nr[lane]);
-              group_sync(g);
-            }
-            // (the four warps hold the same values, so their votes agree)
-            const float to = old == -INFINITY ? m : (m > old + kHeadroom ? m : old);
-            const float f = old == -INFINITY ? 1.f : fast_exp2(old - to);
-            if (wq == 0) {
-              nr[lane] = to == -INFINITY ? -0.0f : 0.f - to;
-              fc[lane] = f;
-            }
-            const bool moved = __any_sync(0xffffffffu, f != 1.f);
-            need |= __any_sync(0xffffffffu, to == -INFINITY) != 0;
-            group_sync(g);
-            if (moved) {
-#pragma unroll
-              for (int c = 0; c < kChunks; ++c) {
-                if (c == ch) {
-                  constexpr int kN = kL / kChunks;
-#pragma unroll
-                  for (int i = 0; i < kN; ++i) l[c * kN + i] *= fc[kPair ? (i / 8) * 16 + (odd ? 8 : 0) + i % 8 : i];
-                }
-              }
-              if (j > 0) {
-                ok = ok && done(t - 1);
-                tc_fence_after();
-#pragma unroll 1
-                for (int e = 0; e < 32; e += 16) {
-                  uint32_t o[16];
-                  tmem_ld16(tO + ch * 32 + e, o);
-                  tmem_wait_ld();
-                  reg_fence<16>(o);
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fc[e + i]);
-                  tmem_st16(tO + ch * 32 + e, o);
-                }
-                tmem_wait_st();
-              }
+              tmem_wait_st();
             }
           }
           if constexpr (kKeep) {
@@ -419,7 +393,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
             }
           }
         }
-        if (kKeep || live == 0) {
+        if (kKeep || !live) {
           tc_fence_before();
           warp_arrive(&bars->s_free);
         }
@@ -428,15 +402,15 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
         if (t >= kB)
           ok = ok && done(t - kB);
         uint8_t* pp = my_p + (kB == 2 ? (t & 1) * Dm::kP : 0);
+        if (live) {
 #pragma unroll
-        for (int w = 0; w < Dm::kCols / kW; ++w) {
-          if (w * kW < live * 32) {
+          for (int w = 0; w < Dm::kCols / kW; ++w) {
             if constexpr (!kKeep) {
               uint32_t v[16];
               tmem_ld16(tS + w * kW, v);
               tmem_wait_ld();
               reg_fence<16>(v);
-              if ((w + 1) * kW == live * 32) {
+              if ((w + 1) * kW == Dm::kCols) {
                 tc_fence_before();
                 warp_arrive(&bars->s_free);
               }
@@ -449,17 +423,9 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
             }
 #pragma unroll
             for (int i = 0; i < kW; ++i) x[i] = fast_exp2(x[i]);
-            if constexpr (kPair) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) {
-                const float y = __shfl_xor_sync(0xffffffffu, odd ? x[i] : x[8 + i], 1);
-                l[w * 8 + i] += (odd ? x[8 + i] : x[i]) + y;
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < kW; i += 2)
-                fadd2(l[w * kW + i], l[w * kW + i + 1], l[w * kW + i], l[w * kW + i + 1], x[i], x[i + 1]);
-            }
+            for (int i = 0; i < kW; i += 2)
+              fadd2(l[w * kW + i], l[w * kW + i + 1], l[w * kW + i], l[w * kW + i + 1], x[i], x[i + 1]);
 #pragma unroll
             for (int i = 0; i < kW / 8; ++i)
               *reinterpret_cast<uint4*>(pp + (((pch0 + w * (kW / 8) + i) ^ (key_lane & 7)) << 4)) =
@@ -504,21 +470,51 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
       }
       ring0 += 2 * tiles;
       if (more) deliver_q();   // the next unit's first scores overlap this epilogue
+      const int rec = s.rec;
+      // where this thread's first row goes: the unit's rows are node-major, the G heads of a node next to each other
+      const int row0 = s.rt * NR + col0, node0 = row0 / p.G, g0 = row0 - node0 * p.G;
+      const size_t hr0 = size_t(s.n0 + node0) * p.Hq + s.head * p.G + g0;
+      // row sums: over the warp's lanes (each step leaves half the rows to a lane, at the end one), then over the four warps
+      if (live) {
+        int r = 0;       // this lane's row after the steps
+#pragma unroll
+        for (int st = 16; st > 0; st >>= 1) {
+          const bool up = (lane & st) != 0;
+#pragma unroll
+          for (int i = 0; i < st; ++i) {
+            const float send = up ? l[i] : l[i + st];
+            const float keep = up ? l[i + st] : l[i];
+            l[i] = keep + __shfl_xor_sync(0xffffffffu, send, st);
+          }
+          r += up ? st : 0;
+        }
+        s_x[wq * Dm::kCols + r] = l[0];
+        group_sync(g);
+        const int row = tid & 127;
+        if (row < Dm::kCols) {
+          const float nr = nref[row], m = __float_as_uint(nr) == 0x80000000u ? -INFINITY : -nr;
+          const float sum = s_x[row] + s_x[Dm::kCols + row] + s_x[2 * Dm::kCols + row] + s_x[3 * Dm::kCols + row];
+          // what the row's O is multiplied by, and where it goes (elements from the first row's)
+          const uint32_t at = rec >= 0 ? row : row + (g0 + row) / p.G * (p.Hq - p.G);
+          fac[row] = rec >= 0 ? 1.f : row_inv(sum);
+          reinterpret_cast<uint32_t*>(s_x)[row] = at * D;
+          if (col0 + row < rows) {
+            if (rec >= 0)
+              p.rec_ml[size_t(rec) * NR + col0 + row] = make_float2(m, sum);
+            else
+              p.lse[hr0 + at] = row_lse(m, sum);
+          }
+        }
+        group_sync(g);
+      }
       ok = ok && done(t - 1);
       tc_fence_after();
-      const size_t rec = s.rec;
-      if (tid == 0) {
-        if (tile0 == 0) p.unit_rec[s.unit].x = int(rec);
-        if (s.last) p.unit_rec[s.unit].y = int(rec) + 1;
-      }
       uint32_t odd_v = 0;      // a node whose V is not all finite
       if (tile0 + tiles > ctx)
         for (int i = 0; i < kMaxNodes / 32; ++i) odd_v |= bars->flag[seg & 1][i];
-      float* dst = p.rec_o + (rec * NR + col0) * D + key_lane;
-#pragma unroll 1
-      for (int ch = 0; ch < live; ++ch) {
+      if (live) {
         uint32_t o[32];
-        tmem_ld32(tO + ch * 32, o);
+        tmem_ld32(tO, o);
         tmem_wait_ld();
         reg_fence<32>(o);
         if (D == 128 || wq < D / 32) {
@@ -531,50 +527,35 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
               if (isfinite(y)) continue;
 #pragma unroll
               for (int i = 0; i < 32; ++i) {
-                const int node = (s.rt * NR + col0 + ch * 32 + i) / p.G;
+                const int node = (s.rt * NR + col0 + i) / p.G;
                 if (node < nodes && (p.mask == nullptr || p.mask[int64_t(s.n0 + node) * p.mask_row + j]))
                   o[i] = __float_as_uint(__uint_as_float(o[i]) + y);
               }
             }
           }
+          // eight rows at a time, none behind the last: this is one warp's serial code at the end of every unit
+          const uint32_t* off = reinterpret_cast<const uint32_t*>(s_x);
+          float* f32 = rec >= 0 ? p.rec_o + (size_t(rec) * NR + col0) * D : reinterpret_cast<float*>(p.o) + hr0 * D;
+          T* low = reinterpret_cast<T*>(p.o) + hr0 * D;
+          const bool wide = rec >= 0 || p.o_f32;
 #pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (col0 + ch * 32 + i < rows) dst[(ch * 32 + i) * D] = __uint_as_float(o[i]);
+          for (int e = 0; e < 32; e += 8) {
+            if (col0 + e < rows) {
+#pragma unroll
+              for (int i = e; i < e + 8; ++i) {
+                const float y = __uint_as_float(o[i]) * fac[i];
+                if (col0 + i < rows) {
+                  if (wide)
+                    f32[off[i] + key_lane] = y;
+                  else
+                    low[off[i] + key_lane] = T(y);
+                }
+              }
+            }
+          }
         }
       }
       tc_fence_before();
-      // row sums: over the warp's lanes (each step leaves half the rows to a lane), then over the four warps
-      if (live > 0) {
-        int r = 0;       // this lane's first sum after the steps
-#pragma unroll
-        for (int st = 16, n = kL / 2; st > (kPair ? 1 : 0); st >>= 1, n >>= 1) {
-          const bool up = (lane & st) != 0;
-#pragma unroll
-          for (int i = 0; i < n; ++i) {
-            const float send = up ? l[i] : l[i + n];
-            const float keep = up ? l[i + n] : l[i];
-            l[i] = keep + __shfl_xor_sync(0xffffffffu, send, st);
-          }
-          r += up ? n : 0;
-        }
-        float* s_l = Dm::kRoomX ? s_x
-                                     : reinterpret_cast<float*>(smem + Dm::kOffP + g * kHalf);   // read by no product now
-#pragma unroll
-        for (int i = 0; i < kChunks; ++i) {
-          const int e = r + i;
-          s_l[wq * Dm::kCols + (kPair ? (e / 8) * 16 + (odd ? 8 : 0) + e % 8 : e)] = l[i];
-        }
-        group_sync(g);
-        const int row = tid & 127;
-        if (row < Dm::kCols && col0 + row < rows)
-        {
-          const float nr = nref[row];
-          p.rec_ml[rec * NR + col0 + row] =
-              make_float2(__float_as_uint(nr) == 0x80000000u ? -INFINITY : -nr,
-                          s_l[row] + s_l[Dm::kCols + row] + s_l[2 * Dm::kCols + row] + s_l[3 * Dm::kCols + row]);
-        }
-        group_sync(g);
-      }
       warp_arrive(&bars->seg_empty[seg % kSegRing]);
       ++seg;
     }
@@ -602,8 +583,7 @@ cudaError_t rows(const TreeParams& p, const CUtensorMap* m, cudaStream_t s) {
   switch (p.Mt) {
     case 32: return launch<T, D, 32>(p, m, s);
     case 64: return launch<T, D, 64>(p, m, s);
-    case 128: return launch<T, D, 128>(p, m, s);
-    default: return launch<T, D, 256>(p, m, s);
+    default: return launch<T, D, 128>(p, m, s);
   }
 }
 

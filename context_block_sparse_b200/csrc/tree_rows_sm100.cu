@@ -1,14 +1,20 @@
-// The records of draft-tree attention on tcgen05 for row tiles of 128 or 256 rows: rows as M, one or
-// two 128-row tiles (A, B) that share every 128-key tile of K and V,
+// The records of draft-tree attention on tcgen05 for row tiles of 256 rows: rows as M, two 128-row
+// tiles (A, B) that share every 128-key tile of K and V,
 //   S_x [128 rows x 128 keys] = Q_x K^T,     O_x [128 rows x d] += P_x V.
 //
-// From 128 rows on the transposed products (tree_context_sm100.cu) are held up by shared memory and by
+// At 256 rows the transposed products (tree_context_sm100.cu) are held up by shared memory and by
 // agreeing on row statistics across lanes; here a TMEM lane is a row, so a softmax thread owns a row:
 // its maximum, its sum, its reference, no barrier and no exchange, and P goes back over S in tensor
-// memory as the second product's A operand instead of through shared memory.  A pair of tiles costs the
-// tensor core 2048 clocks a key tile at d = 128 (32 instructions of 64 clocks), the exponentials 2048
-// clocks of the MUFU units (128 x 256 at 16 a clock), HBM 2735: while one group of four warps forms its
-// tile's probabilities, the other tile's products run.
+// memory as the second product's A operand instead of through shared memory.  (4 x 64 nodes of G = 4 over 64k to 80k
+// keys: 427 us transposed, 335 here.  With one tile of 128 rows this form loses: 32 x 32 nodes over 8k 291 us, 245
+// transposed.)
+//
+// A pair of row tiles costs the tensor core 2048 clocks a key tile at d = 128 (32 instructions of 64 clocks), the
+// exponentials 2048 clocks of the MUFU units (128 x 256 at 16 a clock), HBM 2735 at 1965 MHz: while one group of four
+// warps forms its tile's probabilities, the other tile's products run.  Long calls are bound by power: 4 x 64 nodes over
+// 101k to 124k keys take 505 us, 57 % of the measured bf16 and HBM rates each, at 1 kW and 1590 MHz.  Scores in halves
+// of 64 keys, whose products overlap the other half's softmax, saved 20 % of the clocks and took 525 us: the
+// clock fell by more (N = 64 products read more of shared memory for the same work).
 //
 // As in the training kernels P = exp2(s - reference), where the reference is the row's first maximum and
 // moves only when a later one exceeds it by kHeadroom (the row's O and sum are then rescaled).  Scores of
@@ -24,8 +30,9 @@ namespace tree {
 namespace {
 
 constexpr int kFile = 7 * 10000;              // site number of this file's waits
+constexpr int kTiles = 2;                     // row tiles A and B
 
-template <int D, int kTiles>
+template <int D>
 struct Dims {
   static constexpr int kThreads = 128 * kTiles + 64;
   static constexpr uint32_t kTile = uint32_t(D / 64) * kHalf;       // 128 rows x D
@@ -35,7 +42,7 @@ struct Dims {
   static constexpr uint32_t kOffMeta = kOffQ + kTiles * kTile;
   static constexpr uint32_t kSmem = kOffMeta + kBarBytes;
   // tensor memory: S_x in 128 columns each, then O_x in D columns each
-  static constexpr uint32_t kTmem = kTiles == 2 ? 512 : 256;
+  static constexpr uint32_t kTmem = 512;
 };
 
 struct Bars : CommonBars {
@@ -43,13 +50,13 @@ struct Bars : CommonBars {
 };
 static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
 
-template <typename T, int D, int kTiles>
-__global__ void __launch_bounds__(Dims<D, kTiles>::kThreads, 1)
+template <typename T, int D>
+__global__ void __launch_bounds__(Dims<D>::kThreads, 1)
     tree_rows_sm100_kernel(SPLITKV_TREE_MAPS, const TreeParams p) {
-  using Dm = Dims<D, kTiles>;
+  using Dm = Dims<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars* bars = reinterpret_cast<Bars*>(smem + Dm::kOffMeta);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const WaitCtx wctx{&bars->abort_flag, p.status, kWaitLimitNs};
   constexpr int kSoftWarps = 4 * kTiles;
 
@@ -95,67 +102,71 @@ __global__ void __launch_bounds__(Dims<D, kTiles>::kThreads, 1)
     load_tiles<D, Dm::kStages, false>(bars, smem, tm_k, tm_v, tm_kb, tm_vb, p, n_places, wctx);
   } else if (warp == kSoftWarps + 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t kIdS = idesc(kIsF16<T>, 128, kKeys, 0, 0), kIdO = idesc(kIsF16<T>, 128, D, 0, 1);
-      const uint64_t dK = smem_desc_sw128(smem_u32(smem), 16, 1024), dV = smem_desc_sw128(smem_u32(smem), kHalf, 1024);
-      const uint64_t dQ = smem_desc_sw128(smem_u32(smem + Dm::kOffQ), 16, 1024);
-      uint32_t c = 0, seg = 0;                 // ring slots, segments so far
-      uint32_t np[2] = {0, 0};                 // tiles of each row tile so far
-      bool ok = true;
-      auto full = [&](uint32_t i) -> bool {
-        return mbar_wait(&bars->full[i % Dm::kStages], (i / Dm::kStages) & 1, wctx, kFile + __LINE__);
-      };
-      // S_x = Q_x K^T from slot i
-      auto scores = [&](int x, uint32_t i) {
-        const uint64_t a = dQ + (x * Dm::kTile >> 4), b = dK + ((i % Dm::kStages) * Dm::kTile >> 4);
+    const bool one = elect_one();
+    constexpr uint32_t kIdS = idesc(kIsF16<T>, 128, kKeys, 0, 0), kIdO = idesc(kIsF16<T>, 128, D, 0, 1);
+    const uint64_t dK = smem_desc_sw128(smem_u32(smem), 16, 1024), dV = smem_desc_sw128(smem_u32(smem), kHalf, 1024);
+    const uint64_t dQ = smem_desc_sw128(smem_u32(smem + Dm::kOffQ), 16, 1024);
+    uint32_t c = 0, seg = 0;                 // ring slots, segments so far
+    uint32_t np[2] = {0, 0};                 // tiles of each row tile so far
+    bool ok = true;
+    auto full = [&](uint32_t i) -> bool {
+      return warp_wait(&bars->full[i % Dm::kStages], (i / Dm::kStages) & 1, wctx, kFile + __LINE__);
+    };
+    // S_x = Q_x K^T from slot i
+    auto scores = [&](int x, uint32_t i) {
+      const uint64_t a = dQ + (x * Dm::kTile >> 4), b = dK + ((i % Dm::kStages) * Dm::kTile >> 4);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t at = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
-          mma_ss(tmem + x * 128, a + at, b + at, kIdS, kk > 0 ? 1u : 0u);
-        }
-        mma_commit(&bars->s_full[x]);
-      };
-      while (ok) {
-        const int at = int(seg % kSegRing);
-        if (!mbar_wait(&bars->seg_full[at], (seg / kSegRing) & 1, wctx, kFile + __LINE__)) { ok = false; break; }
-        const int tiles = bars->seg[at].tiles, nx = kTiles == 2 && bars->seg[at].rows > 128 ? 2 : 1;
-        if (tiles == 0) break;
-        mbar_arrive(&bars->seg_empty[at]);
-        if (!mbar_wait(&bars->q_full, seg & 1, wctx, kFile + __LINE__)) { ok = false; break; }
-        ++seg;
-        if (!full(c)) { ok = false; break; }
-        tc_fence_after();
-        for (int x = 0; x < nx; ++x) scores(x, c);
-        mma_commit(&bars->empty[c % Dm::kStages]);
-        // slots: K(j) at c + 2 j, V(j) at c + 2 j + 1
-        for (int j = 0; j < tiles && ok; ++j) {
-          const uint32_t v = c + 2 * j + 1, k = v + 1;
-          const bool more = j + 1 < tiles;
-          for (int x = 0; x < nx; ++x) {
-            if (!mbar_wait(&bars->p_ready[x], np[x] & 1, wctx, kFile + __LINE__)) { ok = false; break; }
-            ++np[x];
-            if (x == 0 && !full(v)) { ok = false; break; }
-            tc_fence_after();
-            const uint64_t b = dV + ((v % Dm::kStages) * Dm::kTile >> 4);
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t at = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+        if (one) mma_ss(tmem + x * 128, a + at, b + at, kIdS, kk > 0 ? 1u : 0u);
+      }
+      if (one) mma_commit(&bars->s_full[x]);
+    };
+    while (ok) {
+      const int at = int(seg % kSegRing);
+      if (!warp_wait(&bars->seg_full[at], (seg / kSegRing) & 1, wctx, kFile + __LINE__)) { ok = false; break; }
+      const int tiles = __shfl_sync(0xffffffffu, bars->seg[at].tiles, 0);
+      const int nx = __shfl_sync(0xffffffffu, bars->seg[at].rows, 0) > 128 ? 2 : 1;
+      if (tiles == 0) break;
+      warp_arrive(&bars->seg_empty[at]);
+      if (!warp_wait(&bars->q_full, seg & 1, wctx, kFile + __LINE__)) { ok = false; break; }
+      ++seg;
+      if (!full(c)) { ok = false; break; }
+      tc_fence_after();
+      for (int x = 0; x < nx; ++x) scores(x, c);
+      if (one) mma_commit(&bars->empty[c % Dm::kStages]);
+      // slots: K(j) at c + 2 j, V(j) at c + 2 j + 1
+      for (int j = 0; j < tiles && ok; ++j) {
+        const uint32_t v = c + 2 * j + 1, k = v + 1;
+        const bool more = j + 1 < tiles;
+        for (int x = 0; x < nx; ++x) {
+          if (!warp_wait(&bars->p_ready[x], np[x] & 1, wctx, kFile + __LINE__)) { ok = false; break; }
+          ++np[x];
+          if (x == 0 && !full(v)) { ok = false; break; }
+          tc_fence_after();
+          const uint64_t b = dV + ((v % Dm::kStages) * Dm::kTile >> 4);
 #pragma unroll
-            for (int kk = 0; kk < kKeys / 16; ++kk)
-              mma_ts(tmem + kO + x * D, tmem + x * 128 + kk * 8, b + (kk * 2048 >> 4), kIdO, kk > 0 ? 1u : (j > 0 ? 1u : 0u));
-            if (x == nx - 1) mma_commit(&bars->empty[v % Dm::kStages]);
-            if (more) {
-              if (x == 0) {
-                if (!full(k)) { ok = false; break; }
-                tc_fence_after();
-              }
-              scores(x, k);
-              if (x == nx - 1) mma_commit(&bars->empty[k % Dm::kStages]);
-            } else {
-              mma_commit(&bars->o_full[x]);
+          for (int kk = 0; kk < kKeys / 16; ++kk)
+            if (one)
+              mma_ts(tmem + kO + x * D, tmem + x * 128 + kk * 8, b + (kk * 2048 >> 4), kIdO,
+                     kk > 0 ? 1u : (j > 0 ? 1u : 0u));
+          if (one && x == nx - 1) mma_commit(&bars->empty[v % Dm::kStages]);
+          if (more) {
+            if (x == 0) {
+              if (!full(k)) { ok = false; break; }
+              tc_fence_after();
             }
+            scores(x, k);
+            if (one && x == nx - 1) mma_commit(&bars->empty[k % Dm::kStages]);
+          } else {
+            if (one) mma_commit(&bars->o_full[x]);
           }
         }
-        c += 2 * tiles;
       }
-      if (!ok) bars->abort_flag = 1;
+      c += 2 * tiles;
+    }
+    if (!ok) bars->abort_flag = 1;
+    if (one) {
       mma_commit(&bars->mma_done);   // every product ends before tensor memory is released
       mbar_drain(&bars->mma_done, 0, wctx, kFile + __LINE__);
     }
@@ -280,25 +291,23 @@ __global__ void __launch_bounds__(Dims<D, kTiles>::kThreads, 1)
           const bool part = wrong != 0 || limit < kKeys || tree;
           if (part) hide(s, tree, key0, limit, wrong);
           // the row's maximum in log2 units (a scale below zero turns the smallest score into it)
+          uint32_t v[128];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) tmem_ld32p(tS + q * 32, v + q * 32);
+          tmem_wait_ld();
+          reg_fence<128>(v);
           float m0 = hidden, m1 = hidden, m2 = hidden, m3 = hidden;
+          if (scale > 0.f) {
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t v[32];
-            tmem_ld32(tS + q * 32, v);
-            tmem_wait_ld();
-            reg_fence<32>(v);
-            if (scale > 0.f) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                m0 = fmax3(m0, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
-                m1 = fmax3(m1, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
-                m2 = fmax3(m2, __uint_as_float(v[i + 4]), __uint_as_float(v[i + 5]));
-                m3 = fmax3(m3, __uint_as_float(v[i + 6]), __uint_as_float(v[i + 7]));
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) m0 = fminf(m0, __uint_as_float(v[i]));
+            for (int i = 0; i < 128; i += 8) {
+              m0 = fmax3(m0, __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+              m1 = fmax3(m1, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]));
+              m2 = fmax3(m2, __uint_as_float(v[i + 4]), __uint_as_float(v[i + 5]));
+              m3 = fmax3(m3, __uint_as_float(v[i + 6]), __uint_as_float(v[i + 7]));
             }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 128; ++i) m0 = fminf(m0, __uint_as_float(v[i]));
           }
           const float m = scale > 0.f ? fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * scale : m0 * scale;
           float f = 1.f;
@@ -330,15 +339,13 @@ __global__ void __launch_bounds__(Dims<D, kTiles>::kThreads, 1)
           float s0 = 0.f, s1 = 0.f, s2 = 0.f, s3 = 0.f;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            uint32_t v[32], pk[16];
-            tmem_ld32(tS + q * 32, v);
-            tmem_wait_ld();
-            reg_fence<32>(v);
+            uint32_t pk[16];
 #pragma unroll
             for (int i = 0; i < 32; i += 4) {
               float a, b, c, d;
-              ffma2(a, b, __uint_as_float(v[i]), __uint_as_float(v[i + 1]), scale, scale, nref, nref);
-              ffma2(c, d, __uint_as_float(v[i + 2]), __uint_as_float(v[i + 3]), scale, scale, nref, nref);
+              ffma2(a, b, __uint_as_float(v[q * 32 + i]), __uint_as_float(v[q * 32 + i + 1]), scale, scale, nref, nref);
+              ffma2(c, d, __uint_as_float(v[q * 32 + i + 2]), __uint_as_float(v[q * 32 + i + 3]), scale, scale, nref,
+                    nref);
               a = fast_exp2(a);
               b = fast_exp2(b);
               c = fast_exp2(c);
@@ -388,16 +395,14 @@ __global__ void __launch_bounds__(Dims<D, kTiles>::kThreads, 1)
         ok = ok && warp_wait(&bars->o_full[x], no & 1, wctx, kFile + __LINE__);
         ++no;
         tc_fence_after();
-        const size_t rec = s.rec;
-        if (tid == 0) {
-          if (tile0 == 0) p.unit_rec[s.unit].x = int(rec);
-          if (s.last) p.unit_rec[s.unit].y = int(rec) + 1;
-        }
+        const int rec = s.rec, row0 = s.rt * p.Mt + x * 128 + r;
         uint32_t odd_v = 0;      // a node whose V is not all finite
         if (tile0 + tiles > ctx)
           for (int i = 0; i < kMaxNodes / 32; ++i) odd_v |= bars->flag[seg & 1][i];
         const bool live = x * 128 + r < s.rows;
-        float* dst = p.rec_o + (rec * p.Mt + x * 128 + r) * D;
+        const size_t at = size_t(max(rec, 0)) * p.Mt + x * 128 + r;                 // the row's place in the records
+        const size_t hr = size_t(s.n0 + row0 / p.G) * p.Hq + s.head * p.G + row0 % p.G;   // and in O
+        const float inv = row_inv(l);
 #pragma unroll 1
         for (int e = 0; e < D; e += 32) {
           uint32_t o[32];
@@ -405,7 +410,7 @@ __global__ void __launch_bounds__(Dims<D, kTiles>::kThreads, 1)
           tmem_wait_ld();
           reg_fence<32>(o);
           if (odd_v && live) {
-            const int node = (s.rt * p.Mt + x * 128 + r) / p.G;
+            const int node = row0 / p.G;
 #pragma unroll 1
             for (int j = max(0, tile0 - ctx) * kKeys; j < min(nodes, (tile0 + tiles - ctx) * kKeys); ++j) {
               if (!((bars->flag[seg & 1][j >> 5] >> (j & 31)) & 1u)) continue;
@@ -418,15 +423,32 @@ __global__ void __launch_bounds__(Dims<D, kTiles>::kThreads, 1)
               }
             }
           }
-          if (live) {
+          if (rec < 0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+          }
+          if (live && (rec >= 0 || p.o_f32)) {
+            float* dst = rec >= 0 ? p.rec_o + at * D + e : reinterpret_cast<float*>(p.o) + hr * D + e;
 #pragma unroll
             for (int i = 0; i < 32; i += 4)
-              *reinterpret_cast<uint4*>(dst + e + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+              *reinterpret_cast<uint4*>(dst + i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+          } else if (live) {
+            uint32_t w[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w[i] = pack<T>(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
+#pragma unroll
+            for (int i = 0; i < 16; i += 4)
+              *reinterpret_cast<uint4*>(p.o + (hr * D + e + 2 * i) * 2) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
           }
           __syncwarp();
         }
         tc_fence_before();
-        if (live) p.rec_ml[rec * p.Mt + x * 128 + r] = make_float2(ref, l);
+        if (live) {
+          if (rec >= 0)
+            p.rec_ml[at] = make_float2(ref, l);
+          else
+            p.lse[hr] = row_lse(ref, l);
+        }
       }
       ++na;
       ring0 += 2 * tiles;
@@ -442,26 +464,21 @@ __global__ void __launch_bounds__(Dims<D, kTiles>::kThreads, 1)
   if (warp == kSoftWarps + 1) tmem_dealloc(tmem, Dm::kTmem);
 }
 
-template <typename T, int D, int kTiles>
+template <typename T, int D>
 cudaError_t launch(const TreeParams& p, const CUtensorMap* m, cudaStream_t s) {
-  using Dm = Dims<D, kTiles>;
-  cudaError_t e = cudaFuncSetAttribute(tree_rows_sm100_kernel<T, D, kTiles>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  using Dm = Dims<D>;
+  cudaError_t e = cudaFuncSetAttribute(tree_rows_sm100_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        int(Dm::kSmem));
   if (e != cudaSuccess) return e;
-  tree_rows_sm100_kernel<T, D, kTiles><<<p.ctas * p.hg, Dm::kThreads, Dm::kSmem, s>>>(m[0], m[1], m[2], m[3], p);
+  tree_rows_sm100_kernel<T, D><<<p.ctas * p.hg, Dm::kThreads, Dm::kSmem, s>>>(m[0], m[1], m[2], m[3], p);
   return cudaGetLastError();
-}
-
-template <typename T, int D>
-cudaError_t rows(const TreeParams& p, const CUtensorMap* m, cudaStream_t s) {
-  return p.Mt == 128 ? launch<T, D, 1>(p, m, s) : launch<T, D, 2>(p, m, s);
 }
 
 }  // namespace
 
 cudaError_t launch_tree_rows_sm100(const TreeParams& p, int dtype, const CUtensorMap* m, cudaStream_t s) {
-  if (dtype == SPLITKV_DTYPE_F16) return p.d == 128 ? rows<__half, 128>(p, m, s) : rows<__half, 64>(p, m, s);
-  return p.d == 128 ? rows<__nv_bfloat16, 128>(p, m, s) : rows<__nv_bfloat16, 64>(p, m, s);
+  if (dtype == SPLITKV_DTYPE_F16) return p.d == 128 ? launch<__half, 128>(p, m, s) : launch<__half, 64>(p, m, s);
+  return p.d == 128 ? launch<__nv_bfloat16, 128>(p, m, s) : launch<__nv_bfloat16, 64>(p, m, s);
 }
 
 }  // namespace tree

@@ -47,6 +47,15 @@ __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   }
 }
 
+// One lane of a converged warp.  The warp that issues the products runs them as a whole and lets this lane act: its
+// operands then stay in uniform registers.  With one lane in a branch of its own each product takes some ten instructions
+// more, and beside eight busy softmax warps a pair of row tiles' products took 4350 clocks instead of 2260 (2050 alone).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // Barriers over one softmax group (128 threads); vote returns whether any thread's predicate holds.
 __device__ __forceinline__ void group_sync(int g) { asm volatile("bar.sync %0, 128;" ::"r"(g + 1) : "memory"); }
 __device__ __forceinline__ bool group_any(int g, bool pred) {
@@ -64,11 +73,12 @@ __device__ __forceinline__ bool group_any(int g, bool pred) {
   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,                      \
       const __grid_constant__ CUtensorMap tm_kb, const __grid_constant__ CUtensorMap tm_vb
 
-// One stretch of a unit's tiles on this CTA, as the loading warp hands it to the others.
+// A unit's tiles in this CTA's stretch, as the loading warp hands it to the others.
 struct Segment {
   int n0, n, rows, len;    // first node, nodes; rows of the row tile (past NR: a full one); context length
   int tile0, tiles, ctx;   // key tiles (tiles == 0: the end); tiles from number ctx on are the tree's
-  int rt, head, unit, rec, last;   // its number and this part's record; last: the unit ends with this segment
+  int rt, head;
+  int rec;                 // this part's record; -1: the unit is all here
 };
 constexpr int kSegRing = 4;
 
@@ -78,8 +88,8 @@ struct CommonBars {
   uint64_t seg_full[kSegRing], seg_empty[kSegRing];   // one arrival of the loading warp; of every reader
   Segment seg[kSegRing];
   long long scan[20];
-  long long rel;
-  int seq;
+  long long rel, line, stop;          // first place within sequence seq, places of the line, the stretch's end
+  int seq, ctas;
   uint32_t tmem_base;
   int abort_flag;
   int bad[kMetaRing];
@@ -89,17 +99,18 @@ struct CommonBars {
 // The segments of a CTA's stretch of the line, in order.
 struct Walk {
   long long left;   // places not yet handed out
+  int rest;         // places of the unit handed out last in later stretches
   int b, unit, at;  // the next place: `at` of unit `unit` of sequence b
   SeqWork w;
   bool bad;
-  __device__ void begin(const TreeParams& p, int seq, long long rel, long long n) {
+  __device__ void begin(const TreeParams& p, const CommonBars* c, long long n) {
     left = n;
-    b = seq;
+    b = n > 0 ? c->seq : 0;
     bad = false;
     if (n <= 0) return;
     w = seq_work(p, b, bad);
-    unit = int(rel / (p.lead + w.nt));
-    at = int(rel % (p.lead + w.nt));
+    unit = int(c->rel / (p.lead + w.nt));
+    at = int(c->rel % (p.lead + w.nt));
   }
   __device__ bool next(const TreeParams& p, Segment& s) {
     while (left > 0) {
@@ -114,7 +125,8 @@ struct Walk {
       s.rt = unit % w.rts;
       s.tile0 = max(0, at - p.lead);
       s.tiles = max(0, at + take - p.lead) - s.tile0;
-      s.last = at + take == p.lead + w.nt;
+      rest = p.lead + w.nt - at - take;
+      s.rec = s.tile0 > 0 ? 2 * int(blockIdx.x) : rest > 0 ? 2 * int(blockIdx.x) + 1 : -1;
       left -= take;
       ++unit;
       at = 0;
@@ -124,19 +136,18 @@ struct Walk {
       s.ctx = w.ctx;
       s.rows = w.n * p.G - s.rt * p.Mt;
       s.len = w.len;
-      s.unit = (b * p.Hkv + s.head) * p.RT + s.rt;
-      s.rec = int(record(p, b, pair, s.rt));
       return true;
     }
     return false;
   }
 };
 
-// Block-wide: this CTA's stretch of the line, and the sequence it begins in (bars->seq, bars->rel: valid after the next
-// block barrier).  Returns its places.
+// Block-wide: this CTA's stretch of the line, and the sequence it begins in (bars->seq, rel, line, stop, ctas: valid after the
+// next block barrier).  Returns its places.
 template <int kThreads>
 __device__ __forceinline__ long long find_stretch(const TreeParams& p, CommonBars* bars) {
   const int tid = threadIdx.x;
+  if (tid == 0) p.split[blockIdx.x].w = -1;
   const int per = (p.B + kThreads - 1) / kThreads;
   const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
   long long mine = 0, before;
@@ -146,7 +157,12 @@ __device__ __forceinline__ long long find_stretch(const TreeParams& p, CommonBar
   const long long W = block_prefix<kThreads>(mine, before, bars->scan);
   const int ctas = int(min((long long)(p.ctas), W)), c = blockIdx.x / p.hg;
   if (c >= ctas) return 0;
-  const long long x0 = stretch(W, c, ctas);
+  const long long x0 = stretch(W, c, ctas), x1 = stretch(W, c + 1, ctas);
+  if (tid == 0) {
+    bars->line = W;
+    bars->stop = x1;
+    bars->ctas = ctas;
+  }
   if (x0 >= before && x0 < before + mine) {
     long long at = before;
     for (int b = b0; b < b1; ++b) {
@@ -159,7 +175,7 @@ __device__ __forceinline__ long long find_stretch(const TreeParams& p, CommonBar
       at += t;
     }
   }
-  return stretch(W, c + 1, ctas) - x0;
+  return x1 - x0;
 }
 
 // The loading warp: hands out the segments, and brings their tiles into the ring in the order in which the products
@@ -175,7 +191,7 @@ __device__ __forceinline__ void load_tiles(CommonBars* bars, uint8_t* smem, cons
   uint32_t c = 0, kc = 0, seg = 0;
   bool ok = true;
   Walk walk;
-  walk.begin(p, n_places > 0 ? bars->seq : 0, n_places > 0 ? bars->rel : 0, n_places);
+  walk.begin(p, bars, n_places);
   const int boxes = kKeys / box;
   // lane l's page of a tile
   auto page_of = [&](const Segment& s, int j) -> int {
@@ -227,6 +243,10 @@ __device__ __forceinline__ void load_tiles(CommonBars* bars, uint8_t* smem, cons
     warp_arrive(&bars->seg_full[ring]);
     ++seg;
     if (!more) break;
+    if (lane == 0 && sg.tile0 == 0 && walk.rest > 0) {      // the merge finds the unit here
+      p.split[blockIdx.x] = make_int4(sg.n0, sg.n, sg.head | sg.rt << 16,
+                                      cta_before(bars->line, bars->stop + walk.rest, bars->ctas));
+    }
     int now = page_of(sg, 0), nxt = sg.tiles > 1 ? page_of(sg, 1) : -2;
     note(now);
     if (!load(&tm_k, &tm_kb, sg, 0, now)) { ok = false; break; }
@@ -254,7 +274,7 @@ __device__ __forceinline__ void load_tiles(CommonBars* bars, uint8_t* smem, cons
 #endif  // __CUDACC__
 
 // Row tiles of this many rows and more are rows as M (tree_rows_sm100.cu), smaller ones rows as N.
-constexpr int kRowsFrom = 128;
+constexpr int kRowsFrom = 256;
 cudaError_t launch_tree_rows_sm100(const TreeParams& p, int dtype, const CUtensorMap* m, cudaStream_t s);
 
 }  // namespace tree
