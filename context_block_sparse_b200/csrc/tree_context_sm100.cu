@@ -1,5 +1,5 @@
-// The records of draft-tree attention on tcgen05 for row tiles of 32 to 128 rows (of 256: tree_rows_sm100.cu): every row
-// of a unit (sequence, KV head, row tile) against the sequence's cached keys and the tree's.
+// Draft-tree attention on tcgen05 with rows as N, for row tiles of 32 and 64 rows, and 128 at d = 128: every row of a unit
+// (sequence, KV head, row tile) against the sequence's cached keys and the tree's.
 //
 // A row tile's keys stream past it once, so the kernel wants HBM speed: a 128-key tile of K and V
 // (64 KB at d = 128) reaches an SM every ~2700 clocks.  A tcgen05.mma needs M = 128 (or 64) rows in
@@ -583,7 +583,7 @@ cudaError_t rows(const TreeParams& p, const CUtensorMap* m, cudaStream_t s) {
   switch (p.Mt) {
     case 32: return launch<T, D, 32>(p, m, s);
     case 64: return launch<T, D, 64>(p, m, s);
-    default: return launch<T, D, 128>(p, m, s);
+    default: return launch<T, 128, 128>(p, m, s);      // (at d = 64 these are rows as M)
   }
 }
 
@@ -599,7 +599,7 @@ cudaError_t launch_tree_context_sm100(const TreeParams& p, int dtype, cudaStream
       !make_page_map_4d(&m[2], p.kb, f16, p.d, p.Hkv, p.Nq, 1, p.kb_head, p.kb_node, 0, kKeys) ||
       !make_page_map_4d(&m[3], p.vb, f16, p.d, p.Hkv, p.Nq, 1, p.vb_head, p.vb_node, 0, kKeys))
     return cudaErrorInvalidValue;
-  if (p.Mt >= kRowsFrom) return launch_tree_rows_sm100(p, dtype, m, s);
+  if (rows_as_m(p.Mt, p.d)) return launch_tree_rows_sm100(p, dtype, m, s);
   if (f16) return p.d == 128 ? rows<__half, 128>(p, m, s) : rows<__half, 64>(p, m, s);
   return p.d == 128 ? rows<__nv_bfloat16, 128>(p, m, s) : rows<__nv_bfloat16, 64>(p, m, s);
 }

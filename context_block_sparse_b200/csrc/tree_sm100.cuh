@@ -68,6 +68,18 @@ __device__ __forceinline__ bool group_any(int g, bool pred) {
       : "memory");
   return out != 0;
 }
+// The same over both groups of tree_rows_sm100.cu.
+__device__ __forceinline__ void both_sync() { asm volatile("bar.sync 3, 256;" ::: "memory"); }
+__device__ __forceinline__ bool both_any(bool pred) {
+  uint32_t out;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 3, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(out)
+      : "r"(pred ? 1u : 0u)
+      : "memory");
+  return out != 0;
+}
 // The parameters of both kernels: tensor maps of the cache's and the nodes' keys and values.
 #define SPLITKV_TREE_MAPS                                                                                  \
   const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,                      \
@@ -273,8 +285,6 @@ __device__ __forceinline__ void load_tiles(CommonBars* bars, uint8_t* smem, cons
 
 #endif  // __CUDACC__
 
-// Row tiles of this many rows and more are rows as M (tree_rows_sm100.cu), smaller ones rows as N.
-constexpr int kRowsFrom = 256;
 cudaError_t launch_tree_rows_sm100(const TreeParams& p, int dtype, const CUtensorMap* m, cudaStream_t s);
 
 }  // namespace tree

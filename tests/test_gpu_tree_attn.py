@@ -82,6 +82,8 @@ class Case:
     ([33, 64, 20], [1000, 127, 300], 16, 4, 128),           # pairs of row tiles, some with one of them empty
     ([3, 2], [129, 256], 80, 1, 16),                        # 80 heads on one: a node's rows cross the row groups
     ([130, 129, 1], [128, 0, 127], 3, 1, 32),               # two tree tiles; rows of a node across row tiles
+    ([32, 30, 5], [1000, 257, 130], 8, 2, 64),              # row tiles of 128 rows, odd and even numbers of key tiles
+    ([128, 100], [0, 600], 2, 2, 16),                       # 128 nodes
 ])
 def test_matches_64_bits(splitkv, counts, lens, hq, hkv, page, dt, d):
     c = Case(counts, lens, hq, hkv, d, page, dt, seed=len(counts) + page)
@@ -103,6 +105,18 @@ def test_many_sequences(splitkv, B):
     lens = (rng.integers(0, 90, B) * (rng.random(B) < 0.7)).tolist()
     c = Case(counts, lens, 4, 2, 64, 16, seed=B, width=4)
     c.check(c.call())
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nodes", [1, 4, 12, 30, 60])
+@pytest.mark.parametrize("out", [None, torch.float32])
+def test_more_units_than_ctas(splitkv, nodes, d, out):
+    """Units that lie in one CTA's stretch, of one key tile and of several, beside such as are cut."""
+    rng = np.random.default_rng(nodes)
+    counts = np.minimum(nodes, rng.integers(nodes // 2, nodes + 1, 48).clip(1)).tolist()
+    lens = rng.integers(0, 700, 48).tolist()
+    c = Case(counts, lens, 32, 8, d, 64, seed=nodes, width=nodes)
+    c.check(c.call(out_dtype=out), out)
 
 
 def test_long_context_and_wide_rows(splitkv):
@@ -134,10 +148,11 @@ def test_rows_that_see_nothing_and_lowest_scores(splitkv):
 
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
 @pytest.mark.parametrize("d", [64, 128])
-def test_unseen_values_stay_away(splitkv, value, d):
+@pytest.mark.parametrize("heads", [(8, 4), (4, 4)])
+def test_unseen_values_stay_away(splitkv, value, d, heads):
     """Infinities and NaN in nodes that a row does not see, in cache slots behind the context, in pages of nobody:
     only the rows that see them meet them."""
-    c = Case([12, 70], [35, 100], 8, 4, d, 16, seed=6)       # the cache's unused slots are NaN already
+    c = Case([12, 70], [35, 100], *heads, d, 16, seed=6)     # the cache's unused slots are NaN already
     c.mask[0, 0], c.mask[12, 0] = True, True
     dark = [3, 12 + 40, 12 + 66]                             # nodes that only themselves see
     for r in dark:

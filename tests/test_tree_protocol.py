@@ -324,6 +324,143 @@ class Rows(Core):
         self.run({"loader": self.loader(), "products": self.products(), "group0": self.group(0), "group1": self.group(1)})
 
 
+class Split(Core):
+    """tree_rows_sm100.cu with one row tile: two softmax groups take key tiles in turn, each with scores and an O of its
+    own; both join the Os when the segment ends.  K0, K1, V0, K2, V1, ..."""
+
+    def __init__(self, segs, seed, stages=6, drop=None):
+        names = ([f"full{i}" for i in range(stages)] + [f"empty{i}" for i in range(stages)] + ["q_full", "joined", "left"] +
+                 [f"{n}{x}" for n in ("s_full", "p_ready", "o_full") for x in range(2)] +
+                 [f"seg_full{i}" for i in range(RING)] + [f"seg_empty{i}" for i in range(RING)])
+        super().__init__(seed, names)
+        self.B["joined"] = Bar(2)      # the groups' named barrier, its two uses a segment
+        self.B["left"] = Bar(2)
+        for i in range(RING):
+            self.B[f"seg_empty{i}"] = Bar(3)
+        self.segs, self.stages, self.drop = segs, stages, drop     # segs: tiles
+        self.ring, self.info = [None] * stages, [None] * RING
+        self.Q, self.S, self.O, self.readers = None, [None] * 2, [None] * 2, [0, 0]
+
+    w, land, loader = Tree.w, Tree.land, Tree.loader
+
+    def products(self):
+        c, np = 0, [0, 0]
+
+        def scores(x, s, j, slot):
+            self.check(self.ring[slot] == ("K", s, j) and self.Q == s, "K or Q")
+            self.check(self.S[x] is None, "S overwritten")
+            self.S[x], self.ring[slot] = ("S", s, j), None
+
+        def second(x, s, j, slot):
+            self.check(self.ring[slot] == ("V", s, j), "V")
+            self.check(self.S[x] == ("P", s, j), "P")
+            self.check(self.O[x] == (s, j - 2) if j > 1 else not self.readers[x], "O")
+            self.S[x], self.O[x], self.readers[x], self.ring[slot] = None, (s, j), 2, None
+
+        def next_(f, x, s, j, name):
+            slot = c % self.stages
+            yield from self.w(f"full{slot}", c // self.stages, name)
+            self.mma(lambda: f(x, s, j, slot))
+
+        for s in range(len(self.segs) + 1):
+            yield from self.w(f"seg_full{s % RING}", s // RING, "seg_full")
+            self.check(self.info[s % RING] == s, "segment")
+            if s == len(self.segs):
+                return
+            tiles = self.segs[s]
+            self.B[f"seg_empty{s % RING}"].arrive()
+            yield from self.w("q_full", s, "q_full")
+            for j in range(min(tiles, 2)):
+                yield from next_(scores, j, s, j, "K full")
+                self.commit(f"s_full{j}")
+                self.commit(f"empty{c % self.stages}")
+                c += 1
+            for j in range(tiles):
+                x = j % 2
+                yield from self.w(f"p_ready{x}", np[x], "p_ready")
+                np[x] += 1
+                yield from next_(second, x, s, j, "V full")
+                self.commit(f"empty{c % self.stages}")
+                c += 1
+                if j + 2 < tiles:
+                    yield from next_(scores, x, s, j + 2, "K full")
+                    self.commit(f"s_full{x}")
+                    self.commit(f"empty{c % self.stages}")
+                    c += 1
+                else:
+                    self.commit(f"o_full{x}")
+                yield
+
+    def group(self, x):
+        def open_(s):
+            yield from self.w(f"seg_full{s % RING}", s // RING, "seg_full")
+            self.check(self.info[s % RING] == s, "segment")
+
+        ns, no, ring0 = 0, 0, 0
+        yield from open_(0)
+        if x == 0:
+            self.Q = 0
+            self.B["q_full"].arrive()
+        for s, tiles in enumerate(self.segs):
+            more, mine = s + 1 < len(self.segs), (tiles - 1) % 2 == x or self.drop == "early Q"
+            for j in range(x, tiles, 2):
+                yield from self.w(f"s_full{x}", ns, "s_full")
+                ns += 1
+                self.check(self.S[x] == ("S", s, j), "S")
+                if j + 1 == tiles or (self.drop == "early Q" and j + 2 == tiles):
+                    yield from open_(s + 1)
+                    self.Q = s + 1
+                if j > 1:
+                    self.check(self.O[x] == (s, j - 2), "O rescaled")
+                yield
+                if self.rng.random() < 0.4:
+                    i = ring0 + 2 * j + (2 if j + 1 < tiles else 1)
+                    yield from self.w(f"full{i % self.stages}", i // self.stages, "V zeroed")
+                    self.check(self.ring[i % self.stages] == ("V", s, j), "V zeroed")
+                self.S[x] = ("P", s, j)
+                self.B[f"p_ready{x}"].arrive()
+            if (tiles - 1) % 2 != x:
+                yield from open_(s + 1)
+            elif more:
+                self.B["q_full"].arrive()
+            if x < tiles:
+                yield from self.w(f"o_full{x}", no, "o_full")
+                no += 1
+            self.B["joined"].arrive()
+            yield from self.w("joined", s, "joined")
+            for y in range(min(tiles, 2)):
+                self.check(self.O[y] == (s, tiles - 1 - (tiles - 1 - y) % 2), "O read")
+                yield
+                self.readers[y] -= 1
+            ring0 += 2 * tiles
+            self.B[f"seg_empty{s % RING}"].arrive()
+            self.B["left"].arrive()
+            yield from self.w("left", s, "left")
+
+    def go(self):
+        self.run({"loader": self.loader(), "products": self.products(), "group0": self.group(0), "group1": self.group(1)})
+
+
+SPLIT_SEGS = [[1], [2, 1], [1, 1, 1, 1, 2, 1], [7], [3, 1, 4, 1, 5], [1] * 6 + [2] * 3, [6, 5]]
+
+
+@pytest.mark.parametrize("stages", [5, 6, 8])
+def test_split_protocol(stages):
+    for seed in range(80):
+        Split(SPLIT_SEGS[seed % len(SPLIT_SEGS)], seed, stages).go()
+
+
+@pytest.mark.parametrize("drop", ["seg_empty", "empty", "K full", "V full", "p_ready", "s_full", "q_full", "o_full", "joined",
+                                  "left", "early Q", "V zeroed"])
+def test_a_missing_wait_of_the_split_form_is_caught(drop):
+    for seed in range(400):
+        try:
+            Split(SPLIT_SEGS[seed % len(SPLIT_SEGS)], seed, 8 if drop == "seg_empty" else 5, drop).go()
+        except Hazard:
+            return
+    pytest.fail(f"no schedule shows the hazard that {drop} guards")
+
+
 ROW_SEGS = [[(1, 2)], [(2, 1), (1, 2)], [(1, 1), (1, 2), (1, 1), (1, 1), (2, 2), (1, 2)], [(7, 2)],
             [(3, 2), (1, 1), (4, 2), (1, 2), (5, 1)], [(1, 1)] * 6 + [(2, 2)] * 3]
 
