@@ -55,13 +55,19 @@ class SplitKVAttention:
         if rotary is not None:
             if rotary.head_dim != head_dim:
                 raise ValueError(f"rotary is for heads of {rotary.head_dim}, not {head_dim}")
-            lens, anc = np.asarray(sample_lens, dtype=np.int64), np.asarray(anchors, dtype=np.int64)
-            starts = np.concatenate([[0], np.cumsum(lens)])
-            ctx = np.arange(starts[-1]) - np.repeat(starts[:-1], lens)
-            rows = (anc - starts[np.searchsorted(starts, anc, side="right") - 1])[:, None] + np.arange(block_size)
-            self._ctx_pos, self._row_pos = (torch.from_numpy(x.astype(np.int32).ravel()).to(self.device)
-                                            for x in (ctx, rows))
+            self._place()
         self._grad32 = None   # float32 gradients behind bf16 ones (grad_dtype=torch.bfloat16)
+
+    def _place(self):
+        """The plan's positions on the device."""
+        p = self.plan.problem
+        lens, anc = (np.asarray(x, dtype=np.int64) for x in self.plan._keep)
+        starts = np.concatenate([[0], np.cumsum(lens)])
+        ctx = np.arange(starts[-1]) - np.repeat(starts[:-1], lens)
+        rows = (anc - starts[np.searchsorted(starts, anc, side="right") - 1])[:, None] + np.arange(p.block_size)
+        self._ctx_pos, self._row_pos = (torch.from_numpy(x.astype(np.int32).ravel()).to(self.device)
+                                        for x in (ctx, rows))
+        self._placed = p
 
     def ws_bwd(self) -> torch.Tensor:
         if self._ws_bwd is None:
@@ -73,6 +79,8 @@ class SplitKVAttention:
         """q, k, kb as the attention takes them (the rotated ones are this call's own)."""
         if self.rotary is None:
             return q, k, kb
+        if self._placed is not self.plan.problem:   # splitkv_plan_update: new positions (not inside a capture)
+            self._place()
         if kb is None:
             q = self.rotary.forward(self._row_pos, q)
         else:

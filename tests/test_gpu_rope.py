@@ -180,6 +180,23 @@ def test_attention_with_rotary(splitkv, rb):
     assert_close("dv", g["dv"].double().cpu().numpy(), rg["dv"], TOL_OUT)
 
 
+def test_attention_with_rotary_after_a_plan_update(splitkv):
+    """The positions are those of the plan as it is, not as it was made."""
+    from context_block_sparse_b200.rotary import Rotary
+    from context_block_sparse_b200.torch_api import SplitKVAttention
+    rot, made = Rotary(64, base=500.0), [([30, 130], [35, 20, 140]), ([100, 60], [10, 70, 120])]   # (the larger first)
+    g = torch.Generator().manual_seed(5)
+    t = [torch.randn(*s, generator=g).bfloat16().cuda() for s in
+         ((48, 4, 64), (160, 2, 64), (160, 2, 64), (48, 2, 64), (48, 2, 64))]
+    att = SplitKVAttention(*made[0], 16, 4, 2, 64, 64, num_workers=148, rotary=rot)
+    att.forward(*t, 0.125)
+    splitkv.splitkv_plan_update(att.plan, *made[1])
+    splitkv.splitkv_plan_upload(att.plan)
+    got = att.forward(*t, 0.125)
+    want = SplitKVAttention(*made[1], 16, 4, 2, 64, 64, num_workers=148, rotary=rot).forward(*t, 0.125)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_attention_refuses_another_head_size(splitkv):
     from context_block_sparse_b200.rotary import Rotary
     from context_block_sparse_b200.torch_api import SplitKVAttention
