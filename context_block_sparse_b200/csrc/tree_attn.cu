@@ -1,6 +1,6 @@
-// Attention of draft trees over a paged cache: the records of every row against its sequence's
-// cached keys and its own tree, split over the CTAs (here on mma.sync, for few rows; on tcgen05 in
-// tree_context_sm100.cu), and the merge of a row's records.
+// Attention of draft trees over a paged cache: every row against its sequence's cached keys and its own
+// tree, the work cut over the CTAs (here on mma.sync, for few rows and short contexts; on tcgen05 in
+// tree_context_sm100.cu and tree_rows_sm100.cu), and the merge of the rows that were cut.
 //
 // Per row (node i, query head h) of sequence b, over the keys j of its context [0, len_b) and
 // the nodes j of its own tree that mask lets i see, with KV head h / G:
@@ -705,9 +705,12 @@ extern "C" int splitkv_tree_attn(const splitkv_tree_args* a, void* ws, size_t ws
       !a->node_ptr || !a->context_lens || !splitkv::ptr_aligned(a->lse, 4))
     return SPLITKV_ERR_INVALID_ARG;
   if (a->mask && a->mask_stride < 0) return SPLITKV_ERR_INVALID_ARG;
+  // (the page table is read even where the cache has no page: every entry is then a bad one)
+  if (a->max_pages > 0 && (!a->page_table || !splitkv::ptr_aligned(a->page_table, 4) || a->table_stride < 0))
+    return SPLITKV_ERR_INVALID_ARG;
   if (a->max_pages > 0 && a->num_pages > 0 &&
       (!rows_ok(a->k_cache, a->k_stride[0], a->k_stride[1], a->k_stride[2]) ||
-       !rows_ok(a->v_cache, a->v_stride[0], a->v_stride[1], a->v_stride[2]) || !a->page_table || a->table_stride < 0))
+       !rows_ok(a->v_cache, a->v_stride[0], a->v_stride[1], a->v_stride[2])))
     return SPLITKV_ERR_INVALID_ARG;
   if (ws_bytes < z.total) return SPLITKV_ERR_WORKSPACE_TOO_SMALL;
   TreeParams p;

@@ -15,16 +15,22 @@
 // with R_1 + ... + R_i > u' sum R (R = p where the residual has no mass), so the accepted
 // tokens and it are distributed as the target's own samples.
 //
-// The outputs are whole numbers decided at borders, so sums and comparisons are float64 of
-// the given values, in a fixed order.
+// The outputs are whole numbers decided at borders, so a warp's sums are pairs of float32 (an exact
+// two-sum and its carried error, some 48 bits), what joins them and every comparison is float64, all in a
+// fixed order.  (A conversion and a float64 addition an entry bound the first kernel: 64 chains over 131072
+// entries took 67 us, now 24.)
 //
 // HBM-bound for large batches: the two rows of the node where the walk ends, 2 V elements a
 // sequence; otherwise latency.  One cluster of CTAs takes a sequence: each prefetches all
 // children's p(x), q(x) at once (one round of gathers instead of one a level), walks in
 // shared memory, and sums its slice of the vocabulary; slice sums are exchanged through
 // distributed shared memory and read in rank order, so every CTA takes the same decisions.
-// Each warp keeps the sums of its 1024-element chunks: the search for the next token
+// Each warp keeps the sums of its chunks of 512 entries: the search for the next token
 // re-reads one chunk (from L2).
+//
+// Measured: one chain of 16 nodes over 32000 entries 8.6 us; 64 chains over 131072 24 us, 10 of
+// them HBM's; 24 trees of 40 nodes over 50001 (rows that do not begin on 16 bytes) 25 us.  The rest is the
+// walk's serial steps: the gathers, one pass over the rows a rejection or an end, cluster barriers.
 #include <cooperative_groups.h>
 #include <cstdint>
 
@@ -392,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 3) tree_verify_kernel(const VerifyPa
     const double all = S;
     // the first entry whose running sum exceeds the goal; below the total, so one exists
     double goal = double(p.u_sample[b]) * all;
-    goal = fmin(goal, all * (1.0 - 1.2e-16));
+    goal = fmin(fmax(goal, 0.0), all * (1.0 - 1.2e-16));
     const double mine = s_total[(pass - 1) & 1];
     // the CTA in whose slice the goal lies: the slices' sums partition [0, all)
     const bool here = all > 0.0 && mine > 0.0 && before <= goal && goal < before + mine;
@@ -511,7 +517,8 @@ extern "C" int splitkv_tree_verify(const splitkv_verify_args* a, void* stream) {
   if (!a->node_ptr || !a->path || !a->count || !a->next || !a->u_sample) return SPLITKV_ERR_INVALID_ARG;
   if (a->num_nodes > 0 && (!a->target || !a->tokens || !a->parents || !a->u_accept)) return SPLITKV_ERR_INVALID_ARG;
   if (!splitkv::ptr_aligned(a->target, es) || !splitkv::ptr_aligned(a->draft, es) || a->target_stride < 0 ||
-      a->draft_stride < 0 || a->target_stride > (int64_t(1) << 40) || a->draft_stride > (int64_t(1) << 40))
+      a->draft_stride < 0 || a->target_stride > (int64_t(1) << 40) || a->draft_stride > (int64_t(1) << 40) ||
+      (a->num_seqs > 1 && a->path_stride < a->max_path) || a->path_stride > (int64_t(1) << 40))
     return SPLITKV_ERR_INVALID_ARG;
   VerifyParams p;
   p.target = a->target;

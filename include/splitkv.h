@@ -634,7 +634,7 @@ typedef struct splitkv_verify_args {
                                      NULL: children were proposed with certainty                    */
   const void*    tokens;          /* [num_nodes]                                                   */
   const int32_t  *parents, *node_ptr;   /* [num_nodes] local, smaller than the node; [B + 1]         */
-  const float    *u_accept, *u_sample;  /* [num_nodes], [B]: uniform in [0, 1)                       */
+  const float    *u_accept, *u_sample;  /* [num_nodes], [B]: uniform in [0, 1); u_sample is clamped to it */
   int32_t        *path, *count;   /* [B][max_path] local nodes, -1 behind them; [B]                 */
   void*          next;            /* [B]                                                           */
   int32_t*       status;
@@ -648,8 +648,8 @@ typedef struct splitkv_verify_args {
  * S_{k+1} = S_k - p(x_k)).  Where no child is accepted (or max_path nodes are), the next token is the
  * first i with R_1 + ... + R_i > u_sample sum R; R = p where the residual has no mass.  path lists the
  * accepted nodes from node 0 on, count how many.  With u_* uniform, the accepted tokens and the next
- * one are distributed as the target's own samples.  Sums and comparisons are float64; entries that are
- * negative, infinite or NaN have no mass; rows are taken as normalised.  next is -1 for a sequence
+ * one are distributed as the target's own samples.  Sums hold some 48 bits and comparisons are float64;
+ * entries that are negative, infinite or NaN have no mass; rows are taken as normalised.  next is -1 for a sequence
  * without nodes or whose row has no mass.  A node whose parent is not an earlier node, or whose token
  * is outside the vocabulary, is never reached, and INVALID_ARG is recorded.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */

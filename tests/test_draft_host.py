@@ -98,7 +98,7 @@ def _tree(abi, **kw):
     (dict(q=4098), BAD), (dict(lse=None), BAD), (dict(o=None), BAD), (dict(k_cache=None), BAD),
     (dict(page_table=None), BAD), (dict(context_lens=None), BAD), (dict(node_ptr=None), BAD),
     (dict(q_stride=_pair(1020, 128)), BAD), (dict(q_stride=_pair(1024, -128)), BAD),
-    (dict(max_pages=0x7fffffff), UNSUP)])
+    (dict(max_pages=0x7fffffff), UNSUP), (dict(page_table=None, num_pages=0), BAD), (dict(page_table=4098), BAD)])
 def test_tree_attn_refuses(splitkv, kw, code):
     lib, a = splitkv._lib, _tree(splitkv._abi, **kw)
     assert lib.splitkv_tree_attn(ctypes.byref(a), 4096, 1 << 40, None) == code
@@ -128,7 +128,7 @@ def _verify(abi, **kw):
     (dict(vocab=0), BAD), (dict(vocab=(1 << 21) + 1), UNSUP), (dict(max_nodes=1025), UNSUP), (dict(max_nodes=0), BAD),
     (dict(max_path=0), BAD), (dict(dtype=9), BAD), (dict(target=None), BAD), (dict(target=4098), BAD),
     (dict(draft=4097), BAD), (dict(u_sample=None), BAD), (dict(path=None), BAD), (dict(target_stride=-1), BAD),
-    (dict(tokens=None), BAD), (dict(num_seqs=-1), BAD)])
+    (dict(tokens=None), BAD), (dict(num_seqs=-1), BAD), (dict(path_stride=3), BAD), (dict(path_stride=-4), BAD)])
 def test_verify_refuses(splitkv, kw, code):
     assert splitkv._lib.splitkv_tree_verify(ctypes.byref(_verify(splitkv._abi, **kw)), None) == code
     assert splitkv._lib.splitkv_tree_verify(ctypes.byref(_verify(splitkv._abi, num_seqs=0)), None) == 0

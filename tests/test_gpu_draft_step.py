@@ -116,6 +116,15 @@ def test_verify_edges(splitkv):
     _same(_verify(odd, 3), odd, 3)
 
 
+@pytest.mark.parametrize("u,token", [(-0.5, 1), (float("nan"), 1), (float("-inf"), 1), (1.0, 3), (2.5, 3), (float("inf"), 3)])
+def test_verify_numbers_outside_the_unit_interval(splitkv, u, token):
+    """A next token is the first or the last one with mass, never left unwritten."""
+    a = dict(target=torch.tensor([[0.0, 0.25, 0.5, 0.25, 0.0]]), draft=None, tokens=torch.zeros(1).int(),
+             parents=torch.tensor([-1]).int(), node_ptr=torch.tensor([0, 1]).int(), u_accept=torch.zeros(1),
+             u_sample=torch.tensor([u]))
+    assert _verify(a, 1)[2].item() == token
+
+
 def test_verify_bad_nodes_are_recorded(splitkv):
     from context_block_sparse_b200.draft_tree import check_status, new_status
     status = new_status()
