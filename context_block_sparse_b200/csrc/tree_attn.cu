@@ -176,6 +176,27 @@ __device__ __forceinline__ void store4(const TreeParams& p, size_t at, float4 o,
     *reinterpret_cast<uint2*>(p.o + at * 2) = make_uint2(pack2(o.x, o.y, T()), pack2(o.z, o.w, T()));
 }
 
+// Sixteen rows of a whole unit from the context kernel: each thread's float4s of the sums in s_o, the rows' statistics of
+// the kKG warps in s_ml; row0: the first row's number in the unit, whose first node's first head is hr0.  Kept out of the
+// kernel's straight code, which a call of one tile a CTA runs once, on a cold instruction cache (one token over 1k keys: 9.5 us,
+// 11.3 in line).
+template <typename T, int D, int kKG>
+__device__ __noinline__ void finish_rows(const TreeParams& p, const float* s_o, const float2 (*s_ml)[16], size_t hr0,
+                                         int row0, int rows) {
+#pragma unroll 1
+  for (int i = 0; i < D / 32; ++i) {
+    const int e = (i * kThreads + threadIdx.x) * 4, r = e / D, c = e % D, row = row0 + r;
+    if (row >= rows) break;
+    float m = -INFINITY, l = 0.f;
+    for (int x = 0; x < kKG; ++x) m = fmaxf(m, s_ml[x][r].x);
+    for (int x = 0; x < kKG; ++x) l += s_ml[x][r].y * fast_exp2(s_ml[x][r].x - (m == -INFINITY ? 0.f : m));
+    const int node = row / p.G;
+    const size_t hr = hr0 + size_t(node) * p.Hq + (row - node * p.G);
+    store4<T>(p, hr * D + c, *reinterpret_cast<const float4*>(s_o + r * D + (c ^ ((r & 3) << 3))), row_inv(l));
+    if (c == 0) p.lse[hr] = row_lse(m, l);
+  }
+}
+
 // ---------------------------------------------------------------------------- context kernel
 // A CTA's place on the line: the unit and key tile of the tile it points at.
 struct Cursor {
@@ -216,7 +237,7 @@ struct Cfg {
 };
 
 template <typename T, int D, int RG>
-__global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const TreeParams p) {
+__global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const __grid_constant__ TreeParams p) {
   using C = Cfg<D, RG>;
   extern __shared__ __align__(1024) uint8_t smem[];
   T* stages = reinterpret_cast<T*>(smem);
@@ -228,7 +249,6 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
   __shared__ int s_pg[kPgRing][kTileKeys];
   __shared__ int s_part[kPgRing][2];        // a tile's first and second 32 keys: not all of them are there
   __shared__ float2 s_ml[4][16];
-  __shared__ float s_inv[64];               // a finished unit's 1 / sum by row
   __shared__ unsigned long long s_flag;     // nodes of a tree tile whose V is not all finite
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -431,10 +451,6 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
       const int rest = use.w.nt - use.tile - 1, head = use.head * p.hg + sub, row0 = use.rt * p.Mt;
       const int rec = from_start ? (rest > 0 ? 2 * int(blockIdx.x) + 1 : -1) : 2 * int(blockIdx.x);
       const int rows = min(p.Mt, use.w.n * p.G - row0);
-      auto place = [&](int r) -> size_t {      // row r's (node, query head)
-        const int node = (row0 + r) / p.G;
-        return size_t(use.w.n0 + node) * p.Hq + head * p.G + row0 + r - node * p.G;
-      };
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         st.l[k] += __shfl_xor_sync(0xffffffffu, st.l[k], 1);
@@ -453,14 +469,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
 #pragma unroll
         for (int x = 0; x < C::kKG; ++x) l += s_ml[rg * C::kKG + x][r].y * fast_exp2(s_ml[rg * C::kKG + x][r].x - ref);
         f[k] = fast_exp2(st.m[k] - ref);
-        if (kg == 0 && (lane & 3) == 0 && rg * 16 + r < rows) {
-          if (rec >= 0)
-            p.rec_ml[size_t(rec) * p.Mt + rg * 16 + r] = make_float2(m, l);
-          else {
-            p.lse[place(rg * 16 + r)] = row_lse(m, l);
-            s_inv[rg * 16 + r] = row_inv(l);
-          }
-        }
+        if (rec >= 0 && kg == 0 && (lane & 3) == 0 && rg * 16 + r < rows)
+          p.rec_ml[size_t(rec) * p.Mt + rg * 16 + r] = make_float2(m, l);
       }
       float4 acc[D / 32];   // this thread's float4s of the [16][D] block
 #pragma unroll 1
@@ -470,7 +480,8 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
           for (int i = 0; i < D / 8; ++i)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
-              *reinterpret_cast<float2*>(s_o + ((lane >> 2) + 8 * k) * D + ((8 * i + 2 * (lane & 3)) ^ (((lane >> 2) & 3) << 3))) =
+              *reinterpret_cast<float2*>(s_o + ((lane >> 2) + 8 * k) * D +
+                                         ((8 * i + 2 * (lane & 3)) ^ (((lane >> 2) & 3) << 3))) =
                   make_float2(st.o[i][2 * k] * f[k], st.o[i][2 * k + 1] * f[k]);
         }
         __syncthreads();
@@ -484,13 +495,14 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const Tre
             acc[i] = make_float4(acc[i].x + x.x, acc[i].y + x.y, acc[i].z + x.z, acc[i].w + x.w);
           if (w % C::kKG == C::kKG - 1) {
             const int row = (w / C::kKG) * 16 + r;
-            if (row < rows) {
-              if (rec >= 0)
-                *reinterpret_cast<float4*>(p.rec_o + (size_t(rec) * p.Mt + row) * D + c) = acc[i];
-              else
-                store4<T>(p, place(row) * D + c, acc[i], s_inv[row]);
-            }
+            float* dst = rec >= 0 ? p.rec_o + (size_t(rec) * p.Mt + row) * D + c : s_o + r * D + (c ^ ((r & 3) << 3));
+            if (rec < 0 || row < rows) *reinterpret_cast<float4*>(dst) = acc[i];
           }
+        }
+        if (rec < 0 && w % C::kKG == C::kKG - 1) {
+          const int g = w / C::kKG;
+          finish_rows<T, D, C::kKG>(p, s_o, s_ml + g * C::kKG, size_t(use.w.n0) * p.Hq + head * p.G, row0 + g * 16,
+                                    row0 + rows);
         }
         __syncthreads();
       }
