@@ -252,6 +252,38 @@ def test_bad_device_arrays_are_recorded_and_skipped(splitkv):
     tree.check()
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("nodes", [20, 60, 120])
+def test_bad_pages_under_wide_trees(splitkv, nodes, d):
+    """The same in row tiles of 64, 128 and 256 rows: keys on bad pages are absent, whatever half or tile they are in."""
+    from context_block_sparse_b200.draft_tree import SplitKVTreeAttention
+    lens = [300, 200]
+    c = Case([nodes, nodes - 7], lens, 4, 2, d, 16, seed=15)
+    tree = SplitKVTreeAttention(4, 2, d, c.max_nodes)
+    table = c.table.clone()
+    table[0, 6], table[0, 17], table[1, 0], table[1, 12] = -1, c.k.shape[0], -2 ** 31, 2 ** 31 - 1
+    got = c.call(tree, page_table=table)
+    with pytest.raises(splitkv.SplitKVError):
+        tree.check()
+    c2 = Case([nodes, nodes - 7], lens, 4, 2, d, 16, seed=15)
+    for b, bad in enumerate(([6, 17], [0, 12])):
+        keep = torch.tensor([t for t in range(lens[b]) if t // 16 not in bad])
+        pages, t = c.table[b].long(), torch.arange(len(keep))
+        c2.k[pages[t // 16], t % 16] = c.k[pages[keep // 16], keep % 16]
+        c2.v[pages[t // 16], t % 16] = c.v[pages[keep // 16], keep % 16]
+        c2.lens[b] = len(keep)
+    c2.check(got)
+
+
+@pytest.mark.parametrize("kernel", ["mma", "tcgen05"])
+@pytest.mark.parametrize("counts,lens,hq,hkv,d", [
+    ([1], [3000], 8, 2, 128), ([3, 2], [64, 700], 8, 2, 64), ([40, 9], [513, 20], 4, 1, 128), ([30, 7], [300, 0], 8, 2, 64)])
+def test_asked_kernel(splitkv, monkeypatch, kernel, counts, lens, hq, hkv, d):
+    monkeypatch.setenv("SPLITKV_TREE_KERNEL", kernel)
+    c = Case(counts, lens, hq, hkv, d, 16, seed=17)
+    c.check(c.call())
+
+
 def test_offsets_past_32_bits(splitkv):
     """Pages beyond 2^31 elements (and 2^32 bytes) of a large cache."""
     c = Case([6], [300], 8, 8, 128, 128, seed=12)
@@ -267,7 +299,8 @@ def test_offsets_past_32_bits(splitkv):
 
 
 @pytest.mark.parametrize("args", [([6], [300], 8, 8, 128, 128), ([16, 9], [900, 257], 8, 2, 128, 64),
-                                  ([40], [2000], 4, 1, 64, 16)])
+                                  ([40], [2000], 4, 1, 64, 16), ([32, 20], [700, 1500], 8, 2, 64, 64),
+                                  ([60, 33], [1500, 400], 8, 2, 128, 64)])
 def test_cold_caches(splitkv, args):
     """Late keys and values (nothing in L2, the GPU just woken): products queue up behind the softmax's waits."""
     import time
