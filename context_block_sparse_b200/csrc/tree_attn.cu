@@ -514,59 +514,59 @@ __global__ void __launch_bounds__(kThreads, 2) tree_context_mma_kernel(const __g
 }
 
 // ------------------------------------------------------------------------------------ merge
-// A block per split unit and kMergeRows of its rows, a thread per four elements of a row: the row's records in
-// CTA order, each weighted by exp2(m_x - max m) (a record without keys has m = -inf, l = 0).  A stream over
-// the records, a few microseconds; launched early, it waits while the records are still being written.  (16 ragged trees of 16
-// nodes: blocks of 128 threads and 8 rows 64.2 us a call, 16 rows 66.4, 4 rows 65.0; of 256 threads 67.0, of 64 71.0.)
-constexpr int kMergeThreads = 128, kMergeRows = 8;
+// A block per split unit and some of its rows (4 at d = 128, 8 at d = 64), a thread per four elements of a row: the
+// row's records in CTA order, each weighted by exp2(m_x - max m) (a record without keys has m = -inf, l = 0).  A
+// stream over the records, a few microseconds; launched early, it waits while they are still being written.  (Two
+// sequences of 9 nodes over 10k keys, 74 records a row: 30 us a call with two rows a thread one after the other, 26 with one.
+// 16 ragged trees of 16 nodes take 62 us either way, 67 with blocks of 256 threads, 71 of 64.)
+constexpr int kMergeThreads = 128;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreeParams p) {
-  constexpr int kPass = kMergeThreads / (D / 4);
+  constexpr int kRows = kMergeThreads / (D / 4);
   const int first = blockIdx.x, c = threadIdx.x % (D / 4) * 4;       // the CTA in whose stretch the unit begins
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int4 u = p.split[first];
   if (u.w < 0) return;
   const int head = u.z & 0xffff, row0 = (u.z >> 16) * p.Mt, n_rec = u.w - first / p.hg + 1;
-  const int rows = min(int(blockIdx.y + 1) * kMergeRows, min(p.Mt, u.y * p.G - row0));
-  for (int r = blockIdx.y * kMergeRows + threadIdx.x / (D / 4); r < rows; r += kPass) {
-    float m = -INFINITY, l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kBatch = 8;
+  const int r = blockIdx.y * kRows + threadIdx.x / (D / 4);
+  if (r >= min(p.Mt, u.y * p.G - row0)) return;
+  float m = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int kBatch = 8;
 #pragma unroll 1
-    for (int k0 = 0; k0 < n_rec; k0 += kBatch) {
-      float2 ml[kBatch];
-      float4 y[kBatch];
-      float nm = m;
+  for (int k0 = 0; k0 < n_rec; k0 += kBatch) {
+    float2 ml[kBatch];
+    float4 y[kBatch];
+    float nm = m;
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        ml[k] = make_float2(-INFINITY, 0.f);
-        if (k0 + k < n_rec) {
-          const size_t at = size_t(k0 + k == 0 ? 2 * first + 1 : 2 * (first + (k0 + k) * p.hg)) * p.Mt + r;
-          ml[k] = p.rec_ml[at];
-          y[k] = *reinterpret_cast<const float4*>(p.rec_o + at * D + c);
-        }
+    for (int k = 0; k < kBatch; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.f);
+      if (k0 + k < n_rec) {
+        const size_t at = size_t(k0 + k == 0 ? 2 * first + 1 : 2 * (first + (k0 + k) * p.hg)) * p.Mt + r;
+        ml[k] = p.rec_ml[at];
+        y[k] = *reinterpret_cast<const float4*>(p.rec_o + at * D + c);
       }
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) nm = fmaxf(nm, ml[k].x);
-      const float ref = nm == -INFINITY ? 0.f : nm;
-      const float f0 = fast_exp2(m - ref);
-      l *= f0;
-      o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k) {
-        if (k0 + k < n_rec) {
-          const float f = fast_exp2(ml[k].x - ref);
-          l += ml[k].y * f;
-          o = make_float4(o.x + y[k].x * f, o.y + y[k].y * f, o.z + y[k].z * f, o.w + y[k].w * f);
-        }
-      }
-      m = nm;
     }
-    const size_t hr = size_t(u.x + (row0 + r) / p.G) * p.Hq + head * p.G + (row0 + r) % p.G;
-    store4<T>(p, hr * D + c, o, row_inv(l));
-    if (c == 0) p.lse[hr] = row_lse(m, l);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) nm = fmaxf(nm, ml[k].x);
+    const float ref = nm == -INFINITY ? 0.f : nm;
+    const float f0 = fast_exp2(m - ref);
+    l *= f0;
+    o = make_float4(o.x * f0, o.y * f0, o.z * f0, o.w * f0);
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (k0 + k < n_rec) {
+        const float f = fast_exp2(ml[k].x - ref);
+        l += ml[k].y * f;
+        o = make_float4(o.x + y[k].x * f, o.y + y[k].y * f, o.z + y[k].z * f, o.w + y[k].w * f);
+      }
+    }
+    m = nm;
   }
+  const size_t hr = size_t(u.x + (row0 + r) / p.G) * p.Hq + head * p.G + (row0 + r) % p.G;
+  store4<T>(p, hr * D + c, o, row_inv(l));
+  if (c == 0) p.lse[hr] = row_lse(m, l);
 }
 
 template <typename T, int D, int RG>
@@ -587,7 +587,7 @@ cudaError_t context_rows(const TreeParams& p, cudaStream_t s) {
 template <typename T, int D>
 cudaError_t merge(const TreeParams& p, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.ctas * p.hg, p.Mt / kMergeRows);
+  cfg.gridDim = dim3(p.ctas * p.hg, p.Mt / (kMergeThreads / (D / 4)));
   cfg.blockDim = dim3(kMergeThreads);
   cfg.stream = s;
   cudaLaunchAttribute at[1];

@@ -239,11 +239,17 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
         bits = 0;
         const int first = s.rt * NR + col0, last = min(first + Dm::kCols, s.rt * NR + s.rows);
         const uint8_t* m = p.mask + int64_t(s.n0) * p.mask_row + key0 + key_lane;
-#pragma unroll 8
-        for (int i = first / p.G; i * p.G < last; ++i) {
-          const int lo = max(i * p.G - first, 0), n = min((i + 1) * p.G - first, 32) - lo;
-          const uint32_t some = n >= 32 ? 0xffffffffu : (1u << n) - 1;
-          if (m[i * p.mask_row]) bits |= some << lo;
+#pragma unroll 1
+        for (int i0 = first / p.G; i0 * p.G < last; i0 += 8) {
+          uint8_t y[8];      // (eight nodes' bytes asked for at once)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) y[k] = (i0 + k) * p.G < last ? m[(i0 + k) * p.mask_row] : uint8_t(0);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int i = i0 + k, lo = max(i * p.G - first, 0), n = min((i + 1) * p.G - first, 32) - lo;
+            const uint32_t some = n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1;
+            if (y[k]) bits |= some << (lo & 31);
+          }
         }
       }
 #pragma unroll
@@ -288,6 +294,8 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
       bool need = live;           // a row has no reference yet
       group_sync(g);
       const int tile0 = s.tile0, ctx = s.ctx, nodes = s.n;
+      if ((tid & 127) < Dm::kCols && col0 + (tid & 127) < rows && tile0 + tiles > ctx)
+        want_mask(p, s.n0 + (s.rt * NR + col0 + (tid & 127)) / p.G, nodes);
       for (int j = 0; j < tiles; ++j, ++t) {
         const bool tree = tile0 + j >= ctx;
         const int key0 = (tile0 + j - (tree ? ctx : 0)) * kKeys, limit = (tree ? nodes : len) - key0;   // keys there are

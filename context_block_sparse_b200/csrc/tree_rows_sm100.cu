@@ -270,15 +270,23 @@ __global__ void __launch_bounds__(Dims<D, kSplit>::kThreads, 1)
         const int row0 = s.rt * p.Mt + r - lane, mine = (row0 + lane) / p.G;
         const int last = min((row0 + 31) / p.G, s.n - 1);
         uint32_t see[4] = {0, 0, 0, 0};
-#pragma unroll 2
-        for (int node = row0 / p.G; node <= last; ++node) {
-          const uint8_t* m = p.mask + int64_t(s.n0 + node) * p.mask_row + key0 + lane;
-          uint32_t w[4];
+#pragma unroll 1
+        for (int node0 = row0 / p.G; node0 <= last; node0 += 8) {
+          // (eight nodes' bytes asked for at once: the loop waits for memory, not for its instructions)
+          const uint8_t* m = p.mask + int64_t(s.n0 + node0) * p.mask_row + key0 + lane;
+          uint8_t y[8][4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) w[q] = __ballot_sync(0xffffffffu, 32 * q + lane < limit && m[32 * q]);
-          if (node == mine) {
+          for (int k = 0; k < 8; ++k)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) see[q] = w[q];
+            for (int q = 0; q < 4; ++q)
+              y[k][q] = node0 + k <= last && 32 * q + lane < limit ? m[k * p.mask_row + 32 * q] : uint8_t(0);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t w = __ballot_sync(0xffffffffu, y[k][q] != 0);
+              if (node0 + k == mine) see[q] = w;
+            }
           }
         }
 #pragma unroll
@@ -311,6 +319,7 @@ __global__ void __launch_bounds__(Dims<D, kSplit>::kThreads, 1)
       const bool rows_here = kSplit || rows > x * 128, mine = kSplit && ((tiles - 1) & 1) == x;
       const bool warp_live = rows > r - lane;       // (a warp without rows only keeps step)
       float ref = -INFINITY, l = 0.f;       // the row's reference (log2 units) and sum
+      if (r < rows && tile0 + tiles > ctx) want_mask(p, s.n0 + (s.rt * p.Mt + r) / p.G, nodes);
       if (!rows_here) {
         // (a row tile without rows keeps step with tile A: its queries' arrival must not fall into the segment before)
         more = open(seg + 1);

@@ -154,6 +154,14 @@ struct Walk {
   }
 };
 
+// The mask row of a node is wanted soon: its lines are asked for into L2.
+__device__ __forceinline__ void want_mask(const TreeParams& p, int node, int n) {
+  if (p.mask == nullptr) return;
+  const uint8_t* m = p.mask + int64_t(node) * p.mask_row;
+  for (int i = 0; i < n; i += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(m + i));
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(m + n - 1));
+}
+
 // Block-wide: this CTA's stretch of the line, and the sequence it begins in (bars->seq, rel, line, stop, ctas: valid after the
 // next block barrier).  Returns its places.
 template <int kThreads>
