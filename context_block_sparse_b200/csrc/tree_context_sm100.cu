@@ -17,12 +17,17 @@
 // second product reads as its MN-major B operand.
 //
 // The first warps are softmax groups of four, 32 rows each, which also load Q and write the
-// records.  Behind them one warp loads pages by TMA (one box a page and 64 columns) into a ring of
+// records or, of whole units, the finished rows.  Behind them one warp loads pages by TMA (one box a page and 64 columns) into a ring of
 // tiles in the order in which the products take them: K0, K1, V0, K2, V1, ...; the last issues the
 // products, S(j + 1) before PV(j), so that scores are formed while the softmax of the tile before
 // runs.
 // Keys behind the context's end or on a bad page are masked as lanes; their V rows are zeroed in
 // shared memory before the product (P = 0 does not hide a NaN).
+//
+// Measured (8 KV heads): d = 128, 32 sequences over 8k keys, 32 rows 172 us and 64 rows 186 (165 at the copy rate), 128
+// rows 225; 16 ragged trees of 64 rows over 1k-8k 62 (47); d = 64, 64 sequences over 4k, 32 rows 99 (83).  A long unit runs
+// at HBM's rate up to 64 rows; what is lost is a tile's chain of product, softmax and product at 128 rows, and at
+// every unit's ends its first references, its row sums and stores, 3000 to 5000 clocks.
 #include <cstdint>
 
 #include <cuda_bf16.h>

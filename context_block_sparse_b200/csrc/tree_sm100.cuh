@@ -162,8 +162,8 @@ __device__ __forceinline__ void want_mask(const TreeParams& p, int node, int n) 
   asm volatile("prefetch.global.L2 [%0];" ::"l"(m + n - 1));
 }
 
-// Block-wide: this CTA's stretch of the line, and the sequence it begins in (bars->seq, rel, line, stop, ctas: valid after the
-// next block barrier).  Returns its places.
+// Block-wide: this CTA's stretch of the line, and the sequence it begins in (bars->seq, rel, line, stop, ctas: valid
+// after the next block barrier).  Returns its places.
 template <int kThreads>
 __device__ __forceinline__ long long find_stretch(const TreeParams& p, CommonBars* bars) {
   const int tid = threadIdx.x;

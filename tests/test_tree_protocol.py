@@ -1,4 +1,5 @@
-"""Barrier protocol of the tcgen05 tree-attention kernel (tree_context_sm100.cu), on randomised schedules (CPU only).
+"""Barrier protocols of the tcgen05 tree-attention kernels (tree_context_sm100.cu; Rows and Split: the two forms of
+tree_rows_sm100.cu), on randomised schedules (CPU only).
 
 Roles: a loading warp (segments through a ring of four, then K0, K1, V0, K2, V1, ... through a ring of tiles), a thread
 that issues the products (S of the next tile before PV of this one), and softmax groups that share S, P^T and O by
