@@ -33,6 +33,14 @@ namespace splitkv {
 namespace tree {
 
 constexpr int kMaxNodes = 256;     // nodes of a sequence
+// P = exp2(s - reference) is rounded to the keys' type for the product with V.  float16 has 2^-14 .. 2^15 with all bits and
+// ends at 2^-24, so there the reference lies this many powers of two below the row's maximum, and P runs up to 2^15: with P up
+// to 1, a long context 18 (nats) below one dominating key of small V was rounded away.  A weight is then held to half a step
+// of itself, or to 2^-(25 + lift) of the row's largest where that is more.  On mma.sync the reference is the running
+// maximum itself; on tcgen05 it may stay behind it by `headroom` (rescaling O costs a tile's time), which takes its
+// share of the range: 8 for bfloat16, whose range is float32's, 3 for float16 (18 nats are 26 powers of two: 12 - 26 = -14).
+constexpr int lift_of(bool f16, bool tcgen05) { return f16 ? (tcgen05 ? 12 : 15) : 0; }
+constexpr int headroom_of(bool f16) { return f16 ? 3 : 8; }
 // On tcgen05: row tiles that are rows as M (tree_rows_sm100.cu); the others are rows as N (tree_context_sm100.cu).  N / M
 // measured: 256 rows, d = 128, 4 x 64 nodes over 64k to 128k 427 / 335 us; 128 rows (32 nodes of G = 4, 8 KV heads): d = 64,
 // 128 sequences over 4k 404 / 302, 32 over 1k 52 / 49, one over 2k 20.7 / 20.6; d = 128, 128 over 4k 467 / 434, but 32 over
@@ -58,9 +66,10 @@ struct TreeParams {
   int hg;                          // neighbouring heads that as many CTAs walk in step: 1 or 2
   int ctas;                        // C: stretches; the context kernel has C hg CTAs
   int o_f32;
+  int lift;                        // powers of two from a row's reference up to its maximum (lift_of)
   float scale_log2;
   float* rec_o;                    // [2 hg C][Mt][d]
-  float2* rec_ml;                  // [2 hg C][Mt]: maximum (log2 units), sum
+  float2* rec_ml;                  // [2 hg C][Mt]: reference (log2 units), sum
   int4* split;                     // [hg C]: the unit that begins in this CTA's stretch and ends in a later one:
                                    // first node, nodes, head + (row tile << 16), the last stretch (-1: none)
 };
@@ -140,9 +149,13 @@ __device__ __forceinline__ int cta_before(long long W, long long x, int C) {
   return int(c);
 }
 
-// A finished row: what O's sums are multiplied by, and its lse.
+// A finished row: what O's sums are multiplied by, and its lse (m: the row's reference, `lift` below its maximum; adding
+// that back and taking it out of l costs nothing and keeps the logarithm small).
 __device__ __forceinline__ float row_inv(float l) { return l == 0.f ? 0.f : 1.f / l; }   // no key: o = 0 (a NaN stays NaN)
-__device__ __forceinline__ float row_lse(float m, float l) { return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f; }
+__device__ __forceinline__ float row_lse(float m, float l, int lift) {
+  const float down = __int_as_float((127 - lift) << 23);   // 2^-lift
+  return l == 0.f ? -INFINITY : ((m + float(lift)) + log2f(l * down)) * 0.693147180559945309f;
+}
 
 // Infinities and NaN among the 16-bit values of x are replaced by 0; returns whether there were any.
 template <typename T>

@@ -17,6 +17,7 @@
 // rounded to the keys' type for the second product, as in the training kernels.
 #include <cstdint>
 #include <cstdlib>
+#include <type_traits>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -95,7 +96,10 @@ __device__ __forceinline__ void scores(float (&s)[kKeys / 8][4], const uint32_t 
   }
 }
 
-// The state of two rows of a thread: maximum (log2 units), this thread's share of the sum, and
+template <typename T>
+constexpr int kLift = lift_of(std::is_same_v<T, __half>, false);
+
+// The state of two rows of a thread: reference (the maximum less kLift; log2 units), this thread's share of the sum, and
 // the rows' NC columns of O.
 template <int NC>
 struct Rows {
@@ -127,7 +131,7 @@ __device__ __forceinline__ void softmax_step(Rows<NC>& st, float (&s)[kKeys / 8]
   for (int k = 0; k < 2; ++k) {
     mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 1));
     mx[k] = fmaxf(mx[k], __shfl_xor_sync(0xffffffffu, mx[k], 2));
-    const float m = fmaxf(st.m[k], mx[k]);
+    const float m = fmaxf(st.m[k], mx[k] - float(kLift<T>));
     ref[k] = m == -INFINITY ? 0.f : m;    // no key yet: every exponential below is exp2(-inf) = 0
     f[k] = fast_exp2(st.m[k] - ref[k]);
     st.m[k] = m;
@@ -193,7 +197,7 @@ __device__ __noinline__ void finish_rows(const TreeParams& p, const float* s_o, 
     const int node = row / p.G;
     const size_t hr = hr0 + size_t(node) * p.Hq + (row - node * p.G);
     store4<T>(p, hr * D + c, *reinterpret_cast<const float4*>(s_o + r * D + (c ^ ((r & 3) << 3))), row_inv(l));
-    if (c == 0) p.lse[hr] = row_lse(m, l);
+    if (c == 0) p.lse[hr] = row_lse(m, l, kLift<T>);
   }
 }
 
@@ -566,7 +570,7 @@ __global__ void __launch_bounds__(kMergeThreads) tree_merge_kernel(const TreePar
   }
   const size_t hr = size_t(u.x + (row0 + r) / p.G) * p.Hq + head * p.G + (row0 + r) % p.G;
   store4<T>(p, hr * D + c, o, row_inv(l));
-  if (c == 0) p.lse[hr] = row_lse(m, l);
+  if (c == 0) p.lse[hr] = row_lse(m, l, p.lift);
 }
 
 template <typename T, int D, int RG>
@@ -771,6 +775,7 @@ extern "C" int splitkv_tree_attn(const splitkv_tree_args* a, void* ws, size_t ws
   p.hg = z.hg;
   p.ctas = z.ctas;
   p.o_f32 = a->o_dtype == SPLITKV_DTYPE_F32;
+  p.lift = splitkv::tree::lift_of(a->dtype == SPLITKV_DTYPE_F16, z.tile_shift == 7);
   // (a scale of 0 as a tiny one: scores stay 0 for any finite product, and a masked score can still be -inf)
   p.scale_log2 = a->scale == 0.f ? 1e-30f : a->scale * splitkv::kLog2e;
   p.rec_o = static_cast<float*>(ws);

@@ -10,7 +10,7 @@
 //
 // In S^T a TMEM lane is a key, so a softmax thread holds one key's scores of 32 rows.
 // Its row maxima would need 128 lanes' agreement at every tile; instead a row keeps a reference, the
-// maximum of its first tile, and P = exp2(s - reference) may grow up to 2^kHeadroom before the
+// maximum of its first tile (less kLift), and P = exp2(s - reference) may grow by 2^kHeadroom before the
 // reference moves (O^T and the sums are then rescaled): a tile costs one barrier vote instead of a
 // reduction.  Row sums stay in registers, one lane's share of 32 rows, and are reduced when the unit
 // ends.  A thread's 32 probabilities are half a 128-byte row of P^T in the swizzled layout that the
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
           }
         }
         bool over = need;
-        if (!need && live) over = group_any(g, mx > kHeadroom);
+        if (!need && live) over = group_any(g, mx > kLift<T> + kHeadroom<T>);
         if (over) {
           need = false;
           // new references of the group's rows: lane i of every warp gets column i's maximum
@@ -366,7 +366,8 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
 #pragma unroll
           for (int w = 0; w < 4; ++w) m = fmaxf(m, s_x[w * Dm::kCols + lane]);
           // (the four warps hold the same values, so their votes agree)
-          const float to = old == -INFINITY ? m : (m > old + kHeadroom ? m : old);
+          m -= kLift<T>;
+          const float to = old == -INFINITY ? m : (m > old + kHeadroom<T> ? m : old);
           const float f = old == -INFINITY ? 1.f : fast_exp2(old - to);
           if (wq == 0) {
             nref[lane] = to == -INFINITY ? -0.0f : 0.f - to;
@@ -515,7 +516,7 @@ __global__ void __launch_bounds__(Dims<D, NR>::kThreads, Dims<D, NR>::kPerSm)
             if (rec >= 0)
               p.rec_ml[size_t(rec) * NR + col0 + row] = make_float2(m, sum);
             else
-              p.lse[hr0 + at] = row_lse(m, sum);
+              p.lse[hr0 + at] = row_lse(m, sum, int(kLift<T>));
           }
         }
         group_sync(g);

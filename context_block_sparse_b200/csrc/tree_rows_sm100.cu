@@ -18,7 +18,7 @@
 // of 64 keys, whose products overlap the other half's softmax, saved 20 % of the clocks and took 525 us: the
 // clock fell by more (N = 64 products read more of shared memory for the same work).
 //
-// As in the training kernels P = exp2(s - reference), where the reference is the row's first maximum and
+// As in the training kernels P = exp2(s - reference), where the reference is the row's first maximum (less kLift) and
 // moves only when a later one exceeds it by kHeadroom (the row's O and sum are then rescaled).  Scores of
 // keys that a row does not see are overwritten in tensor memory before anything else reads them; V rows
 // that are not there are zeroed in shared memory, and what is not finite in a tree's V is taken out of it
@@ -362,11 +362,11 @@ __global__ void __launch_bounds__(Dims<D, kSplit>::kThreads, 1)
 #pragma unroll
               for (int i = 0; i < 128; ++i) m0 = fminf(m0, __uint_as_float(v[i]));
             }
-            const float m = scale > 0.f ? fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * scale : m0 * scale;
+            const float m = (scale > 0.f ? fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * scale : m0 * scale) - kLift<T>;
             float f = 1.f;
             if (ref == -INFINITY) {
               ref = m;                             // (its O and sum are still zero)
-            } else if (m > ref + kHeadroom) {
+            } else if (m > ref + kHeadroom<T>) {
               f = fast_exp2(ref - m);
               ref = m;
             }
@@ -529,7 +529,7 @@ __global__ void __launch_bounds__(Dims<D, kSplit>::kThreads, 1)
           if (rec >= 0)
             p.rec_ml[at] = make_float2(ref, l);
           else
-            p.lse[hr] = row_lse(ref, l);
+            p.lse[hr] = row_lse(ref, l, int(kLift<T>));
         }
       }
       ++na;

@@ -14,7 +14,6 @@ constexpr int kKeys = 128;                    // keys of a tile (M of the first 
 constexpr uint32_t kHalf = kKeys * 128;       // bytes of 128 rows x 64 columns
 constexpr uint32_t kBarBytes = 960;           // barrier block
 constexpr int kMetaRing = 16;                 // page-error masks in flight (K tiles)
-constexpr float kHeadroom = 8.0f;             // log2: P up to 256 (float16 P stays far from its limits)
 
 #ifdef __CUDACC__
 
@@ -37,6 +36,11 @@ template <typename T>
 constexpr bool kIsF16 = false;
 template <>
 constexpr bool kIsF16<__half> = true;
+// log2: how far a row's reference lies below its first maximum, and by how much more a later one may exceed it
+template <typename T>
+constexpr float kLift = float(lift_of(kIsF16<T>, true));
+template <typename T>
+constexpr float kHeadroom = float(headroom_of(kIsF16<T>));
 template <typename T>
 __device__ __forceinline__ uint32_t pack(float lo, float hi) {
   if constexpr (kIsF16<T>) {
