@@ -23,6 +23,7 @@
 #include "common.cuh"
 #include "splitkv.h"
 #include "splitkv_internal.h"
+#include "strided.h"
 
 namespace {
 
@@ -203,13 +204,12 @@ cudaError_t launch(const RopeParams& p, bool interleaved, dim3 grid, cudaStream_
 
 int dtype_bytes(int dt) { return dt == SPLITKV_DTYPE_F32 ? 4 : 2; }
 
-// Bytes from the first to one past the last element of a strided [tokens][heads][d] array.
-int64_t extent(int64_t n, int heads, int64_t st, int64_t sh, int64_t d, int64_t es) {
-  return ((n - 1) * st + (heads - 1) * sh + d) * es;
+splitkv::Strided side(const splitkv_rope_args& a, const void* ptr, int heads, const int64_t* s) {
+  const int64_t es = dtype_bytes(a.dtype);
+  return {ptr, a.head_dim * es, 2, {a.num_tokens, heads}, {s[0] * es, s[1] * es}};
 }
 
-// The output of one side: strides that keep every element apart, and either exactly the
-// input (in place) or memory apart from it.
+// One side by itself: pointers, strides within range, and an output whose elements are apart from each other.
 bool side_ok(const splitkv_rope_args& a, const void* in, const void* out, int heads, const int64_t* is,
              const int64_t* os) {
   if (heads == 0) return true;
@@ -222,11 +222,16 @@ bool side_ok(const splitkv_rope_args& a, const void* in, const void* out, int he
   if (reinterpret_cast<uintptr_t>(in) % es || reinterpret_cast<uintptr_t>(out) % es) return false;
   const bool token_major = (heads == 1 || os[1] >= d) && (n == 1 || os[0] >= (heads - 1) * os[1] + d);
   const bool head_major = (n == 1 || os[0] >= d) && (heads == 1 || os[1] >= (n - 1) * os[0] + d);
-  if (!token_major && !head_major) return false;
-  const uintptr_t i0 = reinterpret_cast<uintptr_t>(in), o0 = reinterpret_cast<uintptr_t>(out);
-  const bool same = i0 == o0 && (n == 1 || is[0] == os[0]) && (heads == 1 || is[1] == os[1]);
-  const uintptr_t i1 = i0 + extent(n, heads, is[0], is[1], d, es), o1 = o0 + extent(n, heads, os[0], os[1], d, es);
-  return same || i1 <= o0 || o1 <= i0;
+  return token_major || head_major;
+}
+
+// An output against one input: exactly that input, where it is its own (in place: a thread reads what it writes), or
+// memory apart from it.  Queries and keys share the launch, so each output is held against both inputs.
+bool output_ok(const splitkv_rope_args& a, const void* out, int heads, const int64_t* os, const void* in, int in_heads,
+               const int64_t* is, bool own) {
+  if (heads == 0 || in_heads == 0) return true;
+  const bool same = own && in == out && (a.num_tokens == 1 || is[0] == os[0]) && (heads == 1 || is[1] == os[1]);
+  return same || splitkv::apart(side(a, out, heads, os), side(a, in, in_heads, is));
 }
 
 }  // namespace
@@ -272,6 +277,12 @@ extern "C" int splitkv_rope(const splitkv_rope_args* a, void* stream) {
     return SPLITKV_ERR_INVALID_ARG;
   if (!side_ok(*a, a->q, a->q_out, a->q_heads, a->q_stride, a->q_out_stride) ||
       !side_ok(*a, a->k, a->k_out, a->k_heads, a->k_stride, a->k_out_stride))
+    return SPLITKV_ERR_INVALID_ARG;
+  if (!output_ok(*a, a->q_out, a->q_heads, a->q_out_stride, a->q, a->q_heads, a->q_stride, true) ||
+      !output_ok(*a, a->q_out, a->q_heads, a->q_out_stride, a->k, a->k_heads, a->k_stride, false) ||
+      !output_ok(*a, a->k_out, a->k_heads, a->k_out_stride, a->q, a->q_heads, a->q_stride, false) ||
+      !output_ok(*a, a->k_out, a->k_heads, a->k_out_stride, a->k, a->k_heads, a->k_stride, true) ||
+      !output_ok(*a, a->q_out, a->q_heads, a->q_out_stride, a->k_out, a->k_heads, a->k_out_stride, false))
     return SPLITKV_ERR_INVALID_ARG;
 
   const int es = dtype_bytes(a->dtype), P = 16 / es;

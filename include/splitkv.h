@@ -536,8 +536,9 @@ int splitkv_read_cta_times(const splitkv_plan_t* plan, int which, int64_t* out_n
 
 /* One rotary call.  HOST struct, read during the call; q and k share positions, dtype and head
  * size, and either may have 0 heads.  Strides are in elements, {token, head}; the last dimension is
- * contiguous.  An output is its input itself (same pointer and strides: in place) or memory apart
- * from every input. */
+ * contiguous.  An output is its own input itself (same pointer and strides: in place) or memory apart
+ * from every input and from the other output (views woven into one buffer, such as the heads of a
+ * fused projection, are apart); anything else is refused. */
 typedef struct splitkv_rope_args {
   int64_t       num_tokens;
   int32_t       q_heads, k_heads;

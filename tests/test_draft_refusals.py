@@ -1,0 +1,109 @@
+"""Refusals of the rotary and draft-tree calls that go by where their arrays lie (host only: nothing is launched)."""
+
+import ctypes
+
+import pytest
+
+BAD, UNSUP = -1, -2
+M = 1 << 20
+
+
+def i64(*x):
+    return (ctypes.c_int64 * len(x))(*x)
+
+
+def _rope(abi, **kw):
+    """10 tokens, 4 + 2 heads of 64 in 16 bits: q 5120 bytes, k 2560."""
+    a = abi.RopeArgs(10, 4, 2, 64, 64, abi.DTYPE_BF16, 0, 1.0, 4096, 8192, M, 2 * M, 3 * M, 4 * M,
+                     (256, 64), (256, 64), (128, 64), (128, 64))
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q_out=3 * M),                                   # q' over k
+    dict(q_out=3 * M - 4096),                            # its last tokens over k's first
+    dict(k_out=M),                                       # k' over q
+    dict(k_out=M + 5120 - 16),                           # over q's last elements
+    dict(k_out=2 * M),                                   # k' over q'
+    dict(k_out=2 * M + 2560),
+    dict(q_out=M, k=M, k_out=M),                         # one array in place as both
+    dict(q_out=M, k=M),                                  # q in place, and k reads it
+    dict(q_out=3 * M, k_out=M),                          # swapped
+    # q in place in a fused buffer of 6 heads a token, k' at its last head: one head of k' would be the next token's
+    dict(q_out=M, q_stride=i64(384, 64), q_out_stride=i64(384, 64), k_out=M + 640, k_out_stride=i64(384, 64)),
+])
+def test_rotary_outputs_over_the_other_side(splitkv, kw):
+    assert splitkv._lib.splitkv_rope(ctypes.byref(_rope(splitkv._abi, **kw)), None) == BAD
+
+
+HARNESS = r"""
+#include <cstdio>
+#include <vector>
+#include "strided.h"
+using splitkv::Strided;
+int main() {
+  Strided a[2];
+  long long p;
+  while (std::scanf("%lld", &p) == 1) {
+    for (int k = 0; k < 2; ++k) {
+      if (k) std::scanf("%lld", &p);
+      long long row, n, s, t;
+      std::scanf("%lld %lld", &row, &n);
+      a[k] = {reinterpret_cast<const void*>(p), row, int(n), {}, {}};
+      for (int i = 0; i < n; ++i) {
+        std::scanf("%lld %lld", &s, &t);
+        a[k].size[i] = s;
+        a[k].stride[i] = t;
+      }
+    }
+    std::printf("%d %d\n", int(splitkv::apart(a[0], a[1])), int(splitkv::apart(a[1], a[0])));
+  }
+}
+"""
+
+
+def _bytes(ptr, row, dims):
+    at = {ptr}
+    for n, s in dims:
+        at = {a + i * s for a in at for i in range(n)}
+    return {a + i for a in at for i in range(row)}
+
+
+def test_apart_arrays(splitkv, tmp_path):
+    """apart() against the bytes themselves: never true for arrays that meet, true for extents that do not and for the
+    woven views that callers have."""
+    import os
+    import random
+    import subprocess
+    from conftest import ROOT
+    src, exe = tmp_path / "apart.cpp", tmp_path / "apart"
+    src.write_text(HARNESS)
+    subprocess.run(["g++", "-std=c++17", "-I", os.path.join(ROOT, "context_block_sparse_b200", "csrc"), str(src), "-o",
+                    str(exe)], check=True)
+    rng = random.Random(1)
+    woven = [((0, 8, [(5, 48), (2, 8)]), (16, 8, [(5, 48), (4, 8)])),        # heads of a fused projection
+             ((0, 8, [(5, 48), (2, 24)]), (8, 8, [(5, 48), (2, 24)])),       # q and k of one head side by side
+             ((0, 8, [(2, 240), (5, 48)]), (24, 8, [(7, 48)])),
+             ((0, 4, [(3, 64), (4, 8)]), (32, 4, [(3, 64), (4, 8)])),        # keys beside values in a page
+             ((0, 4, [(2, 192), (3, 64), (4, 8)]), (32, 4, [(3, 64), (2, 192), (4, 8)])),
+             ((0, 4, [(1, 7), (4, 8)]), (4, 4, [(4, 8)]))]
+    cases = list(woven)
+    for _ in range(4000):
+        mk = lambda: (rng.randrange(60), rng.randint(1, 6), [(rng.randint(1, 4), rng.choice([0, 4, 6, 8, 12, 24, 30, 48]))
+                                                             for _ in range(rng.randint(0, 4))])  # noqa: E731
+        cases.append((mk(), mk()))
+    text = "\n".join(" ".join(f"{4096 + p} {row} {len(dims)} " + " ".join(f"{n} {s}" for n, s in dims)
+                              for p, row, dims in pair) for pair in cases)
+    out = subprocess.run([str(exe)], input=text + "\n", capture_output=True, text=True, check=True).stdout.split()
+    said = list(zip(out[::2], out[1::2]))
+    assert len(said) == len(cases)
+    for i, (pair, (xy, yx)) in enumerate(zip(cases, said)):
+        x, y = (_bytes(*p) for p in pair)
+        assert xy == yx
+        if xy == "1":
+            assert not x & y, pair
+        if i < len(woven) or max(x) < min(y) or max(y) < min(x):
+            assert xy == "1", pair
+    assert sum(xy == "1" for xy, _ in said) > 500
