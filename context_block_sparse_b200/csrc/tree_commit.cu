@@ -17,6 +17,7 @@
 #include "common.cuh"
 #include "splitkv.h"
 #include "splitkv_internal.h"
+#include "strided.h"
 
 namespace {
 
@@ -121,6 +122,20 @@ extern "C" int splitkv_tree_commit(const splitkv_commit_args* a, void* stream) {
       !strides_ok(a->k_cache, a->k_stride, 4, es) || !strides_ok(a->v_cache, a->v_stride, 4, es))
     return SPLITKV_ERR_INVALID_ARG;
   if (!a->node_ptr || !a->page_table || !a->context_lens || (a->path && !a->count)) return SPLITKV_ERR_INVALID_ARG;
+  // A row that is read while another CTA writes it would be either's: the new keys and values lie apart from both caches,
+  // and the caches from each other.
+  const int64_t row = int64_t(a->head_dim) * es, L = a->num_layers, H = a->num_kv_heads;
+  const auto fresh = [&](const void* ptr, const int64_t* s) {
+    return splitkv::Strided{ptr, row, 3, {L, a->num_nodes, H}, {s[0] * es, s[1] * es, s[2] * es}};
+  };
+  const auto cache = [&](const void* ptr, const int64_t* s) {
+    return splitkv::Strided{ptr, row, 4, {L, a->num_pages, a->page_size, H}, {s[0] * es, s[1] * es, s[2] * es, s[3] * es}};
+  };
+  const splitkv::Strided kb = fresh(a->kb, a->kb_stride), vb = fresh(a->vb, a->vb_stride);
+  const splitkv::Strided kc = cache(a->k_cache, a->k_stride), vc = cache(a->v_cache, a->v_stride);
+  if (!splitkv::apart(kb, kc) || !splitkv::apart(kb, vc) || !splitkv::apart(vb, kc) || !splitkv::apart(vb, vc) ||
+      !splitkv::apart(kc, vc))
+    return SPLITKV_ERR_INVALID_ARG;
   CommitParams p;
   p.kb = static_cast<const char*>(a->kb);
   p.vb = static_cast<const char*>(a->vb);

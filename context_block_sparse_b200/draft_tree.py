@@ -112,7 +112,8 @@ def commit_draft(k_cache, v_cache, page_table, context_lens, kb, vb, node_ptr, p
     Caches [pages, page_size, heads, d] with kb, vb [nodes, heads, d], or all layers at once with one more leading
     dimension on the four.  path, count: as verify_draft returns them; without a path every node is appended in
     order (max_nodes then bounds a sequence's nodes).  context_lens is not advanced: add count once all layers are
-    written.  Sequences must not share the pages they write."""
+    written.  Sequences must not share the pages they write, and kb, vb must lie apart from the caches (nodes that are in
+    the cache already are copied out first)."""
     if path is None:
         if max_nodes is None:
             raise ValueError("max_nodes bounds the nodes of a sequence where no path is given")

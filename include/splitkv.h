@@ -677,7 +677,9 @@ typedef struct splitkv_commit_args {
 
 /* Copy row path[b][i] (i < count[b]) of sequence b's new keys and values to cache token
  * context_lens[b] + i, in every layer.  context_lens is not advanced (one sequence state serves all
- * layers): the caller adds count once.  Sequences must not share the pages they write.
+ * layers): the caller adds count once.  Sequences must not share the pages they write.  kb and vb lie
+ * apart from both caches, and the caches from each other (keys and values woven into one cache are
+ * apart): anything else is refused.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 int splitkv_tree_commit(const splitkv_commit_args* args, void* stream);
 

@@ -107,3 +107,25 @@ def test_apart_arrays(splitkv, tmp_path):
         if i < len(woven) or max(x) < min(y) or max(y) < min(x):
             assert xy == "1", pair
     assert sum(xy == "1" for xy, _ in said) > 500
+
+
+def _commit(abi, **kw):
+    """2 layers, 10 pages of 16 tokens, 2 heads of 64 in 16 bits (81920 bytes a cache); 8 new nodes (4096 bytes)."""
+    a = abi.CommitArgs(2, 2, 8, 4, 2, 64, 2, 16, 10, 5, M, 2 * M, 3 * M, 4 * M, 4096, 4096, 4096, 4096, 4096, None,
+                       (1024, 128, 64), (1024, 128, 64), (20480, 2048, 128, 64), (20480, 2048, 128, 64), 4, 5)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("kw", [
+    dict(kb=3 * M),                                                 # new keys that view the first page
+    dict(kb=3 * M + 40960, kb_stride=i64(20480, 128, 64)),          # a page of every layer
+    dict(vb=3 * M + 81920 - 16),                                    # new values over the cache of keys
+    dict(kb=4 * M - 2048),
+    dict(kb=4 * M + 4096, vb=4 * M),
+    dict(v_cache=3 * M), dict(v_cache=3 * M + 128),                 # one cache for both
+    dict(num_pages=2 ** 31 - 1, k_stride=i64(20480, 1 << 44, 128, 64), kb=5 * M),   # an extent past 64 bits
+])
+def test_commit_from_inside_a_cache(splitkv, kw):
+    assert splitkv._lib.splitkv_tree_commit(ctypes.byref(_commit(splitkv._abi, **kw)), None) == BAD

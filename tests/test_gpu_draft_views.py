@@ -38,3 +38,41 @@ def test_rotary_refuses_outputs_that_meet(splitkv):
         with pytest.raises((splitkv.SplitKVError, ValueError)):
             rot.forward(pos, *args, out=out)
     assert torch.equal(buf, keep)
+
+
+def _accepted(dev="cuda"):
+    g = torch.Generator().manual_seed(0)
+    i = lambda *x: torch.tensor(x, dtype=torch.int32, device=dev)  # noqa: E731
+    table = torch.randperm(12, generator=g).int().view(3, 4).to(dev)
+    return dict(table=table, lens=i(30, 0, 15), ptr=i(0, 4, 9, 11), path=i(0, 2, -1, 0, 1, 4, 0, -1, -1).view(3, 3),
+                count=i(2, 3, 1))
+
+
+def test_commit_between_views_of_one_arena(splitkv):
+    """Keys beside values in every page, layers inside the pages, and the new rows behind them in the same buffer."""
+    from context_block_sparse_b200.draft_tree import commit_draft
+    a = _accepted()
+    args = (a["table"], a["lens"])
+    for layers_first in (True, False):
+        cache = 2 * 12 * 2 * 16 * 2 * 64
+        arena = torch.randn(cache + 2 * 2 * 11 * 2 * 64, device="cuda").bfloat16()
+        new = arena[cache:].view(2, 2, 11, 2, 64)                                   # [k / v, layers, nodes, heads, d]
+        pages = arena[:cache].view(2, 12, 2, 16, 2, 64) if layers_first else arena[:cache].view(12, 2, 2, 16, 2, 64).transpose(0, 1)
+        k, v = pages[:, :, 0], pages[:, :, 1]
+        kk, vv, kb, vb = k.clone(), v.clone(), new[0].clone(), new[1].clone()
+        commit_draft(k, v, *args, new[0], new[1], a["ptr"], a["path"], a["count"])
+        commit_draft(kk, vv, *args, kb, vb, a["ptr"], a["path"], a["count"])
+        assert torch.equal(k, kk) and torch.equal(v, vv) and torch.equal(new[0], kb) and torch.equal(new[1], vb)
+
+
+def test_commit_refuses_sources_in_a_cache(splitkv):
+    from context_block_sparse_b200.draft_tree import commit_draft
+    a = _accepted()
+    k, v = (torch.randn(12, 16, 2, 64, device="cuda").bfloat16() for _ in range(2))
+    keep, new = k.clone(), torch.randn(11, 2, 64, device="cuda").bfloat16()
+    inside = k[3, :11]
+    for kb, vb, kc, vc in ((inside, new, k, v), (new, inside, k, v), (new, new, k, k)):
+        with pytest.raises(splitkv.SplitKVError):
+            commit_draft(kc, vc, a["table"], a["lens"], kb, vb, a["ptr"], a["path"], a["count"])
+    assert torch.equal(k, keep)
+    commit_draft(k, v, a["table"], a["lens"], inside.clone(), new, a["ptr"], a["path"], a["count"])
