@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kMaxRows = 32;   // path rows of one CTA
+constexpr int kUnroll = 4;     // vectors of keys and of values in flight a thread
 
 struct CommitParams {
   const char *kb, *vb;
@@ -69,12 +70,11 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const CommitParam
   const char* vb = p.vb + layer * p.vb_s[0];
   char* kc = p.kc + layer * p.kc_s[0];
   char* vc = p.vc + layer * p.vc_s[0];
-  constexpr int kU = 4;
-  for (int i0 = threadIdx.x; i0 < total; i0 += kThreads * kU) {
-    uint4 x[kU], y[kU];
-    int64_t kd[kU], vd[kU];
+  for (int i0 = threadIdx.x; i0 < total; i0 += kThreads * kUnroll) {
+    uint4 x[kUnroll], y[kUnroll];
+    int64_t kd[kUnroll], vd[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
+    for (int u = 0; u < kUnroll; ++u) {
       const int j = i0 + u * kThreads;
       kd[u] = -1;
       if (j < total) {
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(kThreads) tree_commit_kernel(const CommitParam
       }
     }
 #pragma unroll
-    for (int u = 0; u < kU; ++u) {
+    for (int u = 0; u < kUnroll; ++u) {
       if (kd[u] >= 0) {
         *reinterpret_cast<uint4*>(kc + kd[u]) = x[u];
         *reinterpret_cast<uint4*>(vc + vd[u]) = y[u];
@@ -117,6 +117,9 @@ extern "C" int splitkv_tree_commit(const splitkv_commit_args* a, void* stream) {
   if ((int64_t(a->head_dim) * a->elem_bytes) % 16) return SPLITKV_ERR_UNSUPPORTED;
   if (a->num_layers == 0 || a->num_seqs == 0 || a->max_rows == 0 || a->num_nodes == 0) return SPLITKV_OK;
   if (a->num_layers > 65535 || a->num_seqs > 65535) return SPLITKV_ERR_UNSUPPORTED;
+  // (the kernel counts a CTA's 16-byte vectors in 32 bits, and steps past the last of them)
+  if (int64_t(a->num_kv_heads) * a->head_dim * a->elem_bytes / 16 * kMaxRows > 0x7fffffff - kThreads * kUnroll)
+    return SPLITKV_ERR_UNSUPPORTED;
   const int64_t es = a->elem_bytes;
   if (!strides_ok(a->kb, a->kb_stride, 3, es) || !strides_ok(a->vb, a->vb_stride, 3, es) ||
       !strides_ok(a->k_cache, a->k_stride, 4, es) || !strides_ok(a->v_cache, a->v_stride, 4, es))
@@ -168,11 +171,13 @@ extern "C" int splitkv_tree_commit(const splitkv_commit_args* a, void* stream) {
   p.vecs = int(int64_t(a->head_dim) * es / 16);
   // Path rows of a CTA: few when few CTAs would run (the copy is then one CTA's latency),
   // many when the grid fills the GPU anyway.
+  // (Without a path no sequence has more rows than there are nodes, however loose the caller's bound.)
   const int64_t groups = int64_t(a->num_layers) * a->num_seqs;
+  const int64_t most = a->path || a->max_rows < a->num_nodes ? a->max_rows : a->num_nodes;
   int rows = kMaxRows;
-  while (rows > 2 && groups * ((a->max_rows + rows - 1) / rows) < 296) rows /= 2;
+  while (rows > 2 && groups * ((most + rows - 1) / rows) < 296) rows /= 2;
   p.rows_per_cta = rows;
-  const dim3 grid(unsigned((a->max_rows + rows - 1) / rows), unsigned(a->num_seqs), unsigned(a->num_layers));
+  const dim3 grid(unsigned((most + rows - 1) / rows), unsigned(a->num_seqs), unsigned(a->num_layers));
   tree_commit_kernel<<<grid, kThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
   return cudaGetLastError() == cudaSuccess ? SPLITKV_OK : SPLITKV_ERR_CUDA;
 }

@@ -129,3 +129,14 @@ def _commit(abi, **kw):
 ])
 def test_commit_from_inside_a_cache(splitkv, kw):
     assert splitkv._lib.splitkv_tree_commit(ctypes.byref(_commit(splitkv._abi, **kw)), None) == BAD
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(num_kv_heads=65536, head_dim=65536, elem_bytes=4), UNSUP),    # a token of 2^30 vectors: 32 rows pass 2^31
+    (dict(num_kv_heads=4096, head_dim=65536, elem_bytes=4), UNSUP),     # 2^26 of them: just past
+])
+def test_commit_of_tokens_past_the_index_range(splitkv, kw, code):
+    z4, z3 = i64(0, 0, 0, 0), i64(0, 0, 0)
+    a = _commit(splitkv._abi, kb=1 << 50, vb=1 << 51, k_cache=1 << 52, v_cache=1 << 53, kb_stride=z3, vb_stride=z3,
+                k_stride=z4, v_stride=z4, **kw)
+    assert splitkv._lib.splitkv_tree_commit(ctypes.byref(a), None) == code

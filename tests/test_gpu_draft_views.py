@@ -76,3 +76,24 @@ def test_commit_refuses_sources_in_a_cache(splitkv):
             commit_draft(kc, vc, a["table"], a["lens"], kb, vb, a["ptr"], a["path"], a["count"])
     assert torch.equal(k, keep)
     commit_draft(k, v, a["table"], a["lens"], inside.clone(), new, a["ptr"], a["path"], a["count"])
+
+
+@pytest.mark.parametrize("bound", [4, 5, 4000, 2 ** 31 - 1])
+def test_commit_without_a_path_under_any_bound(splitkv, bound):
+    """Every node in order; a bound below a sequence's nodes leaves that sequence out and is recorded."""
+    from context_block_sparse_b200.draft_tree import check_status, commit_draft, new_status
+    a = _accepted()
+    k, v = (torch.randn(12, 16, 2, 64, device="cuda").bfloat16() for _ in range(2))
+    kb, vb = (torch.randn(11, 2, 64, device="cuda").bfloat16() for _ in range(2))
+    want, status = (k.clone(), v.clone()), new_status()
+    for b in range(3):
+        n0, n1, at = int(a["ptr"][b]), int(a["ptr"][b + 1]), int(a["lens"][b])
+        for i in range(n1 - n0 if n1 - n0 <= bound else 0):
+            page, slot = int(a["table"][b, (at + i) // 16]), (at + i) % 16
+            want[0][page, slot], want[1][page, slot] = kb[n0 + i], vb[n0 + i]
+    commit_draft(k, v, a["table"], a["lens"], kb, vb, a["ptr"], max_nodes=bound, status=status)
+    assert torch.equal(k, want[0]) and torch.equal(v, want[1])
+    if bound < 5:
+        with pytest.raises(splitkv.SplitKVError):
+            check_status(status)
+    check_status(status)
