@@ -1,10 +1,16 @@
-// Strided arrays as byte ranges (host): whether two of them share memory.  Not part of the public ABI.
+// Checks of a call's arrays on the host: alignment, and whether two strided ones share memory.  Not part of the public ABI.
 #pragma once
 
 #include <cstdint>
 #include <numeric>
 
 namespace splitkv {
+
+// Arrays of 32-bit words on their boundary (NULL passes).
+template <typename... Ps>
+inline bool all_aligned4(Ps... ps) {
+  return ((reinterpret_cast<uintptr_t>(ps) % 4 == 0) && ...);
+}
 
 // Rows of `row` contiguous bytes at every sum of strides (bytes, >= 0) from ptr on.
 struct Strided {

@@ -23,6 +23,7 @@
 #include <cuda_fp16.h>
 
 #include "common.cuh"
+#include "strided.h"
 #include "tree.h"
 
 namespace splitkv {
@@ -718,7 +719,7 @@ extern "C" int splitkv_tree_attn(const splitkv_tree_args* a, void* ws, size_t ws
   if (a->num_seqs == 0 || a->num_nodes == 0) return SPLITKV_OK;
   if (!rows_ok(a->q, a->q_stride[0], a->q_stride[1]) || !rows_ok(a->kb, a->kb_stride[0], a->kb_stride[1]) ||
       !rows_ok(a->vb, a->vb_stride[0], a->vb_stride[1]) || !splitkv::all_aligned16(a->o, ws) || !a->lse ||
-      !a->node_ptr || !a->context_lens || !splitkv::ptr_aligned(a->lse, 4))
+      !a->node_ptr || !a->context_lens || !splitkv::all_aligned4(a->lse, a->node_ptr, a->context_lens, a->status))
     return SPLITKV_ERR_INVALID_ARG;
   if (a->mask && a->mask_stride < 0) return SPLITKV_ERR_INVALID_ARG;
   // (the page table is read even where the cache has no page: every entry is then a bad one)

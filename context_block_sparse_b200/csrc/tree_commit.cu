@@ -125,6 +125,9 @@ extern "C" int splitkv_tree_commit(const splitkv_commit_args* a, void* stream) {
       !strides_ok(a->k_cache, a->k_stride, 4, es) || !strides_ok(a->v_cache, a->v_stride, 4, es))
     return SPLITKV_ERR_INVALID_ARG;
   if (!a->node_ptr || !a->page_table || !a->context_lens || (a->path && !a->count)) return SPLITKV_ERR_INVALID_ARG;
+  if (!splitkv::all_aligned4(a->node_ptr, a->page_table, a->context_lens, a->path, a->count, a->status) ||
+      a->table_stride < 0 || (a->path && a->path_stride < 0))
+    return SPLITKV_ERR_INVALID_ARG;
   // A row that is read while another CTA writes it would be either's: the new keys and values lie apart from both caches,
   // and the caches from each other.
   const int64_t row = int64_t(a->head_dim) * es, L = a->num_layers, H = a->num_kv_heads;

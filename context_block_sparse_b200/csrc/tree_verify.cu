@@ -40,6 +40,7 @@
 #include "common.cuh"
 #include "splitkv.h"
 #include "splitkv_internal.h"
+#include "strided.h"
 
 namespace cg = cooperative_groups;
 
@@ -519,6 +520,10 @@ extern "C" int splitkv_tree_verify(const splitkv_verify_args* a, void* stream) {
   if (!splitkv::ptr_aligned(a->target, es) || !splitkv::ptr_aligned(a->draft, es) || a->target_stride < 0 ||
       a->draft_stride < 0 || a->target_stride > (int64_t(1) << 40) || a->draft_stride > (int64_t(1) << 40) ||
       (a->num_seqs > 1 && a->path_stride < a->max_path) || a->path_stride > (int64_t(1) << 40))
+    return SPLITKV_ERR_INVALID_ARG;
+  const int ts = a->token_int64 ? 8 : 4;
+  if (!splitkv::all_aligned4(a->parents, a->node_ptr, a->u_accept, a->u_sample, a->path, a->count, a->status) ||
+      !splitkv::ptr_aligned(a->tokens, ts) || !splitkv::ptr_aligned(a->next, ts))
     return SPLITKV_ERR_INVALID_ARG;
   VerifyParams p;
   p.target = a->target;

@@ -140,3 +140,36 @@ def test_commit_of_tokens_past_the_index_range(splitkv, kw, code):
     a = _commit(splitkv._abi, kb=1 << 50, vb=1 << 51, k_cache=1 << 52, v_cache=1 << 53, kb_stride=z3, vb_stride=z3,
                 k_stride=z4, v_stride=z4, **kw)
     assert splitkv._lib.splitkv_tree_commit(ctypes.byref(a), None) == code
+
+
+def _verify(abi, **kw):
+    a = abi.VerifyArgs(2, 8, 4, 100, abi.DTYPE_F32, 0, 4, 0, *(i * M for i in range(1, 11)), None, 100, 100, 4)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+def _tree(abi, **kw):
+    a = abi.TreeArgs(2, 8, 4, 8, 2, 128, abi.DTYPE_BF16, abi.DTYPE_BF16, 16, 10, 5, 1.0, *(i * M for i in range(1, 6)),
+                     6 * M, 7 * M, 8 * M, 9 * M, 10 * M, 11 * M, None, (1024, 128), (256, 128), (256, 128),
+                     (4096, 256, 128), (4096, 256, 128), 4, 5)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("call,make,kw", [
+    *(("splitkv_tree_commit", _commit, kw) for kw in (
+        dict(node_ptr=4098), dict(context_lens=4097), dict(page_table=4098), dict(path=4098), dict(count=4098),
+        dict(status=4098), dict(table_stride=-5), dict(path_stride=-4))),
+    *(("splitkv_tree_verify", _verify, kw) for kw in (
+        dict(tokens=4098), dict(tokens=4100, token_int64=1), dict(parents=4098), dict(node_ptr=4097),
+        dict(u_accept=4098), dict(u_sample=4098), dict(path=4098), dict(count=4098), dict(next=4098),
+        dict(next=4100, token_int64=1), dict(status=4098))),
+    *(("splitkv_tree_attn", _tree, kw) for kw in (dict(node_ptr=4098), dict(context_lens=4097), dict(status=4098))),
+])
+def test_misaligned_words_and_negative_strides(splitkv, call, make, kw):
+    """A word off its boundary would fault the GPU, and a stride below zero leave the array."""
+    a = ctypes.byref(make(splitkv._abi, **kw))
+    args = (a, 64 * M, 1 << 40, None) if call == "splitkv_tree_attn" else (a, None)
+    assert getattr(splitkv._lib, call)(*args) == BAD
