@@ -92,11 +92,6 @@ bool make_f32_map_3d(void* map, void* base, uint64_t dim0, uint64_t dim1, uint64
 bool make_bf16_store_map_3d(void* map, void* base, uint64_t dim0, uint64_t dim1, uint64_t dim2, uint32_t box1,
                             uint32_t box2);
 
-// Paged cache [pages][slots][heads][d] of 16-bit elements with any strides (bytes, multiples of 16),
-// box {64, 1, box_slots, 1}, 128-byte swizzle, zero fill out of bounds.
-bool make_page_map_4d(void* map, const void* base, bool f16, uint64_t d, uint64_t heads, uint64_t slots, uint64_t pages,
-                      int64_t head_bytes, int64_t slot_bytes, int64_t page_bytes, uint32_t box_slots);
-
 // ---- kernel launchers (defined in the .cu files) ---------------------------
 // part_o / dq_part: float32 records, or bf16 when p.partial_bf16 (tcgen05 path only)
 cudaError_t launch_fwd_partial(const DevPlan& p, const uint16_t* q, const uint16_t* k,

@@ -30,6 +30,12 @@
 #include "splitkv_internal.h"
 
 namespace splitkv {
+
+// Paged cache [pages][slots][heads][d] of 16-bit elements with any strides (bytes, multiples of 16),
+// box {64, 1, box_slots, 1}, 128-byte swizzle, zero fill out of bounds.
+bool make_page_map_4d(void* map, const void* base, bool f16, uint64_t d, uint64_t heads, uint64_t slots, uint64_t pages,
+                      int64_t head_bytes, int64_t slot_bytes, int64_t page_bytes, uint32_t box_slots);   // (tensor_maps.cpp)
+
 namespace tree {
 
 constexpr int kMaxNodes = 256;     // nodes of a sequence
