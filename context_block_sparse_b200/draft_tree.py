@@ -1,6 +1,6 @@
 """Speculative decoding with draft trees over a paged cache: what a trained drafter is for.
 
-One step of B sequences, for a target of L layers (all tensors on one GPU; nothing here synchronises):
+One step of B sequences, for a target of L layers (all tensors on one GPU; nothing but check() synchronises):
 
     tree = SplitKVTreeAttention(num_q_heads, num_kv_heads, head_dim, max_nodes)
     # per layer: nodes packed by sequence, rows node_ptr[b] .. node_ptr[b + 1]
@@ -8,9 +8,15 @@ One step of B sequences, for a target of L layers (all tensors on one GPU; nothi
     o, lse = tree.forward(q, kb, vb, node_ptr, mask, k_cache, v_cache, page_table, context_lens, scale)
     # once, from the target's and the drafter's distributions
     path, count, next_token = verify_draft(target_probs, draft_probs, tokens, parents, node_ptr,
-                                           u_accept, u_sample, max_nodes=max_nodes)
-    commit_draft(k_caches, v_caches, page_table, context_lens, kbs, vbs, node_ptr, path, count)   # all layers
+                                           u_accept, u_sample, max_nodes=max_nodes, status=tree.status)
+    commit_draft(k_caches, v_caches, page_table, context_lens, kbs, vbs, node_ptr, path, count,
+                 status=tree.status)                                                              # all layers
     context_lens += count
+    tree.check()       # now and then: raises if any of these calls met a bad device array (synchronises)
+
+The kernels cannot raise: what they find wrong in device arrays (a page, a length, a node range, a parent, a token, a path
+row) they leave out, and say so in the status words that the call was given.  Without a status nothing says it, and rows
+that a commit left out would be counted as context: give all calls of a step the same words.
 
 Node 0 of a sequence is its last certain token (not yet in the cache), the others are drafted; parents hold
 each node's local parent (-1 for node 0), smaller than the node itself.  A drafter's own block of queries that
@@ -87,7 +93,8 @@ class SplitKVTreeAttention:
                                  self.max_nodes, out_dtype, o, lse, self.status)
 
     def check(self) -> None:
-        """Raise if a call recorded an error about its device arrays (a bad page, length or node range)."""
+        """Raise if a call that was given this object's status words recorded an error about its device arrays (a bad
+        page, length or node range; in verify_draft and commit_draft also a bad parent, token or path row)."""
         check_status(self.status)
 
 
@@ -99,6 +106,7 @@ def verify_draft(target_probs, draft_probs, tokens, parents, node_ptr, u_accept,
     children were drawn from (None: children proposed with certainty, such as a drafter's best candidates);
     float32, bfloat16 or float16.  tokens [nodes] (int32 or int64), parents int32 [nodes], node_ptr int32 [B + 1],
     u_accept float32 [nodes] and u_sample float32 [B] uniform in [0, 1).
+    status: words of new_status(), or a SplitKVTreeAttention's, in which bad nodes are recorded (they are never reached).
     Returns path int32 [B, max_path] (local nodes from node 0 on, -1 behind them; max_path defaults to max_nodes,
     and the walk ends there), count int32 [B], next_token [B] (as tokens; -1 where there is none)."""
     return splitkv_tree_verify(target_probs, draft_probs, tokens, parents, node_ptr, u_accept, u_sample, max_nodes,
@@ -111,7 +119,8 @@ def commit_draft(k_cache, v_cache, page_table, context_lens, kb, vb, node_ptr, p
 
     Caches [pages, page_size, heads, d] with kb, vb [nodes, heads, d], or all layers at once with one more leading
     dimension on the four.  path, count: as verify_draft returns them; without a path every node is appended in
-    order (max_nodes then bounds a sequence's nodes).  context_lens is not advanced: add count once all layers are
+    order (max_nodes then bounds a sequence's nodes).  status: words of new_status(), or a SplitKVTreeAttention's, in
+    which rows that had to be left out are recorded.  context_lens is not advanced: add count once all layers are
     written.  Sequences must not share the pages they write, and kb, vb must lie apart from the caches (nodes that are in
     the cache already are copied out first)."""
     if path is None:

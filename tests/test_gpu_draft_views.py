@@ -97,3 +97,31 @@ def test_commit_without_a_path_under_any_bound(splitkv, bound):
         with pytest.raises(splitkv.SplitKVError):
             check_status(status)
     check_status(status)
+
+
+def test_a_step_reports_what_it_left_out(splitkv):
+    """tree.check() after the documented calls raises for a bad token, path row or page of any of them."""
+    from context_block_sparse_b200.draft_tree import SplitKVTreeAttention, commit_draft, verify_draft
+    a = _accepted()
+    tree = SplitKVTreeAttention(4, 2, 64, 5)
+    k, v = (torch.randn(12, 16, 2, 64, device="cuda").bfloat16() for _ in range(2))
+    q, kb, vb = (torch.randn(11, h, 64, device="cuda").bfloat16() for h in (4, 2, 2))
+    probs = torch.softmax(torch.randn(11, 30, device="cuda"), -1)
+    parents = torch.tensor([-1, 0, 1, 2, -1, 0, 1, 2, 3, -1, 0], dtype=torch.int32, device="cuda")
+    tokens, u = torch.zeros(11, dtype=torch.int32, device="cuda"), torch.rand(11, device="cuda")
+
+    def step(tokens=tokens, path=a["path"], table=a["table"]):
+        tree.forward(q, kb, vb, a["ptr"], None, k, v, table, a["lens"], 0.125)
+        verify_draft(probs, None, tokens, parents, a["ptr"], u, u[:3], max_nodes=5, status=tree.status)
+        commit_draft(k, v, a["table"], a["lens"], kb, vb, a["ptr"], path, a["count"], status=tree.status)
+
+    step()
+    tree.check()
+    bad_token, bad_path, bad_table = tokens.clone(), a["path"].clone(), a["table"].clone()
+    bad_token[3], bad_path[1, 1], bad_table[0, 0] = 30, 5, 12
+    for kw in (dict(tokens=bad_token), dict(path=bad_path), dict(table=bad_table)):
+        step(**kw)
+        with pytest.raises(splitkv.SplitKVError):
+            tree.check()
+        step()
+        tree.check()
