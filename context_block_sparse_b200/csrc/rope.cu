@@ -256,7 +256,7 @@ extern "C" int splitkv_rope_freqs(int32_t rotary_dim, double base, int scaling, 
     }
     freqs[i] = w;
   }
-  if (scaling == SPLITKV_ROPE_SCALE_PARTS && factor > 1) *scale = 0.1 * std::log(factor) + 1.0;
+  if (scaling == SPLITKV_ROPE_SCALE_PARTS) *scale = 0.1 * std::log(factor) + 1.0;
   return SPLITKV_OK;
 }
 
