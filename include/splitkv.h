@@ -564,7 +564,7 @@ int splitkv_rope_freqs(int32_t rotary_dim, double base, int scaling, double fact
 
 /* Rotary positions on queries and keys in one launch: every pair (a, b) of the first rotary_dim
  * elements of a head becomes scale (a cos t - b sin t, b cos t + a sin t), t = position * w_i (formed
- * and reduced in float64); float32 arithmetic, one rounding.  SPLITKV_ROPE_ADJOINT is the backward
+ * and reduced in float64: good to 1e-7 rad plus t 2^-51); float32 arithmetic, one rounding.  SPLITKV_ROPE_ADJOINT is the backward
  * pass.  Errors: INVALID_ARG, UNSUPPORTED (grid beyond the device's limits), CUDA. */
 int splitkv_rope(const splitkv_rope_args* args, void* stream);
 
