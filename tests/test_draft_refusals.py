@@ -173,3 +173,17 @@ def test_misaligned_words_and_negative_strides(splitkv, call, make, kw):
     a = ctypes.byref(make(splitkv._abi, **kw))
     args = (a, 64 * M, 1 << 40, None) if call == "splitkv_tree_attn" else (a, None)
     assert getattr(splitkv._lib, call)(*args) == BAD
+
+
+@pytest.mark.parametrize("call,make,kw", [
+    *(("splitkv_tree_attn", _tree, kw) for kw in (dict(num_seqs=0), dict(num_nodes=0), dict(num_nodes=0, q=None, o=None))),
+    *(("splitkv_tree_verify", _verify, kw) for kw in (dict(num_seqs=0), dict(num_seqs=0, num_nodes=0, target=None))),
+    *(("splitkv_tree_commit", _commit, kw) for kw in (dict(num_seqs=0), dict(num_layers=0), dict(num_nodes=0, kb=None),
+                                                     dict(max_rows=0))),
+    *(("splitkv_rope", _rope, kw) for kw in (dict(num_tokens=0), dict(q_heads=0, k_heads=0, q=None, k=None))),
+])
+def test_calls_without_work_succeed(splitkv, call, make, kw):
+    """Before anything else is asked for: no workspace, no arrays."""
+    a = ctypes.byref(make(splitkv._abi, **kw))
+    args = (a, None, 0, None) if call == "splitkv_tree_attn" else (a, None)
+    assert getattr(splitkv._lib, call)(*args) == 0

@@ -53,3 +53,75 @@ def test_weights_far_below_the_largest(splitkv, monkeypatch, kernel, nodes, d, a
     got = _forward(c, scale)
     assert_within("o", got[0], o, to + vs * 2.0 ** -37, torch.float16)
     assert_within("lse", got[1], lse, tl, torch.float32)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kernel,nodes", FORMS)
+@pytest.mark.parametrize("scale", [0.0, -0.0, -0.3, 1e-40])
+def test_scale_of_any_sign(splitkv, monkeypatch, kernel, nodes, d, scale):
+    """Masked scores are minus infinity under any scale: behind the context's end, in the tree, on pages of NaN."""
+    monkeypatch.setenv("SPLITKV_TREE_KERNEL", kernel)
+    for dt in ("bf16", "fp16"):
+        c = Case([nodes, 3], [140, 0], 4, 1, d, 16, dt, seed=9)
+        c.check(_forward(c, scale), ref=_ref(c, scale))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kernel,nodes", FORMS)
+def test_rows_behind_the_last_sequence(splitkv, monkeypatch, kernel, nodes, d):
+    from context_block_sparse_b200.draft_tree import SplitKVTreeAttention
+    monkeypatch.setenv("SPLITKV_TREE_KERNEL", kernel)
+    c = Case([nodes, 2], [300, 20], 4, 1, d, 16, extra=40, seed=2)
+    tree = SplitKVTreeAttention(4, 1, d, c.max_nodes)
+    o, lse = torch.full(c.q.shape, 7.0, dtype=c.q.dtype, device="cuda"), torch.full(c.q.shape[:2], 7.0, device="cuda")
+    tree.forward(*(x.cuda() for x in (c.q, c.kb, c.vb, c.ptr, c.mask, c.k, c.v, c.table, c.lens)), d ** -0.5, o=o, lse=lse)
+    assert (o[nodes + 2:] == 7).all() and (lse[nodes + 2:] == 7).all()
+    c.check((o, lse))
+
+
+@pytest.mark.parametrize("page", [1, 2, 4])
+@pytest.mark.parametrize("nodes", [1, 9, 30, 90])
+def test_pages_below_eight_tokens(splitkv, nodes, page):
+    c = Case([nodes, max(1, nodes // 2)], [300, 77], 8, 2, 128, page, seed=nodes)
+    c.check(c.call())
+
+
+PAGES = 18000     # of 128 tokens of 1024 elements: 2.36e9 elements, 4.7 GB, for the keys and for the values
+
+
+@pytest.fixture(scope="module")
+def far_cache():
+    k = torch.empty(PAGES, 128, 1024, dtype=torch.bfloat16, device="cuda")
+    return k, torch.empty_like(k)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kernel,nodes", FORMS)
+def test_cache_past_32_bits(splitkv, monkeypatch, far_cache, kernel, nodes, d):
+    monkeypatch.setenv("SPLITKV_TREE_KERNEL", kernel)
+    hkv = 1024 // d
+    c = Case([nodes], [300], 4 * hkv, hkv, d, 128, seed=12)
+    k, v = (x.view(PAGES, 128, hkv, d) for x in far_cache)
+    table = torch.tensor([[PAGES - 1, 3, PAGES - 2]], dtype=torch.int32)
+    for i in range(3):
+        k[table[0, i]], v[table[0, i]] = c.k[c.table[0, i]].cuda(), c.v[c.table[0, i]].cuda()
+    c.check(_forward(c, d ** -0.5, page_table=table, k_cache=k, v_cache=v))
+
+
+def test_commit_into_a_cache_past_32_bits(splitkv, far_cache):
+    from context_block_sparse_b200.draft_tree import commit_draft
+    k, v = (x.view(PAGES, 128, 8, 128) for x in far_cache)
+    g = torch.Generator().manual_seed(1)
+    kb, vb = (torch.randn(5, 8, 128, generator=g).bfloat16().cuda() for _ in range(2))
+    far, near = PAGES - 1, 2
+    k[far], v[far], k[near], v[near] = 0, 0, 0, 0
+    # the page where the low 32 bits of the far page's byte offset would land (17999 * 2^18 = 2^32 + 1615 * 2^18; its offset
+    # in elements, 17999 * 2^17, is past 2^31 and below 2^32)
+    alias = far * 2 ** 18 % 2 ** 32 // 2 ** 18
+    assert alias == 1615
+    k[alias], v[alias] = 0, 0
+    i = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    commit_draft(k, v, i(near, far)[None], i(126), kb, vb, i(0, 5), i(0, 1, 3, 4)[None], i(4))
+    assert torch.equal(k[near, 126:], kb[:2]) and torch.equal(v[near, 126:], vb[:2])
+    assert torch.equal(k[far, :2], kb[3:]) and torch.equal(v[far, :2], vb[3:])
+    assert (k[far, 2:] == 0).all() and (k[near, :126] == 0).all() and (v[alias] == 0).all() and (k[alias] == 0).all()
