@@ -6,8 +6,8 @@
 
 Objects go to _build/ at the repository root; the shared library lands next
 to this file so the Python binding finds it, and beside it the torch extension
-_draft_ext.so (the bindings of the rotary and draft-tree calls).  Only splitkv_* symbols are
-exported.  Nothing here needs a GPU: nvcc cross-compiles.
+_draft_ext.so (the bindings of the rotary and draft-tree calls; left out, with a note, where there is no
+torch).  Only splitkv_* symbols are exported.  Nothing here needs a GPU: nvcc cross-compiles.
 """
 
 from __future__ import annotations
@@ -75,14 +75,32 @@ def build(verbose: bool = False, force: bool = False, ptxas_info: bool = False) 
     return LIB
 
 
-def build_ext(verbose: bool = False, force: bool = False) -> str:
-    """The torch extension _draft_ext.so beside libsplitkv.so, which it links against."""
-    newest = max(os.path.getmtime(EXT_SRC), os.path.getmtime(os.path.join(INCLUDE, "splitkv.h")))
-    if not force and os.path.exists(EXT) and os.path.getmtime(EXT) >= newest:
-        return EXT
+def _torch_version():
+    """The installed torch's version, or None (read without importing it)."""
+    from importlib import metadata
+    try:
+        return metadata.version("torch")
+    except metadata.PackageNotFoundError:
+        return None
+
+
+def build_ext(verbose: bool = False, force: bool = False):
+    """The torch extension _draft_ext.so beside libsplitkv.so, which it links against: built again when its source, the
+    header, this file, torch or the interpreter changed.  Without torch there is nothing to bind to: None, and a note."""
+    newest = max(os.path.getmtime(f) for f in (EXT_SRC, os.path.join(INCLUDE, "splitkv.h"), os.path.abspath(__file__)))
+    stamp = os.path.join(BUILD, "draft_ext.for")       # what the extension that is there was built for
+    made_for = f"torch {_torch_version()}, python {sys.version}"
+    if not force and os.path.exists(EXT) and os.path.getmtime(EXT) >= newest and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == made_for:
+                return EXT
     import sysconfig
-    import torch
-    from torch.utils import cpp_extension
+    try:
+        import torch
+        from torch.utils import cpp_extension
+    except ImportError as e:
+        print(f"_draft_ext.so (the rotary and draft-tree calls from torch) is not built: {e}", file=sys.stderr)
+        return None
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
     cmd = [os.environ.get("CXX") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE,
@@ -94,6 +112,8 @@ def build_ext(verbose: bool = False, force: bool = False) -> str:
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.run(cmd, check=True)
+    with open(stamp, "w") as f:
+        f.write(made_for)
     return EXT
 
 
