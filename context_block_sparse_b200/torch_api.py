@@ -35,7 +35,9 @@ class SplitKVAttention:
         contiguous_schedule: the contiguous baseline schedule instead of LPT.
         rotary: a Rotary applied to q, k and kb inside forward and backward (which take and differentiate the
         unrotated ones): a context token's position is its offset in its sample, row r of block b's is its
-        anchor's offset + r (the context positions the block's tokens stand for)."""
+        anchor's offset + r (the context positions the block's tokens stand for).  After splitkv_plan_update the next call
+        of forward or backward brings the new positions, in place where their numbers stay (that call must not be
+        captured)."""
         self.device = torch.device("cuda") if device is None else torch.device(device)
         if num_workers is None:
             num_workers = torch.cuda.get_device_properties(self.device).multi_processor_count
@@ -55,18 +57,23 @@ class SplitKVAttention:
         if rotary is not None:
             if rotary.head_dim != head_dim:
                 raise ValueError(f"rotary is for heads of {rotary.head_dim}, not {head_dim}")
+            self._ctx_pos = self._row_pos = None
             self._place()
         self._grad32 = None   # float32 gradients behind bf16 ones (grad_dtype=torch.bfloat16)
 
     def _place(self):
-        """The plan's positions on the device."""
+        """The plan's positions on the device: in the same tensors as long as their sizes stay."""
         p = self.plan.problem
         lens, anc = (np.asarray(x, dtype=np.int64) for x in self.plan._keep)
         starts = np.concatenate([[0], np.cumsum(lens)])
         ctx = np.arange(starts[-1]) - np.repeat(starts[:-1], lens)
         rows = (anc - starts[np.searchsorted(starts, anc, side="right") - 1])[:, None] + np.arange(p.block_size)
-        self._ctx_pos, self._row_pos = (torch.from_numpy(x.astype(np.int32).ravel()).to(self.device)
-                                        for x in (ctx, rows))
+        new = [torch.from_numpy(x.astype(np.int32).ravel()) for x in (ctx, rows)]
+        if self._ctx_pos is not None and [x.shape for x in new] == [self._ctx_pos.shape, self._row_pos.shape]:
+            self._ctx_pos.copy_(new[0])       # (a captured graph holds these)
+            self._row_pos.copy_(new[1])
+        else:
+            self._ctx_pos, self._row_pos = (x.to(self.device) for x in new)
         self._placed = p
 
     def ws_bwd(self) -> torch.Tensor:
