@@ -702,6 +702,34 @@ bool rows_ok(const void* ptr, int64_t s0, int64_t s1, int64_t s2 = 0) {
          s2 < kMax && s0 % 8 == 0 && s1 % 8 == 0 && s2 % 8 == 0;
 }
 
+// o, lse and the workspace share no memory with each other and with what the call reads, but o may be q itself (a
+// unit's rows are read before they are written, and by that unit alone).
+bool outputs_apart(const splitkv_tree_args* a, const void* ws, size_t ws_bytes) {
+  using splitkv::Strided;
+  const int64_t nq = a->num_nodes, hq = a->num_q_heads, hkv = a->num_kv_heads, row = 2 * a->head_dim;
+  const int64_t es = a->o_dtype == SPLITKV_DTYPE_F32 ? 4 : 2;
+  const auto nodes = [&](const void* ptr, const int64_t* s, int64_t heads) {
+    return Strided{ptr, row, 2, {nq, heads}, {s[0] * 2, s[1] * 2}};
+  };
+  const auto cache = [&](const void* ptr, const int64_t* s) {
+    return Strided{ptr, row, 3, {a->num_pages, a->page_size, hkv}, {s[0] * 2, s[1] * 2, s[2] * 2}};
+  };
+  const Strided out[3] = {{a->o, nq * hq * a->head_dim * es, 0, {}, {}}, {a->lse, nq * hq * 4, 0, {}, {}},
+                          {ws, int64_t(ws_bytes), 0, {}, {}}};
+  const Strided in[5] = {nodes(a->q, a->q_stride, hq), nodes(a->kb, a->kb_stride, hkv), nodes(a->vb, a->vb_stride, hkv),
+                         cache(a->k_cache, a->k_stride), cache(a->v_cache, a->v_stride)};
+  const int n_in = a->max_pages > 0 && a->num_pages > 0 ? 5 : 3;
+  const bool in_place = a->o == a->q && es == 2 && (hq == 1 || a->q_stride[1] == a->head_dim) &&
+                        (nq == 1 || a->q_stride[0] == hq * a->head_dim);
+  for (int i = 0; i < 3; ++i) {
+    for (int j = 0; j < i; ++j)
+      if (!splitkv::apart(out[i], out[j])) return false;
+    for (int j = i == 0 && in_place ? 1 : 0; j < n_in; ++j)
+      if (!splitkv::apart(out[i], in[j])) return false;
+  }
+  return true;
+}
+
 }  // namespace
 
 extern "C" int splitkv_tree_workspace_size(const splitkv_tree_args* args, size_t* bytes) {
@@ -730,6 +758,7 @@ extern "C" int splitkv_tree_attn(const splitkv_tree_args* a, void* ws, size_t ws
        !rows_ok(a->v_cache, a->v_stride[0], a->v_stride[1], a->v_stride[2])))
     return SPLITKV_ERR_INVALID_ARG;
   if (ws_bytes < z.total) return SPLITKV_ERR_WORKSPACE_TOO_SMALL;
+  if (!outputs_apart(a, ws, z.total)) return SPLITKV_ERR_INVALID_ARG;
   TreeParams p;
   p.q = static_cast<const char*>(a->q);
   p.kb = static_cast<const char*>(a->kb);

@@ -619,7 +619,9 @@ int splitkv_tree_workspace_size(const splitkv_tree_args* args, size_t* bytes);
  * A row that sees no key gets o = 0, lse = -inf; values that a row does not see never reach it,
  * infinities and NaN among them.  float32 throughout, but the weights exp(s_j - m) are rounded to the
  * keys' type for the product with v (l is the sum of the unrounded ones): float16 holds a weight to
- * 2^-11 of itself, or to 2^-37 of the row's largest where that is more.  Two launches; the workspace is written and read inside the call
+ * 2^-11 of itself, or to 2^-37 of the row's largest where that is more.  o, lse and the
+ * workspace lie apart from each other and from the arrays that the call reads, but o may be q itself (one
+ * type, contiguous).  Two launches; the workspace is written and read inside the call
  * and may be used again by the next call on the stream, not by a concurrent one.  Deterministic.
  * Errors: INVALID_ARG, UNSUPPORTED, WORKSPACE_TOO_SMALL, CUDA. */
 int splitkv_tree_attn(const splitkv_tree_args* args, void* ws, size_t ws_bytes, void* stream);

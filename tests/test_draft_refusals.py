@@ -187,3 +187,15 @@ def test_calls_without_work_succeed(splitkv, call, make, kw):
     a = ctypes.byref(make(splitkv._abi, **kw))
     args = (a, None, 0, None) if call == "splitkv_tree_attn" else (a, None)
     assert getattr(splitkv._lib, call)(*args) == 0
+
+
+@pytest.mark.parametrize("kw", [
+    dict(o=2 * M), dict(o=3 * M), dict(o=4 * M), dict(o=5 * M + 4096), dict(o=2 * M - 16),    # over kb, vb, the caches
+    dict(o=M + 256), dict(o=M, o_dtype=0),                            # over q otherwise than in place
+    dict(o=M, q_stride=(ctypes.c_int64 * 2)(2048, 128)),
+    dict(lse=M), dict(lse=4 * M), dict(lse=10 * M + 64), dict(o=64 * M), dict(lse=64 * M), dict(q=64 * M), dict(k_cache=64 * M),
+])
+def test_tree_attention_outputs_over_its_inputs(splitkv, kw):
+    """Other CTAs still read what an output or the workspace overwrites (o in the place of q itself is taken)."""
+    a = ctypes.byref(_tree(splitkv._abi, **kw))
+    assert splitkv._lib.splitkv_tree_attn(a, 64 * M, 1 << 40, None) == BAD

@@ -125,3 +125,25 @@ def test_commit_into_a_cache_past_32_bits(splitkv, far_cache):
     assert torch.equal(k[near, 126:], kb[:2]) and torch.equal(v[near, 126:], vb[:2])
     assert torch.equal(k[far, :2], kb[3:]) and torch.equal(v[far, :2], vb[3:])
     assert (k[far, 2:] == 0).all() and (k[near, :126] == 0).all() and (v[alias] == 0).all() and (k[alias] == 0).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kernel,nodes", FORMS)
+@pytest.mark.parametrize("lens", [[300, 20, 0, 1500], [40] * 4])
+def test_in_the_place_of_the_queries(splitkv, monkeypatch, kernel, nodes, d, lens):
+    """o = q: the same bits as into memory of its own; over anything else it is refused."""
+    from context_block_sparse_b200.draft_tree import SplitKVTreeAttention
+    monkeypatch.setenv("SPLITKV_TREE_KERNEL", kernel)
+    c = Case([nodes, 1, nodes, max(1, nodes // 2)] * 8, lens * 8, 8, 2, d, 16, seed=nodes)
+    tree = SplitKVTreeAttention(8, 2, d, c.max_nodes)
+    a = [x.cuda() for x in (c.q, c.kb, c.vb, c.ptr, c.mask, c.k, c.v, c.table, c.lens)]
+    o, lse = tree.forward(*a, d ** -0.5)
+    at = a[0].clone()
+    got = tree.forward(at, *a[1:], d ** -0.5, o=at)
+    assert got[0] is at and torch.equal(at, o) and torch.equal(got[1], lse)
+    room = torch.zeros(2 * at.numel(), dtype=at.dtype, device="cuda")
+    inner = room[8:8 + at.numel()].view(at.shape)
+    with pytest.raises(splitkv.SplitKVError):
+        tree.forward(inner, *a[1:], d ** -0.5, o=room[:at.numel()].view(at.shape))
+    with pytest.raises(splitkv.SplitKVError):
+        tree.forward(at, *a[1:], d ** -0.5, o=room[:at.numel()].view(at.shape), lse=room.view(torch.float32)[:lse.numel()].view(lse.shape))
