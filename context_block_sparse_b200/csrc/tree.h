@@ -48,7 +48,7 @@ constexpr int kMaxNodes = 256;     // nodes of a sequence
 constexpr int lift_of(bool f16, bool tcgen05) { return f16 ? (tcgen05 ? 12 : 15) : 0; }
 constexpr int headroom_of(bool f16) { return f16 ? 3 : 8; }
 // On tcgen05: row tiles that are rows as M (tree_rows_sm100.cu); the others are rows as N (tree_context_sm100.cu).  N / M
-// measured: 256 rows, d = 128, 4 x 64 nodes over 64k to 128k 427 / 335 us; 128 rows (32 nodes of G = 4, 8 KV heads): d = 64,
+// measured: 256 rows, d = 128, 4 x 64 nodes over 68k to 79k 427 / 335 us (now 327); 128 rows (32 nodes of G = 4, 8 KV heads): d = 64,
 // 128 sequences over 4k 404 / 302, 32 over 1k 52 / 49, one over 2k 20.7 / 20.6; d = 128, 128 over 4k 467 / 434, but 32 over
 // 1k 62 / 72, one over 64k 70 / 79; 64 rows, d = 64, 64 over 4k 124 / 154.
 constexpr bool rows_as_m(int Mt, int d) { return Mt == 256 || (Mt == 128 && d == 64); }

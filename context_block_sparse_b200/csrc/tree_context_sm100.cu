@@ -25,9 +25,10 @@
 // shared memory before the product (P = 0 does not hide a NaN).
 //
 // Measured (8 KV heads): d = 128, 32 sequences over 8k keys, 32 rows 172 us and 64 rows 186 (165 at the copy rate), 128
-// rows 225; 16 ragged trees of 64 rows over 1k-8k 62 (47); d = 64, 64 sequences over 4k, 32 rows 99 (83).  A long unit runs
-// at HBM's rate up to 64 rows; what is lost is a tile's chain of product, softmax and product at 128 rows, and at
-// every unit's ends its first references, its row sums and stores, 3000 to 5000 clocks.
+// rows 223 (255 in a loop, where the GPU runs at its power limit); 16 ragged trees of 64 rows over 1k-8k 62 (47); d = 64,
+// 64 sequences over 4k, 32 rows 99 (83).  A long unit runs at HBM's rate up to 64 rows; what is lost is a tile's chain of
+// product, softmax and product at 128 rows, and at every unit's ends its first references, its row sums and stores,
+// 3000 to 5000 clocks.
 #include <cstdint>
 
 #include <cuda_bf16.h>

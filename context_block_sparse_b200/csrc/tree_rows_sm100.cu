@@ -14,8 +14,8 @@
 // A pair of row tiles costs the tensor core 2048 clocks a key tile at d = 128 (32 instructions of 64 clocks), the
 // exponentials 2048 clocks of the MUFU units (128 x 256 at 16 a clock), HBM 2735 at 1965 MHz: while one group of four
 // warps forms its tile's probabilities, the other tile's products run.  Long calls are bound by power: 4 x 64 nodes over
-// 101k to 124k keys take 505 us, 57 % of the measured bf16 and HBM rates each, at 1 kW and 1590 MHz.  Scores in halves
-// of 64 keys, whose products overlap the other half's softmax, saved 20 % of the clocks and took 525 us: the
+// 101k to 124k keys take 495 to 525 us, 55 to 58 % of the measured bf16 and HBM rates each, at 1 kW and 1590 MHz.  Scores in halves
+// of 64 keys, whose products overlap the other half's softmax, saved 20 % of the clocks and took 525 us beside 505: the
 // clock fell by more (N = 64 products read more of shared memory for the same work).
 //
 // As in the training kernels P = exp2(s - reference), where the reference is the row's first maximum (less kLift) and

@@ -28,8 +28,9 @@
 // Each warp keeps the sums of its chunks of 512 entries: the search for the next token
 // re-reads one chunk (from L2).
 //
-// Measured: one chain of 16 nodes over 32000 entries 8.6 us; 64 chains over 131072 24 us, 10 of
-// them HBM's; 24 trees of 40 nodes over 50001 (rows that do not begin on 16 bytes) 25 us.  The rest is the
+// Measured (whole calls): one chain of 16 nodes over 32000 entries 8 to 10 us; 64 chains over 131072 25 us, 10 of
+// them HBM's (39 us with certainty drafts); 24 trees of 40 nodes over
+// 50001 (rows that do not begin on 16 bytes) 30 to 36 us.  The rest is the
 // walk's serial steps: the gathers, one pass over the rows a rejection or an end, cluster barriers.
 #include <cooperative_groups.h>
 #include <cstdint>

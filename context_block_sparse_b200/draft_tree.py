@@ -66,7 +66,12 @@ def tree_mask(parents, node_ptr, max_nodes: int) -> np.ndarray:
 
 
 class SplitKVTreeAttention:
-    """Attention of draft-tree nodes over their sequences' paged context and their own trees."""
+    """Attention of draft-tree nodes over their sequences' paged context and their own trees.
+
+    The lengths stay on the device, so the kernel and its row tiles are chosen by bounds that the host knows: max_nodes and
+    the width of the page table.  Keep both tight.  A step of one node a sequence takes 12 us over 1k keys through an object
+    for 1 to 4 nodes and 21 us through one for 64 (64 sequences: 74 and 106 us); an object holds two words, so make one for
+    each kind of step, and pass page_table[:, :w] where w pages are enough for every sequence of the call."""
 
     def __init__(self, num_q_heads: int, num_kv_heads: int, head_dim: int, max_nodes: int, device=None):
         if num_kv_heads < 1 or num_q_heads % num_kv_heads:

@@ -2,7 +2,7 @@
 // outputs and workspaces from torch's allocator, the current stream, one call.  No computation.
 //
 // These calls serve single tokens, where the host's time counts: reading the tensors here costs a
-// few microseconds less a call than through ctypes (tree attention of one token: 24 us a call, 15 us
+// few microseconds less a call than through ctypes (tree attention of one token: 24 us a call, 12 to 13.5 us
 // from here).
 #include <initializer_list>
 #include <optional>
